@@ -49,6 +49,7 @@ extern "C" {
 
 #define MUON_ABI_VERSION 1
 #define MUON_MAX_SHARDS 128
+#define MUON_MAX_EXPERTS 1024
 
 typedef enum muon_status {
   MUON_OK = 0,
@@ -58,8 +59,9 @@ typedef enum muon_status {
   MUON_ERR_TIMEOUT = 4,       /* a device-side wait ran out of its budget              */
   MUON_ERR_OOM = 5,           /* host or device table allocation failed                */
   MUON_ERR_UNSUPPORTED = 6,   /* no sm_103a device, or a size beyond the library limits */
-  MUON_ERR_DEVICE_CHECK = 7   /* debug builds: a device-side range check of a table     */
+  MUON_ERR_DEVICE_CHECK = 7,  /* debug builds: a device-side range check of a table     */
                               /* entry failed; the work it drove was skipped            */
+  MUON_ERR_ROW_OFFSETS = 8    /* row offsets on the device are not ascending in 0..rows */
 } muon_status;
 
 typedef enum muon_ns_dtype {
@@ -150,6 +152,14 @@ muon_status muon_step_grouped(float* const* flat_params, const float* const* fla
                               float* const* flat_momentum, const muon_layout* layout,
                               void* workspace, const muon_group_hparams* groups, int32_t ns_steps,
                               cudaStream_t stream);
+
+/* muon_step_grouped with every gradient first multiplied by *grad_scale, one float on the
+ * device: with muon_grad_norm's coefficient (its norm + 1) the step clips by the global norm
+ * without a pass of its own over the gradients.  flat_grads is only read. */
+muon_status muon_step_scaled(float* const* flat_params, const float* const* flat_grads,
+                             float* const* flat_momentum, const muon_layout* layout,
+                             void* workspace, const muon_group_hparams* groups, int32_t ns_steps,
+                             const float* grad_scale, cudaStream_t stream);
 
 /* The three stages of muon_step, callable one by one (same arguments, same meaning).
  * [P2] _compute_momentum_inputs: momentum update, input build, gather, Frobenius norms. */
@@ -281,10 +291,103 @@ muon_status muon_orthogonalize_full_noalloc(const muon_layout* layout, const flo
                                             float* full_out, int32_t ns_steps,
                                             cudaStream_t stream);
 
+/* ---------------------------------------------------------------- expert layers
+ * What a mixture-of-experts layer computes before the step: the experts' products forward
+ * and backward over rows sorted by expert, the gated activation between them, and the global
+ * gradient norm with clipping.  The pages have no counterpart: they start at the gradients.
+ *
+ * Rows.  Expert e owns rows row_offsets[e] .. row_offsets[e + 1] - 1 of the row-major inputs
+ * (row_offsets: DEVICE array of n_experts + 1 ascending int64 within 0..rows; experts may own
+ * no row).  The host never reads them, so a router's output is used without a copy.  If they
+ * are not ascending within 0..rows, no expert owns a row and a following muon_check reports
+ * MUON_ERR_ROW_OFFSETS.
+ * Sizes.  1 <= n_experts <= MUON_MAX_EXPERTS, 0 <= rows < 2^31, 1 <= k, n, m < 2^31.  ld* are
+ * row pitches in elements (at least the row length); *_stride is the distance in elements
+ * between two experts' matrices, so they may lie in a flat buffer among others.
+ * Pointers need their element's alignment only.  Outputs must not overlap inputs.
+ * Arithmetic.  Products of the 16-bit inputs are summed in fp32 and rounded once, at the
+ * store. */
+typedef enum muon_dtype {
+  MUON_DTYPE_F32 = 0,
+  MUON_DTYPE_BF16 = 1,
+  MUON_DTYPE_F16 = 2
+} muon_dtype;
+
+/* muon_grouped_mm: y[r, :] = x[r, :] W_e for every row r of every expert e, with W_e stored
+ * k x n, or (trans_w != 0) y[r, :] = x[r, :] W_e^T with W_e stored n x k.  The gradient with
+ * respect to x is the same call on dy with the other trans_w.  x: rows x k, y: rows x n; rows
+ * of no expert are set to zero.  dtype: MUON_DTYPE_BF16 or _F16 of x and w; out_dtype: the
+ * same type or MUON_DTYPE_F32.
+ * workspace: muon_grouped_mm_workspace_bytes bytes (0 for operands whose rows all start on
+ * 16 bytes: 16-byte aligned pointers, and pitches and w_stride that are multiples of 8;
+ * others are copied there first), 1024-byte aligned; NULL is accepted for 0 bytes. */
+muon_status muon_grouped_mm(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                            int64_t w_stride, const int64_t* row_offsets, void* y, int64_t ldy,
+                            int64_t rows, int32_t n_experts, int32_t k, int32_t n,
+                            int32_t trans_w, int32_t dtype, int32_t out_dtype, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+muon_status muon_grouped_mm_workspace_bytes(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                            int64_t w_stride, int64_t rows, int32_t n_experts,
+                                            int32_t k, int32_t n, int32_t trans_w, size_t* bytes);
+
+/* muon_grouped_wgrad: dw_e = sum over the rows r of expert e of a[r, :]^T b[r, :], an m x n
+ * matrix in fp32, or (accumulate != 0) dw_e += that sum.  a: rows x m, b: rows x n, both of
+ * type dtype (MUON_DTYPE_BF16 or _F16).  With x and dy this is the gradient of a k x n weight,
+ * with dy and x that of an n x k one; dw may point into the flat gradient buffer of an
+ * unsharded layout.  An expert without rows gets zeros (accumulate: is left as it is).
+ * workspace as for muon_grouped_mm. */
+muon_status muon_grouped_wgrad(const void* a, int64_t lda, const void* b, int64_t ldb,
+                               const int64_t* row_offsets, float* dw, int64_t lddw,
+                               int64_t dw_stride, int64_t rows, int32_t n_experts, int32_t m,
+                               int32_t n, int32_t accumulate, int32_t dtype, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+muon_status muon_grouped_wgrad_workspace_bytes(const void* a, int64_t lda, const void* b,
+                                               int64_t ldb, int64_t rows, int32_t m, int32_t n,
+                                               size_t* bytes);
+
+/* muon_swiglu: out[r, c] = p_r * g * u / (1 + exp(-g)) with g = gate[r, c], u = up[r, c] and
+ * p_r = row_weight[r] (DEVICE, fp32; NULL: 1).  All tensors rows x cols of type dtype (any
+ * muon_dtype) with their own row pitches, so gate and up may be halves of one tensor. */
+muon_status muon_swiglu(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                        const float* row_weight, void* out, int64_t ld_out, int64_t rows,
+                        int32_t cols, int32_t dtype, cudaStream_t stream);
+/* Its gradient: from dout, writes dgate, dup and, unless NULL, d_row_weight[r] = sum over c of
+ * dout * silu(g) * u (fp32). */
+muon_status muon_swiglu_grad(const void* dout, int64_t ld_dout, const void* gate, int64_t ld_gate,
+                             const void* up, int64_t ld_up, const float* row_weight, void* dgate,
+                             int64_t ld_dgate, void* dup, int64_t ld_dup, float* d_row_weight,
+                             int64_t rows, int32_t cols, int32_t dtype, cudaStream_t stream);
+
+/* One tensor of a list: numel consecutive elements on the device. */
+typedef struct muon_tensor {
+  void* data;
+  int64_t numel;   /* >= 0; data may be NULL when 0 */
+  int32_t dtype;   /* a muon_dtype */
+  int32_t pad_;
+} muon_tensor;
+
+/* muon_grad_norm: the 2-norm of all elements of all n tensors (HOST array, read during the
+ * call) and the clipping coefficient: norm[0] = sqrt(sum g^2), norm[1] = min(1, max_norm /
+ * (norm[0] + 1e-6)); norm: DEVICE, 2 floats.  Squares are summed in fp32 per thread over at
+ * most 32 elements and in fp64 from there, covering the whole fp32 range; the order is
+ * fixed, so equal inputs give equal bits.  A NaN or infinite gradient shows as a NaN or
+ * infinite norm (coefficient NaN or 0).
+ * muon_clip_grads: the same, and outs[i] = norm[1] * grads[i].  outs[i] has grads[i]'s length
+ * and either its type or MUON_DTYPE_F32; it may be grads[i] itself (then a coefficient of 1
+ * moves nothing) but must not overlap any tensor otherwise.
+ * max_norm: finite, >= 0.  workspace: muon_clip_workspace_bytes bytes, 8-byte aligned. */
+muon_status muon_grad_norm(const muon_tensor* grads, int32_t n, float max_norm, float* norm,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+muon_status muon_clip_grads(const muon_tensor* grads, const muon_tensor* outs, int32_t n,
+                            float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+muon_status muon_clip_workspace_bytes(const muon_tensor* grads, int32_t n, size_t* bytes);
+
 /* ---------------------------------------------------------------- status
  * Synchronises `stream`, then reports a device-side wait timeout recorded since the last
  * check (MUON_ERR_TIMEOUT, and clears it), a failed range check of a debug build
- * (MUON_ERR_DEVICE_CHECK, and clears it) or a CUDA error (MUON_ERR_CUDA). */
+ * (MUON_ERR_DEVICE_CHECK, and clears it), row offsets that a grouped product refused
+ * (MUON_ERR_ROW_OFFSETS, and clears it) or a CUDA error (MUON_ERR_CUDA). */
 muon_status muon_check(cudaStream_t stream);
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* muon_last_error(void);

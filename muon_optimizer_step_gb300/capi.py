@@ -23,15 +23,21 @@ MUON_ERR_TIMEOUT = 4
 MUON_ERR_OOM = 5
 MUON_ERR_UNSUPPORTED = 6
 MUON_ERR_DEVICE_CHECK = 7
+MUON_ERR_ROW_OFFSETS = 8
 MUON_NS_BF16 = 0
 MUON_NS_FP32 = 1
 MUON_NS_SPLIT_FP32 = 2
+MUON_DTYPE_F32 = 0
+MUON_DTYPE_BF16 = 1
+MUON_DTYPE_F16 = 2
 MUON_MAX_SHARDS = 128
+MUON_MAX_EXPERTS = 1024
 WORKSPACE_ALIGN = 1024
 
 _STATUS_NAMES = {0: "MUON_OK", 1: "MUON_ERR_INVALID_ARG", 2: "MUON_ERR_ALIGNMENT",
                  3: "MUON_ERR_CUDA", 4: "MUON_ERR_TIMEOUT", 5: "MUON_ERR_OOM",
-                 6: "MUON_ERR_UNSUPPORTED", 7: "MUON_ERR_DEVICE_CHECK"}
+                 6: "MUON_ERR_UNSUPPORTED", 7: "MUON_ERR_DEVICE_CHECK",
+                 8: "MUON_ERR_ROW_OFFSETS"}
 
 # (name, restype, argtypes) of every entry point declared in include/muon.h.
 _P = ctypes.c_void_p
@@ -45,6 +51,15 @@ class GroupHparams(ctypes.Structure):
     """muon_group_hparams: one optimizer group's hyper-parameters."""
     _fields_ = [("lr", ctypes.c_float), ("wd", ctypes.c_float), ("mu", ctypes.c_float),
                 ("nesterov", ctypes.c_int32)]
+
+
+class Tensor(ctypes.Structure):
+    """muon_tensor: numel consecutive elements on the device."""
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
+_SZ = ctypes.c_size_t
 
 SIGNATURES = [
     ("muon_abi_version", _I32, []),
@@ -81,6 +96,22 @@ SIGNATURES = [
     ("muon_layout_ns_kernel", _I32, [_P, ctypes.POINTER(_I32), ctypes.POINTER(_I32),
                                      ctypes.POINTER(_I32)]),
     ("muon_layout_fused_apply", _I32, [_P, ctypes.POINTER(_I32)]),
+    ("muon_step_scaled", _I32, [_PP, _PP, _PP, _P, _P, ctypes.POINTER(GroupHparams), _I32, _P,
+                                _P]),
+    ("muon_grouped_mm", _I32, [_P, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I32, _I32, _I32,
+                               _I32, _I32, _I32, _P, _SZ, _P]),
+    ("muon_grouped_mm_workspace_bytes", _I32, [_P, _I64, _P, _I64, _I64, _I64, _I32, _I32, _I32,
+                                               _I32, ctypes.POINTER(_SZ)]),
+    ("muon_grouped_wgrad", _I32, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32,
+                                  _I32, _I32, _P, _SZ, _P]),
+    ("muon_grouped_wgrad_workspace_bytes", _I32, [_P, _I64, _P, _I64, _I64, _I32, _I32,
+                                                  ctypes.POINTER(_SZ)]),
+    ("muon_swiglu", _I32, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I32, _I32, _P]),
+    ("muon_swiglu_grad", _I32, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64,
+                                _I32, _I32, _P]),
+    ("muon_grad_norm", _I32, [_P, _I32, _F, _P, _P, _SZ, _P]),
+    ("muon_clip_grads", _I32, [_P, _P, _I32, _F, _P, _P, _SZ, _P]),
+    ("muon_clip_workspace_bytes", _I32, [_P, _I32, ctypes.POINTER(_SZ)]),
 ]
 
 
@@ -247,6 +278,26 @@ def muon_step_grouped(flat_params, flat_grads, flat_momentum, layout, workspace,
                                  _stream_handle(stream)), "muon_step_grouped")
 
 
+def muon_step_scaled(flat_params, flat_grads, flat_momentum, layout, workspace, groups,
+                     grad_scale, ns_steps=5, stream=None):
+    """muon_step_grouped with the gradients multiplied by grad_scale, a CUDA tensor of one
+    float32 (norm[1:] of muon_grad_norm: the step then clips by the global norm)."""
+    if not isinstance(grad_scale, int):
+        _device_tensor(grad_scale, "grad_scale", ("float32",))
+        if grad_scale.numel() < 1:
+            raise ValueError("grad_scale is empty")
+    arr = (GroupHparams * max(1, len(groups)))(
+        *[GroupHparams(float(lr), float(wd), float(mu), 1 if nest else 0)
+          for lr, wd, mu, nest in groups])
+    if len(groups) < getattr(layout, "n_groups", 1):
+        raise ValueError(f"groups: expected {getattr(layout, 'n_groups', 1)}, got {len(groups)}")
+    _check(lib.muon_step_scaled(_shard_array(layout, flat_params, "flat_params"),
+                                _shard_array(layout, flat_grads, "flat_grads"),
+                                _shard_array(layout, flat_momentum, "flat_momentum"),
+                                layout.handle, _ptr(workspace), arr, int(ns_steps),
+                                _ptr(grad_scale), _stream_handle(stream)), "muon_step_scaled")
+
+
 def muon_compute_momentum_inputs(flat_grads, flat_momentum, layout, workspace, mu,
                                  nesterov=True, stream=None):
     _check(lib.muon_compute_momentum_inputs(
@@ -346,6 +397,213 @@ def muon_export_input(layout, workspace, full_out, stream=None):
 def muon_export_update(layout, workspace, ns_steps, full_out, stream=None):
     _check(lib.muon_export_update(layout.handle, _ptr(workspace), int(ns_steps), _ptr(full_out),
                                   _stream_handle(stream)), "muon_export_update")
+
+
+# ------------------------------------------------------------------ expert layers
+_DTYPES = {}
+
+
+def _dtype_code(t, name, kinds=("float32", "bfloat16", "float16")):
+    """The muon_dtype of tensor t, one of `kinds`."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: (MUON_DTYPE_F32, "float32"),
+                        torch.bfloat16: (MUON_DTYPE_BF16, "bfloat16"),
+                        torch.float16: (MUON_DTYPE_F16, "float16")})
+    code = _DTYPES.get(t.dtype)
+    if code is None or code[1] not in kinds:
+        raise ValueError(f"{name}: type {t.dtype}; one of {', '.join(kinds)} is needed")
+    return code[0]
+
+
+def _device_tensor(t, name, kinds, shape=None):
+    """Checks t's place, shape and unit inner stride; returns its muon_dtype."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dim() > 0 and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _dtype_code(t, name, kinds)
+
+
+def _pitch(t):
+    """Row pitch of a 2-D tensor (strides of dimensions of length 1 mean nothing)."""
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.shape[-1], 1)
+
+
+def _step_of(t):
+    """Distance between the matrices of a 3-D tensor."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1] * t.shape[2], 1)
+
+
+def _offsets(t, n_experts):
+    import torch
+    if not t.is_cuda or t.dtype != torch.int64 or t.dim() != 1 or not t.is_contiguous() \
+            or t.shape[0] != n_experts + 1:
+        raise ValueError(f"offsets: must be {n_experts + 1} contiguous int64 values on the GPU")
+
+
+_16BIT = ("bfloat16", "float16")
+
+
+def _workspace(workspace, nbytes, like, stream):
+    """The caller's workspace, or one from torch's allocator, kept from reuse until the work
+    enqueued on `stream` is done with it."""
+    if workspace is not None or nbytes == 0:
+        return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    import torch
+    raw = torch.empty(nbytes + WORKSPACE_ALIGN, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        raw.record_stream(stream if not isinstance(stream, int)
+                          else torch.cuda.ExternalStream(stream, device=like.device))
+    return raw[(-raw.data_ptr()) % WORKSPACE_ALIGN:][:nbytes], nbytes
+
+
+def muon_grouped_mm(x, w, offsets, y, trans_w=False, workspace=None, stream=None):
+    """y[r] = x[r] @ w[e] (or @ w[e].T with trans_w) for the rows offsets[e]..offsets[e+1]-1 of
+    every expert e; rows of no expert get zeros.
+
+    x (rows, k) and w (experts, k, n) (trans_w: (experts, n, k)) are bfloat16 or float16, y
+    (rows, n) is of their type or float32, offsets holds experts + 1 int64 values on the GPU.
+    Any strides with a contiguous last dimension; operands whose rows do not start on 16 bytes
+    are copied to the workspace first (allocated when None is given)."""
+    e, k, n = w.shape
+    if trans_w:
+        k, n = n, k
+    rows = x.shape[0]
+    dtype = _device_tensor(x, "x", _16BIT, (rows, k))
+    if _device_tensor(w, "w", _16BIT) != dtype:
+        raise ValueError("x and w must have the same type")
+    out = _device_tensor(y, "y", ("float32",) + _16BIT, (rows, n))
+    if out not in (dtype, MUON_DTYPE_F32):
+        raise ValueError("y must have x's type or be float32")
+    _offsets(offsets, e)
+    xp, wp, ldx, ldw, ws = x.data_ptr(), w.data_ptr(), _pitch(x), _pitch(w), _step_of(w)
+    nbytes = 0
+    if (xp | wp) & 15 or (ldx | ldw | ws) & 7:
+        need = _SZ()
+        _check(lib.muon_grouped_mm_workspace_bytes(xp, ldx, wp, ldw, ws, rows, e, k, n,
+                                                   1 if trans_w else 0, ctypes.byref(need)),
+               "muon_grouped_mm_workspace_bytes")
+        nbytes = need.value
+    workspace, nbytes = _workspace(workspace, nbytes, x, stream)
+    _check(lib.muon_grouped_mm(xp, ldx, wp, ldw, ws, offsets.data_ptr(), y.data_ptr(), _pitch(y),
+                               rows, e, k, n, 1 if trans_w else 0, dtype, out, _ptr(workspace),
+                               nbytes, _stream_handle(stream)), "muon_grouped_mm")
+
+
+def muon_grouped_wgrad(a, b, offsets, dw, accumulate=False, workspace=None, stream=None):
+    """dw[e] = a[rows of e].T @ b[rows of e] in float32 for every expert e, or with accumulate
+    dw[e] += that.  a (rows, m) and b (rows, n) are bfloat16 or float16; dw (experts, m, n) is
+    float32 with any strides of its first two dimensions, e.g. a view of the flat gradient
+    buffer."""
+    e, m, n = dw.shape
+    rows = a.shape[0]
+    dtype = _device_tensor(a, "a", _16BIT, (rows, m))
+    if _device_tensor(b, "b", _16BIT, (rows, n)) != dtype:
+        raise ValueError("a and b must have the same type")
+    _device_tensor(dw, "dw", ("float32",))
+    _offsets(offsets, e)
+    ap, bp, lda, ldb = a.data_ptr(), b.data_ptr(), _pitch(a), _pitch(b)
+    nbytes = 0
+    if (ap | bp) & 15 or (lda | ldb) & 7:
+        need = _SZ()
+        _check(lib.muon_grouped_wgrad_workspace_bytes(ap, lda, bp, ldb, rows, m, n,
+                                                      ctypes.byref(need)),
+               "muon_grouped_wgrad_workspace_bytes")
+        nbytes = need.value
+    workspace, nbytes = _workspace(workspace, nbytes, a, stream)
+    _check(lib.muon_grouped_wgrad(ap, lda, bp, ldb, offsets.data_ptr(), dw.data_ptr(), _pitch(dw),
+                                  _step_of(dw), rows, e, m, n, 1 if accumulate else 0, dtype,
+                                  _ptr(workspace), nbytes, _stream_handle(stream)),
+           "muon_grouped_wgrad")
+
+
+_ANY = ("float32",) + _16BIT
+
+
+def _row_weight(t, rows, name):
+    if t is None:
+        return None
+    _device_tensor(t, name, ("float32",), (rows,))
+    return t.data_ptr()
+
+
+def muon_swiglu(gate, up, out, row_weight=None, stream=None):
+    """out = row_weight[:, None] * silu(gate) * up, row by row; all (rows, cols) of one type."""
+    dtype = _device_tensor(gate, "gate", _ANY)
+    for t, name in ((up, "up"), (out, "out")):
+        if _device_tensor(t, name, _ANY, gate.shape) != dtype:
+            raise ValueError(f"{name} must have gate's type")
+    rows, cols = gate.shape
+    _check(lib.muon_swiglu(gate.data_ptr(), _pitch(gate), up.data_ptr(), _pitch(up),
+                           _row_weight(row_weight, rows, "row_weight"), out.data_ptr(),
+                           _pitch(out), rows, cols, dtype, _stream_handle(stream)), "muon_swiglu")
+
+
+def muon_swiglu_grad(dout, gate, up, dgate, dup, row_weight=None, d_row_weight=None, stream=None):
+    """The gradient of muon_swiglu: writes dgate, dup and, where given, d_row_weight."""
+    dtype = _device_tensor(gate, "gate", _ANY)
+    for t, name in ((dout, "dout"), (up, "up"), (dgate, "dgate"), (dup, "dup")):
+        if _device_tensor(t, name, _ANY, gate.shape) != dtype:
+            raise ValueError(f"{name} must have gate's type")
+    rows, cols = gate.shape
+    _check(lib.muon_swiglu_grad(dout.data_ptr(), _pitch(dout), gate.data_ptr(), _pitch(gate),
+                                up.data_ptr(), _pitch(up),
+                                _row_weight(row_weight, rows, "row_weight"), dgate.data_ptr(),
+                                _pitch(dgate), dup.data_ptr(), _pitch(dup),
+                                _row_weight(d_row_weight, rows, "d_row_weight"), rows, cols, dtype,
+                                _stream_handle(stream)), "muon_swiglu_grad")
+
+
+# ------------------------------------------------------------------ gradient norm, clipping
+def _tensor_list(tensors, name):
+    """A host array of muon_tensor from contiguous CUDA tensors."""
+    arr = (Tensor * max(1, len(tensors)))()
+    for r, t in zip(arr, tensors):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous CUDA tensors")
+        r.data, r.numel, r.dtype = t.data_ptr(), t.numel(), _dtype_code(t, name)
+    return arr
+
+
+def _norm_call(grads, norm, workspace, stream):
+    _device_tensor(norm, "norm", ("float32",), (2,))
+    g = _tensor_list(grads, "grads")
+    need = _SZ()
+    _check(lib.muon_clip_workspace_bytes(g, len(grads), ctypes.byref(need)),
+           "muon_clip_workspace_bytes")
+    workspace, nbytes = _workspace(workspace, need.value, norm, stream)
+    return g, workspace, nbytes
+
+
+def muon_grad_norm(grads, max_norm, norm, workspace=None, stream=None):
+    """norm[0] = the 2-norm of all gradients together, norm[1] = min(1, max_norm / (norm[0] +
+    1e-6)).  grads: a sequence of contiguous CUDA tensors; norm: 2 float32 on the GPU."""
+    g, workspace, nbytes = _norm_call(grads, norm, workspace, stream)
+    _check(lib.muon_grad_norm(g, len(grads), float(max_norm), norm.data_ptr(), _ptr(workspace),
+                              nbytes, _stream_handle(stream)), "muon_grad_norm")
+
+
+def muon_clip_grads(grads, outs, max_norm, norm, workspace=None, stream=None):
+    """muon_grad_norm, and outs[i] = norm[1] * grads[i].  outs[i] is grads[i] itself or a tensor
+    of its length and of its type or float32."""
+    if len(outs) != len(grads):
+        raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
+    g, workspace, nbytes = _norm_call(grads, norm, workspace, stream)
+    _check(lib.muon_clip_grads(g, _tensor_list(outs, "outs"), len(grads), float(max_norm),
+                               norm.data_ptr(), _ptr(workspace), nbytes, _stream_handle(stream)),
+           "muon_clip_grads")
+
+
+def layout_grads(layout, flat_grads):
+    """The shards of a flat buffer without the padding behind the last one: what
+    muon_grad_norm sums over for the global norm of a layout's gradients."""
+    if not isinstance(flat_grads, (list, tuple)):
+        flat_grads = [flat_grads]
+    return [g[:max(0, min(layout.shard_len, layout.numel - s * layout.shard_len))]
+            for s, g in enumerate(flat_grads)]
 
 
 def muon_check(stream=None):

@@ -27,7 +27,7 @@ BUILD_DIR_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_PATH_DEBUG = os.path.join(PKG, "libmuon_debug.so")
 
 SOURCES = ["layout.cpp", "capi.cu", "stream_kernels.cu", "gemm_f32.cu", "gemm_ns.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "expert_capi.cu", "grouped_mm.cu", "swiglu.cu", "grad_norm.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

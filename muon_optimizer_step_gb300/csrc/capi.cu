@@ -342,8 +342,8 @@ GroupParams uniform_groups(float lr, float wd, float mu, int nesterov) {
 }
 
 muon_status run_momentum(muon_layout* L, const ShardPtrs& g, const ShardPtrs& m, void* ws,
-                         const GroupParams& gp, cudaStream_t st) {
-  MUON_CUDA(launch_momentum_input(L->plan, L->dt, g, m, ws, gp, st), "momentum_input");
+                         const GroupParams& gp, cudaStream_t st, const float* grad_scale = nullptr) {
+  MUON_CUDA(launch_momentum_input(L->plan, L->dt, g, m, ws, gp, grad_scale, st), "momentum_input");
   MUON_CUDA(launch_norm_finalize(L->plan, L->dt, ws, st), "norm_finalize");
   return MUON_OK;
 }
@@ -398,6 +398,10 @@ muon_status check_scalars(float lr, float wd, float mu) {
 }  // namespace
 
 void muon::set_last_error(const std::string& msg) { g_last_error = msg; }
+
+cudaError_t muon::device_error_word(int dev, int** out) {
+  return err_word(dev, out) == MUON_OK ? cudaSuccess : cudaErrorMemoryAllocation;
+}
 
 extern "C" {
 
@@ -627,10 +631,11 @@ muon_status muon_exchange_plan(const muon_layout* layout, const int32_t* owner, 
   return ok();
 }
 
-muon_status muon_step_grouped(float* const* flat_params, const float* const* flat_grads,
-                              float* const* flat_momentum, const muon_layout* layout,
-                              void* workspace, const muon_group_hparams* groups, int32_t ns_steps,
-                              cudaStream_t stream) {
+// muon_step_grouped, with the gradients first multiplied by *grad_scale where it is given.
+static muon_status step_grouped(float* const* flat_params, const float* const* flat_grads,
+                                float* const* flat_momentum, const muon_layout* layout,
+                                void* workspace, const muon_group_hparams* groups,
+                                int32_t ns_steps, const float* grad_scale, cudaStream_t stream) {
   if (layout == nullptr) return fail(MUON_ERR_INVALID_ARG, "layout is NULL");
   muon_layout* L = const_cast<muon_layout*>(layout);
   if (groups == nullptr) return fail(MUON_ERR_INVALID_ARG, "groups is NULL");
@@ -651,9 +656,28 @@ muon_status muon_step_grouped(float* const* flat_params, const float* const* fla
   std::lock_guard<std::mutex> guard(L->mu);
   MUON_TRY(ensure_device(L));
   MUON_TRY(ensure_tmaps(L, workspace));
-  MUON_TRY(run_momentum(L, g, m, workspace, gp, stream));
+  MUON_TRY(run_momentum(L, g, m, workspace, gp, stream, grad_scale));
   MUON_TRY(run_ns_apply(L, w, workspace, gp, ns_steps, stream));
   return ok();
+}
+
+muon_status muon_step_grouped(float* const* flat_params, const float* const* flat_grads,
+                              float* const* flat_momentum, const muon_layout* layout,
+                              void* workspace, const muon_group_hparams* groups, int32_t ns_steps,
+                              cudaStream_t stream) {
+  return step_grouped(flat_params, flat_grads, flat_momentum, layout, workspace, groups, ns_steps,
+                      nullptr, stream);
+}
+
+muon_status muon_step_scaled(float* const* flat_params, const float* const* flat_grads,
+                             float* const* flat_momentum, const muon_layout* layout,
+                             void* workspace, const muon_group_hparams* groups, int32_t ns_steps,
+                             const float* grad_scale, cudaStream_t stream) {
+  if (grad_scale == nullptr) return fail(MUON_ERR_INVALID_ARG, "grad_scale is NULL");
+  if (reinterpret_cast<uintptr_t>(grad_scale) % sizeof(float) != 0)
+    return fail(MUON_ERR_ALIGNMENT, "grad_scale = %p is not 4-byte aligned", (const void*)grad_scale);
+  return step_grouped(flat_params, flat_grads, flat_momentum, layout, workspace, groups, ns_steps,
+                      grad_scale, stream);
 }
 
 muon_status muon_gather_full(const muon_layout* layout, const float* const* shards, float* full,
@@ -758,6 +782,9 @@ muon_status muon_check(cudaStream_t stream) {
     if (h == MUON_ERR_DEVICE_CHECK)
       return fail(MUON_ERR_DEVICE_CHECK, "a device-side range check of a table entry failed "
                   "(debug build); the work it drove was skipped");
+    if (h == MUON_ERR_ROW_OFFSETS)
+      return fail(MUON_ERR_ROW_OFFSETS, "row offsets of a grouped product were not ascending "
+                  "within 0..rows; no expert got a row");
     return fail(MUON_ERR_CUDA, "device error word %d", h);
   }
   e = cudaGetLastError();

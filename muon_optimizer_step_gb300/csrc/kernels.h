@@ -54,9 +54,10 @@ struct DevTables {
 DebugCtx make_debug_ctx(const Plan& plan, const DevTables& dt);
 
 // Stage 1: momentum, orthogonalization input into X0, per-chunk sums of squares.
+// grad_scale (may be null): device factor of every gradient.
 cudaError_t launch_momentum_input(const Plan& plan, const DevTables& dt, const ShardPtrs& g,
                                   const ShardPtrs& m, void* ws, const GroupParams& gp,
-                                  cudaStream_t st);
+                                  const float* grad_scale, cudaStream_t st);
 // Full fp32 matrices -> X0 plus per-chunk sums of squares.
 cudaError_t launch_full_input(const Plan& plan, const DevTables& dt, const float* full, void* ws,
                               cudaStream_t st);
@@ -91,6 +92,56 @@ bool encode_tensor_maps(const Plan& plan, const void* ws, std::vector<CUtensorMa
                         std::string* err);
 // One-block kernel that waits on an mbarrier nobody arrives on, with `budget` cycles.
 cudaError_t launch_selftest_timeout(int* err, long long budget, cudaStream_t st);
+// ---- expert layer (expert_capi.cu)
+constexpr int kF32 = 0, kBf16 = 1, kF16 = 2;  // muon_dtype values
+constexpr int kMaxExperts = 1024;             // MUON_MAX_EXPERTS
+
+struct GroupedMm {            // y = x W_e per expert (see muon_grouped_mm)
+  const void* x;
+  const void* w;
+  void* y;
+  const int64_t* offsets;
+  int64_t ldx, ldw, w_stride, ldy, rows;
+  int32_t n_experts, k, n, trans, dtype, out_dtype;
+  int* err;
+};
+cudaError_t launch_grouped_mm(const GroupedMm& p, cudaStream_t st);
+
+struct GroupedWgrad {         // dw_e (+)= a^T b per expert (see muon_grouped_wgrad)
+  const void* a;
+  const void* b;
+  float* dw;
+  const int64_t* offsets;
+  int64_t lda, ldb, lddw, dw_stride, rows;
+  int32_t n_experts, m, n, accumulate, dtype;
+  int* err;
+};
+cudaError_t launch_grouped_wgrad(const GroupedWgrad& p, cudaStream_t st);
+
+// n = 3: g, u, a (forward); n = 5: da, g, u, dg, du (gradient).
+struct SwigluArgs {
+  int n;
+  void* ptr[5];
+  int64_t ld[5];
+};
+cudaError_t launch_swiglu(const SwigluArgs& s, int dtype, const float* p, float* dp, int64_t rows,
+                          int32_t cols, int sms, cudaStream_t st);
+
+struct TensorSpec {           // same layout as muon_tensor
+  void* data;
+  int64_t numel;
+  int32_t dtype;
+  int32_t pad_;
+};
+// outs may be null (norm and coefficient only).
+cudaError_t launch_clip(const TensorSpec* grads, const TensorSpec* outs, int n, float max_norm,
+                        float* norm, void* ws, int sms, cudaStream_t st);
+size_t clip_workspace_bytes(const TensorSpec* grads, int n, int sms);
+// Work units of a list; at most 2^31 - 1 fit a launch.
+int64_t clip_chunks(const TensorSpec* grads, int n);
+
+// The word of device `dev` where kernels record errors (allocated and zeroed on first use).
+cudaError_t device_error_word(int dev, int** out);
 // Sets the message muon_last_error() returns on this thread.
 void set_last_error(const std::string& msg);
 // The allocation-free entry point's error word on device `dev` (inside its scratch

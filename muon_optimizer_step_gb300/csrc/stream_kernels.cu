@@ -146,14 +146,23 @@ __device__ __forceinline__ int64_t x_index(const MatDev& mt, int64_t local) {
   return r * mt.ldx + (local - r * mt.cols);
 }
 
-template <typename XT>
+template <bool kScaled>
+__device__ __forceinline__ float4 scaled4(float4 v, float s) {
+  return kScaled ? make_float4(v.x * s, v.y * s, v.z * s, v.w * s) : v;
+}
+
+// kScaled: every gradient is first multiplied by *grad_scale (the clipping coefficient), so
+// that clipping costs no pass of its own over the gradients.
+template <typename XT, bool kScaled>
 __global__ void __launch_bounds__(kThreads)
 momentum_input_kernel(const ChunkDev* __restrict__ chunks, int64_t n_chunks,
                       const MatDev* __restrict__ mats, ShardPtrs G, ShardPtrs M, int64_t L,
                       uint8_t* __restrict__ ws, float* __restrict__ partials,
-                      const __grid_constant__ GroupParams gp, const DebugCtx dbg) {
+                      const __grid_constant__ GroupParams gp,
+                      const float* __restrict__ grad_scale, const DebugCtx dbg) {
   __shared__ float red[32];
   if (debug_halted(dbg)) return;
+  const float gs = kScaled ? *grad_scale : 1.f;
   for (int64_t ci = blockIdx.x; ci < n_chunks; ci += gridDim.x) {
     const ChunkDev ch = chunks[ci];
     if (kDebugChecks && (!debug_chunk_ok(ch, mats, dbg, &G) || !debug_chunk_ok(ch, mats, dbg, &M)))
@@ -175,7 +184,7 @@ momentum_input_kernel(const ChunkDev* __restrict__ chunks, int64_t n_chunks,
         float4 gv[4], mv[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          gv[u] = __ldcs(g4 + v + u * kThreads);
+          gv[u] = scaled4<kScaled>(__ldcs(g4 + v + u * kThreads), gs);
           mv[u] = __ldcs(m4 + v + u * kThreads);
         }
 #pragma unroll
@@ -199,7 +208,7 @@ momentum_input_kernel(const ChunkDev* __restrict__ chunks, int64_t n_chunks,
         }
       }
       for (; v < nv; v += kThreads) {
-        const float4 gv = __ldcs(g4 + v);
+        const float4 gv = scaled4<kScaled>(__ldcs(g4 + v), gs);
         const float4 mv = __ldcs(m4 + v);
         float4 mn, xn;
         mn.x = fmaf(mu, mv.x, gv.x);
@@ -219,8 +228,9 @@ momentum_input_kernel(const ChunkDev* __restrict__ chunks, int64_t n_chunks,
         ss = add_sq4(ss, xn.x, xn.y, xn.z, xn.w);
       }
       for (int t = nv * 4 + threadIdx.x; t < ch.len; t += kThreads) {
-        const float mn = fmaf(mu, m[t], g[t]);
-        const float xn = nesterov ? fmaf(mu, mn, g[t]) : mn;
+        const float gt = kScaled ? g[t] * gs : g[t];
+        const float mn = fmaf(mu, m[t], gt);
+        const float xn = nesterov ? fmaf(mu, mn, gt) : mn;
         m[t] = mn;
         store1(xv + t, xn);
         ss = add_sq1(ss, xn);
@@ -232,7 +242,7 @@ momentum_input_kernel(const ChunkDev* __restrict__ chunks, int64_t n_chunks,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int t = 4 * v + e;
-          const float gt = *elem_ptr(G, ch, L, t);
+          const float gt = kScaled ? *elem_ptr(G, ch, L, t) * gs : *elem_ptr(G, ch, L, t);
           float* mp = elem_ptr(M, ch, L, t);
           const float mn = fmaf(mu, *mp, gt);
           const float xn = nesterov ? fmaf(mu, mn, gt) : mn;
@@ -243,7 +253,7 @@ momentum_input_kernel(const ChunkDev* __restrict__ chunks, int64_t n_chunks,
         ss = add_sq4(ss, xs[0], xs[1], xs[2], xs[3]);
       }
       for (int t = nv * 4 + threadIdx.x; t < ch.len; t += kThreads) {
-        const float gt = *elem_ptr(G, ch, L, t);
+        const float gt = kScaled ? *elem_ptr(G, ch, L, t) * gs : *elem_ptr(G, ch, L, t);
         float* mp = elem_ptr(M, ch, L, t);
         const float mn = fmaf(mu, *mp, gt);
         const float xn = nesterov ? fmaf(mu, mn, gt) : mn;
@@ -448,23 +458,33 @@ DebugCtx make_debug_ctx(const Plan& plan, const DevTables& dt) {
   return d;
 }
 
+template <typename XT>
+static void momentum_as(const Plan& plan, const DevTables& dt, const ShardPtrs& g,
+                        const ShardPtrs& m, uint8_t* w, const GroupParams& gp,
+                        const float* grad_scale, int grid, cudaStream_t st) {
+  const DebugCtx dbg = make_debug_ctx(plan, dt);
+  float* partials = reinterpret_cast<float*>(w + plan.ws_partials);
+  const int64_t n = (int64_t)plan.chunks.size();
+  if (grad_scale != nullptr)
+    momentum_input_kernel<XT, true><<<grid, kThreads, 0, st>>>(
+        dt.chunks, n, dt.mats, g, m, plan.L, w, partials, gp, grad_scale, dbg);
+  else
+    momentum_input_kernel<XT, false><<<grid, kThreads, 0, st>>>(
+        dt.chunks, n, dt.mats, g, m, plan.L, w, partials, gp, nullptr, dbg);
+}
+
 cudaError_t launch_momentum_input(const Plan& plan, const DevTables& dt, const ShardPtrs& g,
                                   const ShardPtrs& m, void* ws, const GroupParams& gp,
-                                  cudaStream_t st) {
+                                  const float* grad_scale, cudaStream_t st) {
   const int grid = grid_for(plan, dt);
   if (grid == 0) return cudaSuccess;
-  const DebugCtx dbg = make_debug_ctx(plan, dt);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  float* partials = reinterpret_cast<float*>(w + plan.ws_partials);
   if (plan.ns_dtype == 0)
-    momentum_input_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(
-        dt.chunks, (int64_t)plan.chunks.size(), dt.mats, g, m, plan.L, w, partials, gp, dbg);
+    momentum_as<__nv_bfloat16>(plan, dt, g, m, w, gp, grad_scale, grid, st);
   else if (plan.ns_dtype == 1)
-    momentum_input_kernel<float><<<grid, kThreads, 0, st>>>(
-        dt.chunks, (int64_t)plan.chunks.size(), dt.mats, g, m, plan.L, w, partials, gp, dbg);
+    momentum_as<float>(plan, dt, g, m, w, gp, grad_scale, grid, st);
   else
-    momentum_input_kernel<Bf16x3><<<grid, kThreads, 0, st>>>(
-        dt.chunks, (int64_t)plan.chunks.size(), dt.mats, g, m, plan.L, w, partials, gp, dbg);
+    momentum_as<Bf16x3>(plan, dt, g, m, w, gp, grad_scale, grid, st);
   return cudaGetLastError();
 }
 
