@@ -88,12 +88,12 @@ muon_status check_pitch(int64_t ld, int64_t len, const char* name) {
   return MUON_OK;
 }
 
-muon_status check_groups(const int64_t* row_offsets, int64_t rows, int32_t n_experts) {
+muon_status check_groups(int64_t rows, int32_t n_experts) {
   if (n_experts < 1 || n_experts > MUON_MAX_EXPERTS)
     return fail(MUON_ERR_INVALID_ARG, "n_experts=%d outside 1..%d", n_experts, MUON_MAX_EXPERTS);
   if (rows < 0 || rows > INT32_MAX)
     return fail(MUON_ERR_INVALID_ARG, "rows=%lld outside 0..2^31-1", (long long)rows);
-  return check_ptr(row_offsets, sizeof(int64_t), "row_offsets");
+  return MUON_OK;
 }
 
 muon_status check_16bit(int32_t dtype, const char* name) {
@@ -113,6 +113,41 @@ muon_status check_dtype(int32_t dtype, const char* name) {
   if (dtype < MUON_DTYPE_F32 || dtype > MUON_DTYPE_F16)
     return fail(MUON_ERR_INVALID_ARG, "%s=%d is no muon_dtype", name, dtype);
   return MUON_OK;
+}
+
+// What muon_grouped_mm and its workspace query both check.
+muon_status check_mm(const GroupedMm& g) {
+  EXPERT_TRY(check_dim(g.k, "k"));
+  EXPERT_TRY(check_dim(g.n, "n"));
+  EXPERT_TRY(check_pitch(g.ldx, g.k, "ldx"));
+  EXPERT_TRY(check_pitch(g.ldw, g.trans ? g.k : g.n, "ldw"));
+  EXPERT_TRY(check_pitch(g.ldy, g.n, "ldy"));
+  if (g.n_experts > 1) EXPERT_TRY(check_pitch(g.w_stride, 1, "w_stride"));
+  if (g.rows > 0) {
+    EXPERT_TRY(check_ptr(g.x, 2, "x"));
+    EXPERT_TRY(check_ptr(g.w, 2, "w"));
+  }
+  return MUON_OK;
+}
+
+muon_status check_wgrad(const GroupedWgrad& g) {
+  EXPERT_TRY(check_dim(g.m, "m"));
+  EXPERT_TRY(check_dim(g.n, "n"));
+  EXPERT_TRY(check_pitch(g.lda, g.m, "lda"));
+  EXPERT_TRY(check_pitch(g.ldb, g.n, "ldb"));
+  EXPERT_TRY(check_pitch(g.lddw, g.n, "lddw"));
+  if (g.n_experts > 1) EXPERT_TRY(check_pitch(g.dw_stride, g.n, "dw_stride"));
+  if (g.rows > 0) {
+    EXPERT_TRY(check_ptr(g.a, 2, "a"));
+    EXPERT_TRY(check_ptr(g.b, 2, "b"));
+  }
+  return MUON_OK;
+}
+
+muon_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (bytes < need)
+    return fail(MUON_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", bytes, need);
+  return need > 0 ? check_ptr(workspace, (size_t)kWsAlign, "workspace") : MUON_OK;
 }
 
 muon_status check_swiglu(const SwigluArgs& s, const char* const* names, const float* p, int64_t rows,
@@ -187,7 +222,11 @@ muon_status muon_grouped_mm_workspace_bytes(const void* x, int64_t ldx, const vo
                                             int64_t w_stride, int64_t rows, int32_t n_experts,
                                             int32_t k, int32_t n, int32_t trans_w, size_t* bytes) {
   if (bytes == nullptr) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = 0;
+  EXPERT_TRY(check_groups(rows, n_experts));
+  const GroupedMm g{x, w, nullptr, nullptr, ldx, ldw, w_stride, n, rows, n_experts, k, n,
+                    trans_w ? 1 : 0, 0, 0, nullptr};
+  EXPERT_TRY(check_mm(g));
+  *bytes = grouped_mm_workspace(g);
   return done(cudaSuccess, "");
 }
 
@@ -196,34 +235,31 @@ muon_status muon_grouped_mm(const void* x, int64_t ldx, const void* w, int64_t l
                             int64_t rows, int32_t n_experts, int32_t k, int32_t n, int32_t trans_w,
                             int32_t dtype, int32_t out_dtype, void* workspace,
                             size_t workspace_bytes, cudaStream_t stream) {
-  EXPERT_TRY(check_groups(row_offsets, rows, n_experts));
-  EXPERT_TRY(check_dim(k, "k"));
-  EXPERT_TRY(check_dim(n, "n"));
+  EXPERT_TRY(check_groups(rows, n_experts));
+  EXPERT_TRY(check_ptr(row_offsets, sizeof(int64_t), "row_offsets"));
   EXPERT_TRY(check_16bit(dtype, "dtype"));
   if (out_dtype != dtype && out_dtype != MUON_DTYPE_F32)
     return fail(MUON_ERR_INVALID_ARG, "out_dtype=%d: the inputs' type (%d) or fp32", out_dtype, dtype);
-  EXPERT_TRY(check_pitch(ldx, k, "ldx"));
-  EXPERT_TRY(check_pitch(ldw, trans_w ? k : n, "ldw"));
-  EXPERT_TRY(check_pitch(ldy, n, "ldy"));
-  if (n_experts > 1) EXPERT_TRY(check_pitch(w_stride, 1, "w_stride"));
-  if (rows > 0) {
-    EXPERT_TRY(check_ptr(x, 2, "x"));
-    EXPERT_TRY(check_ptr(w, 2, "w"));
-    EXPERT_TRY(check_ptr(y, dtype_size(out_dtype), "y"));
-  }
+  GroupedMm g{x, w, y, row_offsets, ldx, ldw, w_stride, ldy, rows, n_experts, k, n,
+              trans_w ? 1 : 0, dtype, out_dtype, nullptr};
+  EXPERT_TRY(check_mm(g));
+  if (rows > 0) EXPERT_TRY(check_ptr(y, dtype_size(out_dtype), "y"));
+  EXPERT_TRY(check_workspace(workspace, workspace_bytes, grouped_mm_workspace(g)));
   Device d;
   EXPERT_TRY(current_device(&d));
   if (rows == 0) return done(cudaSuccess, "");
-  GroupedMm p{x, w, y, row_offsets, ldx, ldw, w_stride, ldy, rows, n_experts, k, n,
-              trans_w ? 1 : 0, dtype, out_dtype, d.err};
-  return done(launch_grouped_mm(p, stream), "grouped product");
+  g.err = d.err;
+  return done(launch_grouped_mm(g, workspace, d.sms, stream), "grouped product");
 }
 
 muon_status muon_grouped_wgrad_workspace_bytes(const void* a, int64_t lda, const void* b,
                                                int64_t ldb, int64_t rows, int32_t m, int32_t n,
                                                size_t* bytes) {
   if (bytes == nullptr) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = 0;
+  EXPERT_TRY(check_groups(rows, 1));
+  const GroupedWgrad g{a, b, nullptr, nullptr, lda, ldb, n, 0, rows, 1, m, n, 0, 0, nullptr};
+  EXPERT_TRY(check_wgrad(g));
+  *bytes = grouped_wgrad_workspace(g);
   return done(cudaSuccess, "");
 }
 
@@ -232,24 +268,18 @@ muon_status muon_grouped_wgrad(const void* a, int64_t lda, const void* b, int64_
                                int64_t dw_stride, int64_t rows, int32_t n_experts, int32_t m,
                                int32_t n, int32_t accumulate, int32_t dtype, void* workspace,
                                size_t workspace_bytes, cudaStream_t stream) {
-  EXPERT_TRY(check_groups(row_offsets, rows, n_experts));
-  EXPERT_TRY(check_dim(m, "m"));
-  EXPERT_TRY(check_dim(n, "n"));
+  EXPERT_TRY(check_groups(rows, n_experts));
+  EXPERT_TRY(check_ptr(row_offsets, sizeof(int64_t), "row_offsets"));
   EXPERT_TRY(check_16bit(dtype, "dtype"));
-  EXPERT_TRY(check_pitch(lda, m, "lda"));
-  EXPERT_TRY(check_pitch(ldb, n, "ldb"));
-  EXPERT_TRY(check_pitch(lddw, n, "lddw"));
-  if (n_experts > 1) EXPERT_TRY(check_pitch(dw_stride, n, "dw_stride"));
-  if (rows > 0) {
-    EXPERT_TRY(check_ptr(a, 2, "a"));
-    EXPERT_TRY(check_ptr(b, 2, "b"));
-  }
+  GroupedWgrad g{a, b, dw, row_offsets, lda, ldb, lddw, dw_stride, rows, n_experts, m, n,
+                 accumulate ? 1 : 0, dtype, nullptr};
+  EXPERT_TRY(check_wgrad(g));
   EXPERT_TRY(check_ptr(dw, sizeof(float), "dw"));
+  EXPERT_TRY(check_workspace(workspace, workspace_bytes, grouped_wgrad_workspace(g)));
   Device d;
   EXPERT_TRY(current_device(&d));
-  GroupedWgrad p{a, b, dw, row_offsets, lda, ldb, lddw, dw_stride, rows, n_experts, m, n,
-                 accumulate ? 1 : 0, dtype, d.err};
-  return done(launch_grouped_wgrad(p, stream), "grouped weight gradient");
+  g.err = d.err;
+  return done(launch_grouped_wgrad(g, workspace, d.sms, stream), "grouped weight gradient");
 }
 
 muon_status muon_swiglu(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,

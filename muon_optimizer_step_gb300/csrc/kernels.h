@@ -105,7 +105,9 @@ struct GroupedMm {            // y = x W_e per expert (see muon_grouped_mm)
   int32_t n_experts, k, n, trans, dtype, out_dtype;
   int* err;
 };
-cudaError_t launch_grouped_mm(const GroupedMm& p, cudaStream_t st);
+// Bytes for copies of operands whose rows do not start on 16 bytes.
+size_t grouped_mm_workspace(const GroupedMm& g);
+cudaError_t launch_grouped_mm(const GroupedMm& g, void* workspace, int sms, cudaStream_t st);
 
 struct GroupedWgrad {         // dw_e (+)= a^T b per expert (see muon_grouped_wgrad)
   const void* a;
@@ -116,7 +118,8 @@ struct GroupedWgrad {         // dw_e (+)= a^T b per expert (see muon_grouped_wg
   int32_t n_experts, m, n, accumulate, dtype;
   int* err;
 };
-cudaError_t launch_grouped_wgrad(const GroupedWgrad& p, cudaStream_t st);
+size_t grouped_wgrad_workspace(const GroupedWgrad& g);
+cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms, cudaStream_t st);
 
 // n = 3: g, u, a (forward); n = 5: da, g, u, dg, du (gradient).
 struct SwigluArgs {

@@ -394,6 +394,11 @@ def test_binding_refuses(capi):
                  (x, y, off[:2], dw)):
         with pytest.raises(ValueError):
             capi.muon_grouped_wgrad(*args)
+    with pytest.raises(capi.MuonError):      # a workspace that is too small
+        xo = torch.zeros(4, 17, device="cuda", dtype=torch.bfloat16)
+        wo = torch.zeros(2, 17, 8, device="cuda", dtype=torch.bfloat16)
+        capi.muon_grouped_mm(xo, wo, off, y,
+                             workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     capi.muon_check()
 
 
