@@ -22,9 +22,20 @@
 // not issued, and before the one that sees both kinds the issuing warp zeroes them in shared
 // memory, in both operands (0 * NaN is NaN).
 //
-// CTA roles (384 threads): warp 0 issues the TMA loads, warp 1 the MMAs, warp 2 owns TMEM,
-// warps 4-11 drain the accumulators (two, in TMEM's 512 columns,
-// so a tile's stores overlap the next one's MMAs).  Every wait is bounded.
+// Tiles run on CTA pairs (a 2-CTA cluster, cta_group::2): each CTA holds 128 of the MMA's 256
+// rows and half of its N columns of operand B, so a k-step brings 32 KB instead of 48 KB into
+// each SM for the same work; on single CTAs the operand traffic from L2 was the bound (53 %
+// tensor pipe on 98304 x 1408 -> 2048, 64 experts).  Single CTAs run where pairs would leave
+// SMs without tiles.
+//
+// The tensor core truncates when it adds to its accumulator, always towards zero, so the error
+// of a sum grows with its number of steps (1.8e-6 of the result after 1536 rows).  Results
+// kept in fp32 are therefore summed in segments of kSegment k-blocks, which the epilogue adds
+// up in registers with rounding to nearest.
+//
+// CTA roles (384 threads): warp 0 issues the TMA loads, warp 1 the MMAs (on the first CTA of a
+// pair), warp 2 owns TMEM, warps 4-11 drain the accumulators (two, in TMEM's 512 columns, so a
+// tile's stores overlap the next one's MMAs).  Every wait is bounded.
 #include <atomic>
 
 #include <cudaTypedefs.h>
@@ -44,17 +55,33 @@ constexpr int kBK = 64;             // k-block: 128 bytes of a 16-bit row
 constexpr int kABytes = kBM * 128;  // 16 KB
 constexpr int kBox = 64 * 128;      // an MN-major box: 64 k-rows of 128 bytes
 constexpr int kAccCols = 256;       // TMEM columns of one accumulator
-constexpr int kStagingBytes = 2048; // per epilogue warp (mm)
+constexpr int kSegment = 8;         // k-blocks per segment of an fp32 result
+constexpr int kMaxStages = 8;
 constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 
-// mm tile variants.  Wide: up to 256 rows per tile, for experts with many rows.  Narrow: up to
-// 64, whose smaller stages leave room for more of the weight in flight: with few rows the
-// product is bound by streaming it.
+// mm tile variants: kMaxN rows of one expert per tile at most, on single CTAs or pairs.
+// Narrow: smaller stages leave room for more of the weight in flight, for experts with few
+// rows, whose product is bound by streaming it.
+struct Pair {
+  static constexpr bool kPair = true;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6;
+};
 struct Wide {
+  static constexpr bool kPair = false;
   static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4;
 };
 struct Narrow {
+  static constexpr bool kPair = false;
   static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 8;
+};
+// What follows from a variant (wgrad uses Pair and Wide).
+template <typename V>
+struct Shape {
+  static constexpr int kCtas = V::kPair ? 2 : 1;
+  static constexpr int kM = kBM * kCtas;                   // M of the MMA
+  static constexpr int kStepN = 16 * kCtas;                // N goes in steps of this
+  static constexpr int kStage = kABytes + V::kMaxN / kCtas * 128;
+  static constexpr int kBlocks = (V::kMaxN + 63) / 64;     // 32-column blocks per epilogue warp
 };
 
 struct MmParams {
@@ -70,7 +97,10 @@ struct WgradParams {
 
 // Barriers and flags of one CTA.
 struct Control {
-  uint64_t full[8], empty[8];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  // wgrad on pairs, last k-block of a tile: the second CTA's own operands have landed, and it
+  // has zeroed the rows that are not its expert's.
+  uint64_t tail[kMaxStages], fixed[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t mma_done;
   uint32_t tmem;
@@ -86,10 +116,100 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, in
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const void* tmap, int x, int y,
+                                                 int z, uint32_t bar_cluster_addr) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar_cluster_addr)
+      : "memory");
+}
+
+// Loads that signal `bar` of this CTA (single) or of the pair's first CTA.
+template <bool kPair>
+__device__ __forceinline__ void load_2d(void* dst, const void* tmap, int x, int y, uint64_t* bar) {
+  if constexpr (kPair) tma_load_2d_pair(smem_u32(dst), tmap, x, y, mapa_shared(smem_u32(bar), 0));
+  else tma_load_2d(dst, tmap, x, y, bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void load_3d(void* dst, const void* tmap, int x, int y, int z,
+                                        uint64_t* bar) {
+  if constexpr (kPair) tma_load_3d_pair(smem_u32(dst), tmap, x, y, z, mapa_shared(smem_u32(bar), 0));
+  else tma_load_3d(dst, tmap, x, y, z, bar);
+}
+
+// Operand descriptors as two words (see smem_desc_sw128): the low one moves with the address.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return (saddr & 0x3FFFF) >> 4 | (lbo >> 4) << 16;
+}
+
+template <bool kPair>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                    uint32_t add) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
+        : "memory");
+}
+
+// One lane of the (whole) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// Bounded wait of a whole warp.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* err, int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitBudget, err, abort));
+}
+
+// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far complete.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (kPair) tc_commit_pair(bar, (uint16_t)0x3);
+  else tc_commit(bar);
+}
+
 // idesc_bf16 with both operand types cleared is the fp16 form.
-__device__ __forceinline__ uint32_t idesc_16(bool bf16, int N, int a_mn, int b_mn) {
-  const uint32_t d = idesc_bf16(kBM, N, a_mn, b_mn);
+__device__ __forceinline__ uint32_t idesc_16(bool bf16, int M, int N, int a_mn, int b_mn) {
+  const uint32_t d = idesc_bf16(M, N, a_mn, b_mn);
   return bf16 ? d : d & ~((1u << 7) | (1u << 10));
+}
+
+// Waits for an arrival from the other CTA of the pair, acquiring what it wrote.
+__device__ __forceinline__ bool wait_peer(uint64_t* bar, uint32_t parity, int* err,
+                                          volatile int* abort) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitBudget) {
+      atomicExch(err, kErrTimeout);
+      *abort = 1;
+      return false;
+    }
+  }
 }
 
 // Waits that ignore the abort flag: copies and MMAs in flight must end before the CTA does.
@@ -115,32 +235,101 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ void setup(Control& c, int stages, int warp) {
+template <bool kPair>
+__device__ __forceinline__ void setup(Control& c, int warp) {
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&c.full[s], 1);
       mbar_init(&c.empty[s], 1);
+      mbar_init(&c.tail[s], 1);
+      mbar_init(&c.fixed[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.acc_full[b], 1);
-      mbar_init(&c.acc_empty[b], kEpiWarps);
+      mbar_init(&c.acc_empty[b], (kPair ? 2 : 1) * kEpiWarps);
     }
     mbar_init(&c.mma_done, 1);
     c.abort = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(&c.tmem, 2 * kAccCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(&c.tmem, 2 * kAccCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&c.tmem, 2 * kAccCols);
+      tmem_relinquish();
+    }
   }
 }
 
-__device__ __forceinline__ void teardown(Control& c, int warp) {
+// Barriers and TMEM are ready in every CTA that may signal them.
+template <bool kPair>
+__device__ __forceinline__ void sync_ctas() {
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+}
+
+template <bool kPair>
+__device__ __forceinline__ void teardown(Control& c, int warp) {
+  sync_ctas<kPair>();
   if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(c.tmem, 2 * kAccCols);
+    if constexpr (kPair) tmem_dealloc_pair(c.tmem, 2 * kAccCols);
+    else tmem_dealloc(c.tmem, 2 * kAccCols);
+  }
+}
+
+// An epilogue warp is done reading accumulator `ab`.
+template <bool kPair>
+__device__ __forceinline__ void release_acc(Control& c, int ab, uint32_t rank, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    if (!kPair || rank == 0) mbar_arrive(&c.acc_empty[ab]);
+    else mbar_arrive_cluster(mapa_shared(smem_u32(&c.acc_empty[ab]), 0));
+  }
+}
+
+// Waits for accumulator use number `use` (epilogue warp).
+__device__ __forceinline__ bool wait_acc(Control& c, int use, int* err) {
+  const bool ok = mbar_wait_bounded(&c.acc_full[use & 1], (use >> 1) & 1, kWaitBudget, err, &c.abort);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  tc_fence_after();
+  return true;
+}
+
+// 32 lanes x 16 consecutive 32-bit columns of TMEM.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// sum (+)= 32 accumulator columns from `col` on of this warp's lanes.
+__device__ __forceinline__ void add_acc(uint32_t tmem, int ab, int q, int col, bool first,
+                                        float (&sum)[32]) {
+  const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kAccCols + col);
+  if (first) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(at, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) sum[k] = __uint_as_float(v[k]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(at + h, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sum[h + k] += __uint_as_float(v[k]);
+    }
   }
 }
 
@@ -181,14 +370,18 @@ __device__ __forceinline__ void count_tiles(const int32_t* off, int n_experts, i
 }
 
 // ---------------------------------------------------------------------------- mm
+constexpr int kMmStaging = 2048;  // per epilogue warp
+
 struct MmTile {
   int expert, row, rows;  // rows row .. row + rows - 1 of x and y, all of `expert`
-  int n;                  // the MMA's N: rows in steps of 16
+  int n;                  // the MMA's N: rows in steps of kStepN
   int f0;                 // first column of y
 };
 
+template <typename V>
 __device__ __forceinline__ MmTile mm_tile(int64_t t, int f_tiles, int n_experts, const int32_t* off,
                                           const int32_t* first) {
+  constexpr int kStep = Shape<V>::kStepN;
   const int rt = (int)(t / f_tiles);
   int lo = 0, hi = n_experts - 1;  // the expert with first[e] <= rt < first[e + 1]
   while (lo < hi) {
@@ -198,12 +391,12 @@ __device__ __forceinline__ MmTile mm_tile(int64_t t, int f_tiles, int n_experts,
   MmTile m;
   m.expert = lo;
   const int rows = off[lo + 1] - off[lo], tiles = first[lo + 1] - first[lo];
-  const int width = ((rows + tiles - 1) / tiles + 15) & ~15;
+  const int width = ((rows + tiles - 1) / tiles + kStep - 1) / kStep * kStep;
   const int begin = (rt - first[lo]) * width;
   m.row = off[lo] + begin;
   m.rows = min(width, rows - begin);
-  m.n = (m.rows + 15) & ~15;
-  m.f0 = (int)(t % f_tiles) * kBM;
+  m.n = (m.rows + kStep - 1) / kStep * kStep;
+  m.f0 = (int)(t % f_tiles) * Shape<V>::kM;
   return m;
 }
 
@@ -212,14 +405,14 @@ __device__ __forceinline__ MmTile mm_tile(int64_t t, int f_tiles, int n_experts,
 // consecutive bytes of a row of y leave together.
 template <typename O>
 __device__ __forceinline__ void mm_store(const GroupedMm& g, const MmTile& m, int c, int f, int lane,
-                                         const uint32_t (&v)[32], O* stage) {
-  constexpr int kRows = kStagingBytes / (32 * sizeof(O));  // rows staged at a time
+                                         const float (&v)[32], O* stage) {
+  constexpr int kRows = kMmStaging / (32 * sizeof(O));  // rows staged at a time
   constexpr int kPer = 16 / sizeof(O), kChunks = 32 / kPer, kPass = 32 / kChunks;
 #pragma unroll
   for (int h = 0; h < 32 / kRows; ++h) {
     if (c * 32 + h * kRows >= m.rows) break;
 #pragma unroll
-    for (int t = 0; t < kRows; ++t) put(&stage[t * 32 + lane], __uint_as_float(v[h * kRows + t]));
+    for (int t = 0; t < kRows; ++t) put(&stage[t * 32 + lane], v[h * kRows + t]);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kRows / kPass; ++i) {
@@ -239,115 +432,148 @@ __device__ __forceinline__ void mm_store(const GroupedMm& g, const MmTile& m, in
 }
 
 template <typename V, typename O>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(Shape<V>::kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 grouped_mm_kernel(const __grid_constant__ MmParams p) {
-  constexpr int kStageBytes = kABytes + V::kMaxN * 128;
+  using S = Shape<V>;
+  constexpr bool kFp32 = sizeof(O) == 4;  // summed in segments
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
   __shared__ int32_t off[kMaxExperts + 1], first[kMaxExperts + 1];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const GroupedMm& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  setup(c, V::kStages, warp);
+  const uint32_t rank = V::kPair ? cluster_ctarank() : 0u;
+  setup<V::kPair>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kMaxN, lane, first);
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
+  sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
   volatile int* abort = &c.abort;
-  const int f_tiles = (g.n - 1) / kBM + 1, k_blocks = (g.k - 1) / kBK + 1;
+  const int f_tiles = (g.n - 1) / S::kM + 1, k_blocks = (g.k - 1) / kBK + 1;
   const int64_t tiles = (int64_t)first[g.n_experts] * f_tiles;
+  const int64_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
 
   if (warp == 0) {
     if (lane == 0) {
       Ring<V::kStages> ring;
       int64_t fills = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const MmTile m = mm_tile(t, f_tiles, g.n_experts, off, first);
-        const int boxes = (m.n + V::kBoxRows - 1) / V::kBoxRows;
-        const uint32_t bytes = kABytes + boxes * V::kBoxRows * 128;
+      for (int64_t t = unit; t < tiles && ok; t += units) {
+        const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
+        const int part = m.n / S::kCtas;  // rows of x this CTA brings
+        const int boxes = (part + V::kBoxRows - 1) / V::kBoxRows;
+        const uint32_t bytes = S::kCtas * (kABytes + boxes * V::kBoxRows * 128);
+        const int f = m.f0 + kBM * (int)rank, row = m.row + part * (int)rank;
         for (int kb = 0; kb < k_blocks; ++kb, ++fills) {
           uint64_t* full = &c.full[ring.stage];
           if (!mbar_wait_bounded(&c.empty[ring.stage], ring.phase ^ 1u, kWaitBudget, g.err, abort)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(full, bytes);
-          uint8_t* sa = smem + ring.stage * kStageBytes;
+          // Only the first CTA of a pair arrives, announcing both CTAs' bytes.
+          if (rank == 0) mbar_arrive_expect_tx(full, bytes);
+          uint8_t* sa = smem + ring.stage * S::kStage;
           const int k0 = kb * kBK;
           if (g.trans) {
-            tma_load_3d(sa, &p.w, k0, m.f0, m.expert, full);
+            load_3d<V::kPair>(sa, &p.w, k0, f, m.expert, full);
           } else {
-            tma_load_3d(sa, &p.w, m.f0, k0, m.expert, full);
-            tma_load_3d(sa + kBox, &p.w, m.f0 + 64, k0, m.expert, full);
+            load_3d<V::kPair>(sa, &p.w, f, k0, m.expert, full);
+            load_3d<V::kPair>(sa + kBox, &p.w, f + 64, k0, m.expert, full);
           }
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sa + kABytes + b * V::kBoxRows * 128, &p.x, k0, m.row + b * V::kBoxRows,
-                        full);
+            load_2d<V::kPair>(sa + kABytes + b * V::kBoxRows * 128, &p.x, k0, row + b * V::kBoxRows,
+                              full);
           ring.next();
         }
       }
-      for (int64_t f = fills - 1; f >= 0 && f >= fills - V::kStages; --f)
-        drain(&c.full[f % V::kStages], (uint32_t)((f / V::kStages) & 1), g.err);
+      if (rank == 0)
+        for (int64_t f = fills - 1; f >= 0 && f >= fills - V::kStages; --f)
+          drain(&c.full[f % V::kStages], (uint32_t)((f / V::kStages) & 1), g.err);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      Ring<V::kStages> ring;
-      int local = 0;
-      bool ok = true;
-      const uint32_t sbase = smem_u32(smem);
-      const int a_mn = g.trans ? 0 : 1;
-      const uint32_t a_step = a_mn ? 16 * 128 : 32, a_lbo = a_mn ? kBox : 16;
-      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++local) {
-        const MmTile m = mm_tile(t, f_tiles, g.n_experts, off, first);
-        const uint32_t idesc = idesc_16(g.dtype == kBf16, m.n, a_mn, 0);
-        const int ab = local & 1;
-        if (!mbar_wait_bounded(&c.acc_empty[ab], ((local >> 1) & 1) ^ 1u, kWaitBudget, g.err, abort))
-          break;
+  } else if (warp == 1 && rank == 0) {
+    // The whole warp walks the k-blocks and one lane issues, so that descriptors and counters
+    // stay warp-uniform.
+    Ring<V::kStages> ring;
+    int use = 0;
+    bool ok = true;
+    const uint32_t a_mn = g.trans ? 0 : 1, a_step = a_mn ? 16 * 128 / 16 : 32 / 16;
+    const uint32_t a0 = desc_lo(smem_u32(smem), a_mn ? kBox : 16);
+    const uint32_t b0 = desc_lo(smem_u32(smem) + kABytes, 16);
+    for (int64_t t = unit; t < tiles && ok; t += units) {
+      const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
+      const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, m.n, a_mn, 0);
+      for (int kb = 0; kb < k_blocks;) {
+        // One accumulator: all k-blocks, or a segment of them.
+        const int end = kFp32 ? min(k_blocks, kb + kSegment) : k_blocks;
+        ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
+        if (!ok) break;
         tc_fence_after();
-        for (int kb = 0; kb < k_blocks; ++kb) {
-          if (!mbar_wait_bounded(&c.full[ring.stage], ring.phase, kWaitBudget, g.err, abort)) {
-            ok = false;
-            break;
+        const uint32_t d = tmem + (use & 1) * kAccCols;
+        uint32_t add = 0;
+        for (; kb < end; ++kb) {
+          ok = wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
+          if (!ok) break;
+          const uint32_t a = a0 + ring.stage * (S::kStage / 16), b = b0 + ring.stage * (S::kStage / 16);
+          if (elect_one()) {
+            // Columns past k are zeros in both operands.
+            mma<V::kPair>(d, a, b, idesc, add);
+            mma<V::kPair>(d, a + a_step, b + 2, idesc, 1);
+            mma<V::kPair>(d, a + 2 * a_step, b + 4, idesc, 1);
+            mma<V::kPair>(d, a + 3 * a_step, b + 6, idesc, 1);
+            commit<V::kPair>(&c.empty[ring.stage]);
           }
-          tc_fence_after();
-          const uint32_t sa = sbase + ring.stage * kStageBytes, sb = sa + kABytes;
-          const int steps = min(4, (g.k - kb * kBK + 15) / 16);
-          for (int s = 0; s < steps; ++s)
-            tc_mma_f16(tmem + ab * kAccCols, smem_desc_sw128(sa + s * a_step, a_lbo, 1024),
-                       smem_desc_sw128(sb + s * 32, 16, 1024), idesc, (kb | s) != 0);
-          tc_commit(&c.empty[ring.stage]);
+          __syncwarp();
+          add = 1;
           ring.next();
         }
-        if (ok) tc_commit(&c.acc_full[ab]);
+        if (!ok) break;
+        if (elect_one()) commit<V::kPair>(&c.acc_full[use & 1]);
+        __syncwarp();
+        ++use;
       }
-      tc_commit(&c.mma_done);
+    }
+    if (elect_one()) {
+      if constexpr (V::kPair) tc_commit_pair(&c.mma_done, (uint16_t)0x1);
+      else tc_commit(&c.mma_done);
       drain(&c.mma_done, 0, g.err);
     }
     __syncwarp();
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;  // a quarter of the lanes, every second block
-    O* stage = reinterpret_cast<O*>(smem + V::kStages * kStageBytes + (warp - 4) * kStagingBytes);
-    int local = 0;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++local) {
-      const MmTile m = mm_tile(t, f_tiles, g.n_experts, off, first);
-      const int ab = local & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c.acc_full[ab], (local >> 1) & 1, kWaitBudget,
-                                                     g.err, abort)))
-        break;
-      tc_fence_after();
-      for (int b = half; b * 32 < m.n; b += 2) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kAccCols + 32 * b), v);
-        tmem_ld_wait();
-        mm_store<O>(g, m, b, m.f0 + 32 * q, lane, v, stage);
+    O* stage = reinterpret_cast<O*>(smem + V::kStages * S::kStage + (warp - 4) * kMmStaging);
+    int use = 0;
+    bool ok = true;
+    for (int64_t t = unit; t < tiles && ok; t += units) {
+      const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
+      const int f = m.f0 + kBM * (int)rank + 32 * q;
+      if constexpr (kFp32) {
+        float sum[S::kBlocks][32];
+        for (int kb = 0; kb < k_blocks; kb += kSegment, ++use) {
+          ok = wait_acc(c, use, g.err);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < S::kBlocks; ++i)
+            if ((2 * i + half) * 32 < m.n)
+              add_acc(tmem, use & 1, q, (2 * i + half) * 32, kb == 0, sum[i]);
+          release_acc<V::kPair>(c, use & 1, rank, lane);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < S::kBlocks; ++i)
+          if ((2 * i + half) * 32 < m.n) mm_store<O>(g, m, 2 * i + half, f, lane, sum[i], stage);
+      } else {
+        ok = wait_acc(c, use, g.err);
+        if (!ok) break;
+        for (int b = half; b * 32 < m.n; b += 2) {
+          float v[32];
+          add_acc(tmem, use & 1, q, 32 * b, true, v);
+          mm_store<O>(g, m, b, f, lane, v, stage);
+        }
+        release_acc<V::kPair>(c, use & 1, rank, lane);
+        ++use;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.acc_empty[ab]);
     }
     // Rows of no expert.
     const int64_t head = off[0], none = head + g.rows - off[g.n_experts];
@@ -356,12 +582,11 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
       for (int64_t f = threadIdx.x - 128; f < g.n; f += kEpiWarps * 32) put(&row[f], 0.f);
     }
   }
-  teardown(c, warp);
+  teardown<V::kPair>(c, warp);
 }
 
 // ---------------------------------------------------------------------------- wgrad
-constexpr int kWgradStages = 4;
-constexpr int kWgradStage = kABytes + 256 * 128;
+constexpr int kWgradStaging = 4096;  // per epilogue warp: a block of 32 x 32 floats
 
 struct WgradTile {
   int expert, row, rows;  // the expert's rows
@@ -373,179 +598,251 @@ struct WgradGrid {
   int64_t tiles;
 };
 
+template <typename V>
 __host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g) {
+  constexpr int kStep = Shape<V>::kStepN;
   WgradGrid w;
-  w.m_tiles = (g.m - 1) / kBM + 1;
-  w.n_tiles = (g.n - 1) / 256 + 1;
-  w.width = ((g.n - 1) / w.n_tiles + 1 + 15) & ~15;  // columns dealt evenly, in steps of 16
+  w.m_tiles = (g.m - 1) / Shape<V>::kM + 1;
+  w.n_tiles = (g.n - 1) / V::kMaxN + 1;
+  w.width = ((g.n - 1) / w.n_tiles + kStep) / kStep * kStep;  // columns dealt evenly
   w.tiles = (int64_t)g.n_experts * w.m_tiles * w.n_tiles;
   return w;
 }
 
+template <typename V>
 __device__ __forceinline__ WgradTile wgrad_tile(const GroupedWgrad& g, const WgradGrid& w, int64_t t,
-                                                const int32_t* off) {
+                                                bool bad) {
+  constexpr int kStep = Shape<V>::kStepN;
   const int64_t per = (int64_t)w.m_tiles * w.n_tiles;
   const int e = (int)(t / per);
   const int64_t r = t - e * per;
   WgradTile x;
   x.expert = e;
-  x.row = off[e];
-  x.rows = off[e + 1] - off[e];
-  x.i0 = (int)(r / w.n_tiles) * kBM;
+  x.row = bad ? 0 : (int)g.offsets[e];
+  x.rows = bad ? 0 : (int)(g.offsets[e + 1] - g.offsets[e]);
+  x.i0 = (int)(r / w.n_tiles) * Shape<V>::kM;
   x.j0 = (int)(r % w.n_tiles) * w.width;
   x.cols = min(w.width, g.n - x.j0);
-  x.n = (x.cols + 15) & ~15;
+  x.n = (x.cols + kStep - 1) / kStep * kStep;
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// Zeroes rows left .. 15 of the last K = 16 step in each of a stage's boxes (whole warp).
+__device__ __forceinline__ void zero_rows(uint8_t* stage, int left, int boxes, int lane) {
+  const int rows = 16 - left % 16;
+  uint8_t* z = stage + left * 128;
+  for (int i = lane; i < boxes * rows * 8; i += 32)
+    *reinterpret_cast<uint4*>(z + i / (rows * 8) * kBox + i % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// dw[row .. row + 31, col .. col + 31] (=, +=) the block whose row `lane` the warp's lane holds.
+// The block is turned around in `stage` (16-byte chunk k of row r in slot k ^ (r & 7), free of
+// bank conflicts both ways), so that four whole 128-byte rows leave per access.
+__device__ __forceinline__ void wgrad_store(const GroupedWgrad& g, float* dw, int rows, int cols,
+                                            int lane, const float (&v)[32], float4* stage) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    stage[8 * lane + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  __syncwarp();
+  const int k = lane & 7, left = cols - 4 * k;
+  float* dst = dw + (int64_t)(lane >> 3) * g.lddw + 4 * k;
+#pragma unroll
+  for (int i = 0; i < 8; ++i, dst += 4 * g.lddw) {
+    const int r = 4 * i + (lane >> 3);
+    if (r >= rows || left <= 0) continue;
+    float4 o = stage[8 * r + (k ^ (r & 7))];
+    if (left >= 4 && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
+      if (g.accumulate) {
+        const float4 d = __ldcs(reinterpret_cast<const float4*>(dst));
+        o = make_float4(d.x + o.x, d.y + o.y, d.z + o.z, d.w + o.w);
+      }
+      __stcs(reinterpret_cast<float4*>(dst), o);
+    } else {
+      const float e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < left) dst[j] = g.accumulate ? dst[j] + e[j] : e[j];
+    }
+  }
+  __syncwarp();
+}
+
+template <typename V>
+__global__ void __cluster_dims__(Shape<V>::kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
+  using S = Shape<V>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
-  __shared__ int32_t off[kMaxExperts + 1];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const GroupedWgrad& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  setup(c, kWgradStages, warp);
-  load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  const uint32_t rank = V::kPair ? cluster_ctarank() : 0u;
+  setup<V::kPair>(c, warp);
+  bool bad = false;
+  for (int e = threadIdx.x; e <= g.n_experts; e += kThreads) {
+    const int64_t o = g.offsets[e];
+    bad |= o < 0 || o > g.rows || (e > 0 && g.offsets[e - 1] > o);
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(g.err, kErrRowOffsets);
+  sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
   volatile int* abort = &c.abort;
-  const WgradGrid w = wgrad_grid(g);
+  const WgradGrid w = wgrad_grid<V>(g);
+  const int64_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
 
   if (warp == 0) {
     if (lane == 0) {
-      Ring<kWgradStages> ring;
+      Ring<V::kStages> ring;
       int64_t fills = 0;
+      uint32_t tails = 0, used = 0;  // per stage: parity of the next use of `tail`; any use
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < w.tiles && ok; t += gridDim.x) {
-        const WgradTile x = wgrad_tile(g, w, t, off);
-        const int boxes = (x.n + 63) / 64;
+      for (int64_t t = unit; t < w.tiles && ok; t += units) {
+        const WgradTile x = wgrad_tile<V>(g, w, t, bad);
+        const int part = x.n / S::kCtas, boxes = (part + 63) / 64;  // columns of b this CTA brings
+        const int i = x.i0 + kBM * (int)rank, j = x.j0 + part * (int)rank;
         for (int r = 0; r < x.rows; r += kBK, ++fills) {
-          uint64_t* full = &c.full[ring.stage];
           if (!mbar_wait_bounded(&c.empty[ring.stage], ring.phase ^ 1u, kWaitBudget, g.err, abort)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(full, (2 + boxes) * kBox);
-          uint8_t* sa = smem + ring.stage * kWgradStage;
-          for (int b = 0; b < 2; ++b)
-            tma_load_2d(sa + b * kBox, &p.a, x.i0 + 64 * b, x.row + r, full);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sa + kABytes + b * kBox, &p.b, x.j0 + 64 * b, x.row + r, full);
+          // A last k-block with rows to zero lands on each CTA's own barrier.
+          const bool own = !V::kPair || (x.rows - r < kBK && (x.rows - r) % 16 != 0);
+          uint64_t* full = own && rank != 0 ? &c.tail[ring.stage] : &c.full[ring.stage];
+          if (own || rank == 0) mbar_arrive_expect_tx(full, (own ? 1 : 2) * (2 + boxes) * kBox);
+          uint8_t* sa = smem + ring.stage * S::kStage;
+          if (own && rank != 0) {
+            tails ^= 1u << ring.stage;
+            used |= 1u << ring.stage;
+          }
+          if (own) {
+            for (int b = 0; b < 2; ++b) load_2d<false>(sa + b * kBox, &p.a, i + 64 * b, x.row + r, full);
+            for (int b = 0; b < boxes; ++b)
+              load_2d<false>(sa + kABytes + b * kBox, &p.b, j + 64 * b, x.row + r, full);
+          } else {
+            for (int b = 0; b < 2; ++b) load_2d<true>(sa + b * kBox, &p.a, i + 64 * b, x.row + r, full);
+            for (int b = 0; b < boxes; ++b)
+              load_2d<true>(sa + kABytes + b * kBox, &p.b, j + 64 * b, x.row + r, full);
+          }
           ring.next();
         }
       }
-      for (int64_t f = fills - 1; f >= 0 && f >= fills - kWgradStages; --f)
-        drain(&c.full[f % kWgradStages], (uint32_t)((f / kWgradStages) & 1), g.err);
+      if (rank == 0)
+        for (int64_t f = fills - 1; f >= 0 && f >= fills - V::kStages; --f)
+          drain(&c.full[f % V::kStages], (uint32_t)((f / V::kStages) & 1), g.err);
+      for (int s = 0; s < V::kStages; ++s)
+        if (used >> s & 1) drain(&c.tail[s], (tails >> s & 1) ^ 1u, g.err);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // The whole warp waits, lane 0 issues: the last k-block of an expert needs all lanes.
-    Ring<kWgradStages> ring;
-    int local = 0;
+  } else if (warp == 1 && rank == 0) {
+    Ring<V::kStages> ring;
+    int use = 0;
+    uint32_t fixes = 0;  // per stage: parity of the next use of its `fixed` barrier
     bool ok = true;
-    const uint32_t sbase = smem_u32(smem);
-    for (int64_t t = blockIdx.x; t < w.tiles && ok; t += gridDim.x) {
-      const WgradTile x = wgrad_tile(g, w, t, off);
-      if (x.rows == 0) continue;
-      const uint32_t idesc = idesc_16(g.dtype == kBf16, x.n, 1, 1);
-      const int ab = local & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&c.acc_empty[ab], ((local >> 1) & 1) ^ 1u,
-                                                     kWaitBudget, g.err, abort));
-      ++local;
-      tc_fence_after();
-      for (int r = 0; r < x.rows && ok; r += kBK) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&c.full[ring.stage], ring.phase, kWaitBudget,
-                                                       g.err, abort));
+    constexpr uint32_t kStep = 16 * 128 / 16;
+    const uint32_t a0 = desc_lo(smem_u32(smem), kBox), b0 = desc_lo(smem_u32(smem) + kABytes, kBox);
+    for (int64_t t = unit; t < w.tiles && ok; t += units) {
+      const WgradTile x = wgrad_tile<V>(g, w, t, bad);
+      const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, x.n, 1, 1);
+      for (int left = x.rows; left > 0;) {
+        ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
-        const int left = x.rows - r, steps = min(4, (left + 15) / 16);
-        if (left < kBK && left % 16 != 0) {
-          // Rows left .. 16 steps - 1 of every box (A's two, then B's) are the next expert's.
-          const int rows = 16 * steps - left, boxes = 2 + (x.n + 63) / 64;
-          uint8_t* z = smem + ring.stage * kWgradStage + left * 128;
-          for (int i = lane; i < boxes * rows * 8; i += 32)
-            *reinterpret_cast<uint4*>(z + i / (rows * 8) * kBox + i % (rows * 8) * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t sa = sbase + ring.stage * kWgradStage, sb = sa + kABytes;
-          for (int s = 0; s < steps; ++s)
-            tc_mma_f16(tmem + ab * kAccCols, smem_desc_sw128(sa + s * 16 * 128, kBox, 1024),
-                       smem_desc_sw128(sb + s * 16 * 128, kBox, 1024), idesc, (r | s) != 0);
-          tc_commit(&c.empty[ring.stage]);
+        const uint32_t d = tmem + (use & 1) * kAccCols;
+        uint32_t add = 0;
+        for (int in = 0; in < kSegment && left > 0; ++in, left -= kBK) {
+          ok = wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
+          if (!ok) break;
+          if (left < kBK && left % 16 != 0) {
+            // The rows behind the expert's last are the next expert's.
+            zero_rows(smem + ring.stage * S::kStage, left, 2 + (x.n / S::kCtas + 63) / 64, lane);
+            if (V::kPair) {
+              ok = __all_sync(0xffffffffu, wait_peer(&c.fixed[ring.stage], fixes >> ring.stage & 1,
+                                                     g.err, &c.abort));
+              if (!ok) break;
+              fixes ^= 1u << ring.stage;
+            }
+          }
+          const uint32_t a = a0 + ring.stage * (S::kStage / 16), b = b0 + ring.stage * (S::kStage / 16);
+          if (elect_one()) {
+            mma<V::kPair>(d, a, b, idesc, add);
+            if (left > 16) mma<V::kPair>(d, a + kStep, b + kStep, idesc, 1);
+            if (left > 32) mma<V::kPair>(d, a + 2 * kStep, b + 2 * kStep, idesc, 1);
+            if (left > 48) mma<V::kPair>(d, a + 3 * kStep, b + 3 * kStep, idesc, 1);
+            commit<V::kPair>(&c.empty[ring.stage]);
+          }
+          __syncwarp();
+          add = 1;
+          ring.next();
         }
-        ring.next();
+        if (!ok) break;
+        if (elect_one()) commit<V::kPair>(&c.acc_full[use & 1]);
+        __syncwarp();
+        ++use;
       }
-      if (ok && lane == 0) tc_commit(&c.acc_full[ab]);
     }
-    if (lane == 0) {
-      tc_commit(&c.mma_done);
+    if (elect_one()) {
+      if constexpr (V::kPair) tc_commit_pair(&c.mma_done, (uint16_t)0x1);
+      else tc_commit(&c.mma_done);
       drain(&c.mma_done, 0, g.err);
     }
     __syncwarp();
+  } else if (warp == 1) {
+    // Second CTA of a pair: zeroes its own part of a last k-block, then tells the first CTA.
+    // A stage's barriers are used again only after the MMAs that waited for this.
+    int64_t fills = 0;
+    uint32_t tails = 0;  // per stage: parity of the next use of its `tail` barrier
+    for (int64_t t = unit; t < w.tiles; t += units) {
+      const WgradTile x = wgrad_tile<V>(g, w, t, bad);
+      fills += (x.rows + kBK - 1) / kBK;
+      const int left = x.rows % kBK;
+      if (left % 16 == 0) continue;
+      const int stage = (int)((fills - 1) % V::kStages);
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c.tail[stage], tails >> stage & 1, kWaitBudget,
+                                                     g.err, abort)))
+        break;
+      tails ^= 1u << stage;
+      zero_rows(smem + stage * S::kStage, left, 2 + (x.n / S::kCtas + 63) / 64, lane);
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&c.fixed[stage]), 0));
+    }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
-    int local = 0;
-    for (int64_t t = blockIdx.x; t < w.tiles; t += gridDim.x) {
-      const WgradTile x = wgrad_tile(g, w, t, off);
+    float4* stage =
+        reinterpret_cast<float4*>(smem + V::kStages * S::kStage + (warp - 4) * kWgradStaging);
+    int use = 0;
+    bool ok = true;
+    for (int64_t t = unit; t < w.tiles && ok; t += units) {
+      const WgradTile x = wgrad_tile<V>(g, w, t, bad);
       if (x.rows == 0 && g.accumulate) continue;
-      const int ab = local & 1;
-      if (x.rows > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c.acc_full[ab], (local >> 1) & 1,
-                                                       kWaitBudget, g.err, abort)))
-          break;
-        ++local;
-        tc_fence_after();
+      float sum[S::kBlocks][32];
+      if (x.rows == 0)
+#pragma unroll
+        for (int i = 0; i < S::kBlocks; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sum[i][k] = 0.f;
+      for (int r = 0; r < x.rows; r += kSegment * kBK, ++use) {
+        ok = wait_acc(c, use, g.err);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < S::kBlocks; ++i)
+          if ((2 * i + half) * 32 < x.n)
+            add_acc(tmem, use & 1, q, (2 * i + half) * 32, r == 0, sum[i]);
+        release_acc<V::kPair>(c, use & 1, rank, lane);
       }
-      const int i = x.i0 + 32 * q + lane;
-      float* row = g.dw + x.expert * g.dw_stride + (int64_t)i * g.lddw + x.j0;
-      for (int b = half; b * 32 < x.n; b += 2) {
-        uint32_t v[32];
-        if (x.rows > 0) {
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kAccCols + 32 * b),
-                             v);
-          tmem_ld_wait();
-        } else {
+      if (!ok) break;
+      const int row = x.i0 + kBM * (int)rank + 32 * q;
+      float* dw = g.dw + x.expert * g.dw_stride + (int64_t)row * g.lddw + x.j0;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0u;
-        }
-        if (i >= g.m) continue;
-        float* dst = row + 32 * b;
-        if (b * 32 + 32 <= x.cols && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
-          float4 o[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            o[k] = g.accumulate ? __ldcs(reinterpret_cast<const float4*>(dst) + k)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            o[k].x += __uint_as_float(v[4 * k]);
-            o[k].y += __uint_as_float(v[4 * k + 1]);
-            o[k].z += __uint_as_float(v[4 * k + 2]);
-            o[k].w += __uint_as_float(v[4 * k + 3]);
-            __stcs(reinterpret_cast<float4*>(dst) + k, o[k]);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (b * 32 + k < x.cols)
-              dst[k] = g.accumulate ? dst[k] + __uint_as_float(v[k]) : __uint_as_float(v[k]);
-        }
-      }
-      if (x.rows > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.acc_empty[ab]);
+      for (int i = 0; i < S::kBlocks; ++i) {
+        const int col = (2 * i + half) * 32;
+        if (col < x.cols && row < g.m)
+          wgrad_store(g, dw + col, g.m - row, x.cols - col, lane, sum[i], stage);
       }
     }
   }
-  teardown(c, warp);
+  teardown<V::kPair>(c, warp);
 }
 
 // ---------------------------------------------------------------------------- operand copies
@@ -629,10 +926,11 @@ cudaError_t encode(CUtensorMap* map, const Operand& o, int32_t dtype, bool batch
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Launches a persistent kernel; its shared-memory size is set once per device.
+// Launches a persistent kernel of `ctas`-CTA units; its shared-memory size is set once per
+// device.
 template <typename P>
-cudaError_t launch(void (*kernel)(P), const P& p, int grid, int smem, std::atomic<uint64_t>* ready,
-                   cudaStream_t st) {
+cudaError_t launch(void (*kernel)(P), const P& p, int64_t tiles, int ctas, int sms, int smem,
+                   std::atomic<uint64_t>* ready, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -641,20 +939,23 @@ cudaError_t launch(void (*kernel)(P), const P& p, int grid, int smem, std::atomi
     if (e != cudaSuccess) return e;
     ready->fetch_or(1ull << dev, std::memory_order_release);
   }
-  kernel<<<grid, kThreads, smem, st>>>(p);
+  const int64_t most = sms / ctas, units = tiles < 1 ? 1 : tiles < most ? tiles : most;
+  kernel<<<(unsigned)(units * ctas), kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-int grid_for(int64_t tiles, int sms) { return (int)(tiles < 1 ? 1 : tiles < sms ? tiles : sms); }
+// At least as many tiles as the offsets can make of the rows.
+template <typename V>
+int64_t mm_tiles(const GroupedMm& g) {
+  return (g.rows / V::kMaxN + (g.rows < g.n_experts ? g.rows : g.n_experts)) *
+         ((g.n - 1) / Shape<V>::kM + 1);
+}
 
 template <typename V, typename O>
 cudaError_t launch_mm(const MmParams& p, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  const GroupedMm& g = p.g;
-  const int64_t row_tiles = g.rows / V::kMaxN + (g.rows < g.n_experts ? g.rows : g.n_experts);
-  const int64_t tiles = row_tiles * ((g.n - 1) / kBM + 1);
-  const int smem = V::kStages * (kABytes + V::kMaxN * 128) + kEpiWarps * kStagingBytes + 1024;
-  return launch(grouped_mm_kernel<V, O>, p, grid_for(tiles, sms), smem, &ready, st);
+  return launch(grouped_mm_kernel<V, O>, p, mm_tiles<V>(p.g), Shape<V>::kCtas, sms,
+                V::kStages * Shape<V>::kStage + kEpiWarps * kMmStaging + 1024, &ready, st);
 }
 
 template <typename V>
@@ -662,6 +963,13 @@ cudaError_t launch_mm_as(const MmParams& p, int sms, cudaStream_t st) {
   return p.g.out_dtype == kF32 ? launch_mm<V, float>(p, sms, st)
          : p.g.out_dtype == kBf16 ? launch_mm<V, __nv_bfloat16>(p, sms, st)
                                   : launch_mm<V, __half>(p, sms, st);
+}
+
+template <typename V>
+cudaError_t launch_wgrad(const WgradParams& p, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  return launch(grouped_wgrad_kernel<V>, p, wgrad_grid<V>(p.g).tiles, Shape<V>::kCtas, sms,
+                V::kStages * Shape<V>::kStage + kEpiWarps * kWgradStaging + 1024, &ready, st);
 }
 
 Operand x_of(const GroupedMm& g) { return {g.x, g.rows, g.k, g.ldx, 1, 0}; }
@@ -690,15 +998,16 @@ cudaError_t launch_grouped_mm(const GroupedMm& g, void* workspace, int sms, cuda
   if (e == cudaSuccess) e = align_operand(&w, &at, sms, st);
   // Few rows per expert: streaming the weights is the whole cost.
   const bool narrow = g.rows <= 64 || g.rows <= 32 * (int64_t)g.n_experts;
+  const bool pair = !narrow && g.n > kBM && mm_tiles<Pair>(g) >= sms / 2;
   if (e == cudaSuccess)
     e = encode(&p.x, x, g.dtype, false, narrow ? Narrow::kBoxRows : Wide::kBoxRows);
   if (e == cudaSuccess) e = encode(&p.w, w, g.dtype, true, g.trans ? kBM : 64);
   if (e != cudaSuccess) return e;
-  return narrow ? launch_mm_as<Narrow>(p, sms, st) : launch_mm_as<Wide>(p, sms, st);
+  return narrow ? launch_mm_as<Narrow>(p, sms, st)
+         : pair ? launch_mm_as<Pair>(p, sms, st) : launch_mm_as<Wide>(p, sms, st);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms, cudaStream_t st) {
-  static std::atomic<uint64_t> ready{0};
   WgradParams p;
   p.g = g;
   Operand a = a_of(g), b = b_of(g);
@@ -711,8 +1020,8 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
     if (e == cudaSuccess) e = encode(&p.b, b, g.dtype, false, 64);
   }
   if (e != cudaSuccess) return e;
-  return launch(grouped_wgrad_kernel, p, grid_for(wgrad_grid(g).tiles, sms),
-                kWgradStages * kWgradStage + 1024, &ready, st);
+  const bool pair = g.m > kBM && wgrad_grid<Pair>(g).tiles >= sms / 2;
+  return pair ? launch_wgrad<Pair>(p, sms, st) : launch_wgrad<Wide>(p, sms, st);
 }
 
 }  // namespace muon

@@ -127,6 +127,17 @@ def test_mm_strides_and_starts(capi, start, wstart, extra, trans):
               pitch=(k + extra, (k if trans else n) + extra), start=start, wstart=wstart)
 
 
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp32"), ("bf16", "fp32")])
+@pytest.mark.parametrize("sizes,k,n", [
+    ([300, 0, 33, 31, 512, 129], 200, 2312),
+    ([1, 2, 95, 96, 97, 256, 257, 600], 1608, 1416),   # several segments of an fp32 sum
+    ([5000], 72, 1160),
+])
+def test_mm_enough_tiles_for_pairs(capi, sizes, k, n, trans, dtype, out):
+    _check_mm(capi, sizes, k, n, trans, dtype, out, first=2, tail=5)
+
+
 def test_mm_many_experts(capi):
     sizes = [(i * 7) % 5 for i in range(1024)]
     _check_mm(capi, sizes, 64, 64, False, "bf16", "bf16")
@@ -211,6 +222,17 @@ def _check_wgrad(capi, sizes, m, n, dtype, accumulate, first=0, tail=0, pitch=No
 ])
 def test_wgrad(capi, sizes, m, n, dtype, accumulate):
     _check_wgrad(capi, sizes, m, n, dtype, accumulate)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("sizes,m,n", [
+    ([1, 15, 16, 17, 63, 64, 65], 776, 520),
+    ([0, 3, 5, 0, 33, 47, 1, 2000], 264, 1416),
+    ([511, 512, 513, 1030, 1], 512, 2000),     # segments of the sum
+])
+def test_wgrad_enough_tiles_for_pairs(capi, sizes, m, n, accumulate):
+    _check_wgrad(capi, sizes, m, n, "bf16", accumulate, first=3, tail=7)
+    _check_wgrad(capi, sizes, m, n, "fp16", accumulate, first=3, tail=7, dstart=3)
 
 
 @pytest.mark.parametrize("m,n", [(1, 1), (3, 5), (130, 520), (129, 257), (517, 63)])
