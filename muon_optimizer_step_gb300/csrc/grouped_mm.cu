@@ -107,35 +107,40 @@ struct Control {
   int abort;
 };
 
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, int x, int y, int z,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const void* tmap, int x, int y,
-                                                 int z, uint32_t bar_cluster_addr) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar_cluster_addr)
-      : "memory");
-}
-
-// Loads that signal `bar` of this CTA (single) or of the pair's first CTA.
+// Loads of one box to shared address dst, signalling the barrier at `bar`: of this CTA
+// (kPair false), or of either CTA of the pair (a shared::cluster address).
 template <bool kPair>
-__device__ __forceinline__ void load_2d(void* dst, const void* tmap, int x, int y, uint64_t* bar) {
-  if constexpr (kPair) tma_load_2d_pair(smem_u32(dst), tmap, x, y, mapa_shared(smem_u32(bar), 0));
-  else tma_load_2d(dst, tmap, x, y, bar);
+__device__ __forceinline__ void load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 template <bool kPair>
-__device__ __forceinline__ void load_3d(void* dst, const void* tmap, int x, int y, int z,
-                                        uint64_t* bar) {
-  if constexpr (kPair) tma_load_3d_pair(smem_u32(dst), tmap, x, y, z, mapa_shared(smem_u32(bar), 0));
-  else tma_load_3d(dst, tmap, x, y, z, bar);
+__device__ __forceinline__ void load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
+                                        uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Arrives on an own barrier (given by its shared address), which then expects `bytes`.
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
 }
 
 // Operand descriptors as two words (see smem_desc_sw128): the low one moves with the address.
@@ -220,6 +225,20 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* err) 
       atomicExch(err, kErrTimeout);
       return;
     }
+}
+
+// Ends a producer: every copy it issued has landed (a pair's first CTA counts both CTAs') and,
+// unless the launch is giving up, every stage has been handed back.  The second waits for the
+// MMAs' arrivals on this CTA's own barriers, which come from the pair's first CTA: none may be
+// on its way when this CTA ends and its shared memory goes to the next one.
+template <typename V>
+__device__ __forceinline__ void drain_ring(Control& c, int64_t fills, uint32_t rank, int* err) {
+  for (int64_t f = fills - 1; f >= 0 && f >= fills - V::kStages; --f) {
+    const int stage = (int)(f % V::kStages);
+    const uint32_t phase = (uint32_t)((f / V::kStages) & 1);
+    if (rank == 0) drain(&c.full[stage], phase, err);
+    if (*reinterpret_cast<volatile int*>(&c.abort) == 0) drain(&c.empty[stage], phase, err);
+  }
 }
 
 // Position in the ring of operand stages.
@@ -449,48 +468,48 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
   __syncthreads();
   sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
-  volatile int* abort = &c.abort;
   const int f_tiles = (g.n - 1) / S::kM + 1, k_blocks = (g.k - 1) / kBK + 1;
   const int64_t tiles = (int64_t)first[g.n_experts] * f_tiles;
   const int64_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
 
   if (warp == 0) {
-    if (lane == 0) {
-      Ring<V::kStages> ring;
-      int64_t fills = 0;
-      bool ok = true;
-      for (int64_t t = unit; t < tiles && ok; t += units) {
-        const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
-        const int part = m.n / S::kCtas;  // rows of x this CTA brings
-        const int boxes = (part + V::kBoxRows - 1) / V::kBoxRows;
-        const uint32_t bytes = S::kCtas * (kABytes + boxes * V::kBoxRows * 128);
-        const int f = m.f0 + kBM * (int)rank, row = m.row + part * (int)rank;
-        for (int kb = 0; kb < k_blocks; ++kb, ++fills) {
-          uint64_t* full = &c.full[ring.stage];
-          if (!mbar_wait_bounded(&c.empty[ring.stage], ring.phase ^ 1u, kWaitBudget, g.err, abort)) {
-            ok = false;
-            break;
-          }
+    Ring<V::kStages> ring;
+    int64_t fills = 0;
+    bool ok = true;
+    const uint32_t full0 = smem_u32(c.full), dst0 = smem_u32(smem);
+    // A pair's second CTA signals the first one's barriers.
+    const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
+    for (int64_t t = unit; t < tiles && ok; t += units) {
+      const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
+      const int part = m.n / S::kCtas;  // rows of x this CTA brings
+      const int boxes = (part + V::kBoxRows - 1) / V::kBoxRows;
+      const uint32_t bytes = S::kCtas * (kABytes + boxes * V::kBoxRows * 128);
+      const int f = m.f0 + kBM * (int)rank, row = m.row + part * (int)rank;
+      for (int kb = 0; kb < k_blocks; ++kb, ++fills) {
+        ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
+        if (!ok) break;
+        const uint32_t sig = sig0 + 8 * ring.stage, a = dst0 + ring.stage * S::kStage;
+        const int k0 = kb * kBK;
+        if (elect_one()) {
           // Only the first CTA of a pair arrives, announcing both CTAs' bytes.
-          if (rank == 0) mbar_arrive_expect_tx(full, bytes);
-          uint8_t* sa = smem + ring.stage * S::kStage;
-          const int k0 = kb * kBK;
+          if (rank == 0) expect(full0 + 8 * ring.stage, bytes);
           if (g.trans) {
-            load_3d<V::kPair>(sa, &p.w, k0, f, m.expert, full);
+            load_3d<V::kPair>(a, &p.w, k0, f, m.expert, sig);
           } else {
-            load_3d<V::kPair>(sa, &p.w, f, k0, m.expert, full);
-            load_3d<V::kPair>(sa + kBox, &p.w, f + 64, k0, m.expert, full);
+            load_3d<V::kPair>(a, &p.w, f, k0, m.expert, sig);
+            load_3d<V::kPair>(a + kBox, &p.w, f + 64, k0, m.expert, sig);
           }
-          for (int b = 0; b < boxes; ++b)
-            load_2d<V::kPair>(sa + kABytes + b * V::kBoxRows * 128, &p.x, k0, row + b * V::kBoxRows,
-                              full);
-          ring.next();
+#pragma unroll
+          for (int b = 0; b < V::kMaxN / S::kCtas / V::kBoxRows; ++b)
+            if (b < boxes)
+              load_2d<V::kPair>(a + kABytes + b * V::kBoxRows * 128, &p.x, k0, row + b * V::kBoxRows,
+                                sig);
         }
+        __syncwarp();
+        ring.next();
       }
-      if (rank == 0)
-        for (int64_t f = fills - 1; f >= 0 && f >= fills - V::kStages; --f)
-          drain(&c.full[f % V::kStages], (uint32_t)((f / V::kStages) & 1), g.err);
     }
+    if (elect_one()) drain_ring<V>(c, fills, rank, g.err);
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // The whole warp walks the k-blocks and one lane issues, so that descriptors and counters
@@ -689,49 +708,54 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
   if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(g.err, kErrRowOffsets);
   sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
-  volatile int* abort = &c.abort;
   const WgradGrid w = wgrad_grid<V>(g);
   const int64_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
 
   if (warp == 0) {
-    if (lane == 0) {
-      Ring<V::kStages> ring;
-      int64_t fills = 0;
-      uint32_t tails = 0, used = 0;  // per stage: parity of the next use of `tail`; any use
-      bool ok = true;
-      for (int64_t t = unit; t < w.tiles && ok; t += units) {
-        const WgradTile x = wgrad_tile<V>(g, w, t, bad);
-        const int part = x.n / S::kCtas, boxes = (part + 63) / 64;  // columns of b this CTA brings
-        const int i = x.i0 + kBM * (int)rank, j = x.j0 + part * (int)rank;
-        for (int r = 0; r < x.rows; r += kBK, ++fills) {
-          if (!mbar_wait_bounded(&c.empty[ring.stage], ring.phase ^ 1u, kWaitBudget, g.err, abort)) {
-            ok = false;
-            break;
+    Ring<V::kStages> ring;
+    int64_t fills = 0;
+    uint32_t tails = 0, used = 0;  // per stage: parity of the next use of `tail`; any use
+    bool ok = true;
+    const uint32_t full0 = smem_u32(c.full), tail0 = smem_u32(c.tail), dst0 = smem_u32(smem);
+    const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
+    for (int64_t t = unit; t < w.tiles && ok; t += units) {
+      const WgradTile x = wgrad_tile<V>(g, w, t, bad);
+      const int part = x.n / S::kCtas, boxes = (part + 63) / 64;  // columns of b this CTA brings
+      const int i = x.i0 + kBM * (int)rank, j = x.j0 + part * (int)rank;
+      for (int r = 0; r < x.rows; r += kBK, ++fills) {
+        ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
+        if (!ok) break;
+        const uint32_t a = dst0 + ring.stage * S::kStage;
+        const int y = x.row + r;
+        // A last k-block with rows to zero lands on each CTA's own barrier.
+        const bool own = V::kPair && x.rows - r < kBK && (x.rows - r) % 16 != 0;
+        if (own) {
+          const uint32_t bar = (rank == 0 ? full0 : tail0) + 8 * ring.stage;
+          if (elect_one()) {
+            expect(bar, (2 + boxes) * kBox);
+            for (int b = 0; b < 2; ++b) load_2d<false>(a + b * kBox, &p.a, i + 64 * b, y, bar);
+            for (int b = 0; b < boxes; ++b)
+              load_2d<false>(a + kABytes + b * kBox, &p.b, j + 64 * b, y, bar);
           }
-          // A last k-block with rows to zero lands on each CTA's own barrier.
-          const bool own = !V::kPair || (x.rows - r < kBK && (x.rows - r) % 16 != 0);
-          uint64_t* full = own && rank != 0 ? &c.tail[ring.stage] : &c.full[ring.stage];
-          if (own || rank == 0) mbar_arrive_expect_tx(full, (own ? 1 : 2) * (2 + boxes) * kBox);
-          uint8_t* sa = smem + ring.stage * S::kStage;
-          if (own && rank != 0) {
+          if (rank != 0) {
             tails ^= 1u << ring.stage;
             used |= 1u << ring.stage;
           }
-          if (own) {
-            for (int b = 0; b < 2; ++b) load_2d<false>(sa + b * kBox, &p.a, i + 64 * b, x.row + r, full);
-            for (int b = 0; b < boxes; ++b)
-              load_2d<false>(sa + kABytes + b * kBox, &p.b, j + 64 * b, x.row + r, full);
-          } else {
-            for (int b = 0; b < 2; ++b) load_2d<true>(sa + b * kBox, &p.a, i + 64 * b, x.row + r, full);
-            for (int b = 0; b < boxes; ++b)
-              load_2d<true>(sa + kABytes + b * kBox, &p.b, j + 64 * b, x.row + r, full);
-          }
-          ring.next();
+        } else if (elect_one()) {
+          const uint32_t sig = sig0 + 8 * ring.stage;
+          if (rank == 0) expect(full0 + 8 * ring.stage, S::kCtas * (2 + boxes) * kBox);
+          load_2d<V::kPair>(a, &p.a, i, y, sig);
+          load_2d<V::kPair>(a + kBox, &p.a, i + 64, y, sig);
+#pragma unroll
+          for (int b = 0; b < V::kMaxN / S::kCtas / 64; ++b)
+            if (b < boxes) load_2d<V::kPair>(a + kABytes + b * kBox, &p.b, j + 64 * b, y, sig);
         }
+        __syncwarp();
+        ring.next();
       }
-      if (rank == 0)
-        for (int64_t f = fills - 1; f >= 0 && f >= fills - V::kStages; --f)
-          drain(&c.full[f % V::kStages], (uint32_t)((f / V::kStages) & 1), g.err);
+    }
+    if (elect_one()) {
+      drain_ring<V>(c, fills, rank, g.err);
       for (int s = 0; s < V::kStages; ++s)
         if (used >> s & 1) drain(&c.tail[s], (tails >> s & 1) ^ 1u, g.err);
     }
@@ -801,7 +825,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
       if (left % 16 == 0) continue;
       const int stage = (int)((fills - 1) % V::kStages);
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c.tail[stage], tails >> stage & 1, kWaitBudget,
-                                                     g.err, abort)))
+                                                     g.err, &c.abort)))
         break;
       tails ^= 1u << stage;
       zero_rows(smem + stage * S::kStage, left, 2 + (x.n / S::kCtas + 63) / 64, lane);
