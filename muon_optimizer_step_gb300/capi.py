@@ -52,13 +52,6 @@ class GroupHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("wd", ctypes.c_float), ("mu", ctypes.c_float),
                 ("nesterov", ctypes.c_int32)]
 
-
-class Tensor(ctypes.Structure):
-    """muon_tensor: numel consecutive elements on the device."""
-    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64),
-                ("dtype", ctypes.c_int32), ("pad_", ctypes.c_int32)]
-
-
 _SZ = ctypes.c_size_t
 
 SIGNATURES = [
@@ -283,9 +276,9 @@ def muon_step_scaled(flat_params, flat_grads, flat_momentum, layout, workspace, 
     """muon_step_grouped with the gradients multiplied by grad_scale, a CUDA tensor of one
     float32 (norm[1:] of muon_grad_norm: the step then clips by the global norm)."""
     if not isinstance(grad_scale, int):
-        _device_tensor(grad_scale, "grad_scale", ("float32",))
-        if grad_scale.numel() < 1:
-            raise ValueError("grad_scale is empty")
+        if not grad_scale.is_cuda or grad_scale.numel() < 1 \
+                or _kind(grad_scale, "grad_scale") != MUON_DTYPE_F32:
+            raise ValueError("grad_scale: must be a float32 value on the GPU")
     arr = (GroupHparams * max(1, len(groups)))(
         *[GroupHparams(float(lr), float(wd), float(mu), 1 if nest else 0)
           for lr, wd, mu, nest in groups])
@@ -400,64 +393,95 @@ def muon_export_update(layout, workspace, ns_steps, full_out, stream=None):
 
 
 # ------------------------------------------------------------------ expert layers
-_DTYPES = {}
+# These calls are short, so their checks are: one look at each tensor's attributes, and torch's
+# stream handle instead of a stream object.
+_KINDS = {}   # torch dtype -> muon_dtype
 
 
-def _dtype_code(t, name, kinds=("float32", "bfloat16", "float16")):
-    """The muon_dtype of tensor t, one of `kinds`."""
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: (MUON_DTYPE_F32, "float32"),
-                        torch.bfloat16: (MUON_DTYPE_BF16, "bfloat16"),
-                        torch.float16: (MUON_DTYPE_F16, "float16")})
-    code = _DTYPES.get(t.dtype)
-    if code is None or code[1] not in kinds:
-        raise ValueError(f"{name}: type {t.dtype}; one of {', '.join(kinds)} is needed")
-    return code[0]
+def _kinds():
+    import torch
+    _KINDS.update({torch.float32: MUON_DTYPE_F32, torch.bfloat16: MUON_DTYPE_BF16,
+                   torch.float16: MUON_DTYPE_F16})
+    return _KINDS
 
 
-def _device_tensor(t, name, kinds, shape=None):
-    """Checks t's place, shape and unit inner stride; returns its muon_dtype."""
+def _kind(t, name):
+    """t's muon_dtype."""
+    k = _KINDS.get(t.dtype)
+    if k is None:
+        k = _kinds().get(t.dtype)
+        if k is None:
+            raise ValueError(f"{name}: type {t.dtype}; float32, bfloat16 or float16 is needed")
+    return k
+
+
+def _matrix(t, name, shape=None):
+    """(pointer, row pitch, muon_dtype) of a 2-D CUDA tensor with contiguous rows.  Strides of
+    dimensions of length 1 mean nothing."""
+    size = t.shape
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dim() > 0 and t.stride(-1) != 1 and t.shape[-1] > 1:
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{name}: shape {tuple(size)}, expected "
+                         f"{'two dimensions' if shape is None else tuple(shape)}")
+    pitch, step = t.stride()
+    if step != 1 and size[1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _dtype_code(t, name, kinds)
+    return t.data_ptr(), pitch if size[0] > 1 else max(size[1], 1), _kind(t, name)
 
 
-def _pitch(t):
-    """Row pitch of a 2-D tensor (strides of dimensions of length 1 mean nothing)."""
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.shape[-1], 1)
+def _matrices(t, name):
+    """(pointer, pitch, distance between matrices, muon_dtype) of a 3-D CUDA tensor."""
+    size = t.shape
+    if not t.is_cuda or len(size) != 3:
+        raise ValueError(f"{name}: must be a CUDA tensor of three dimensions")
+    apart, pitch, step = t.stride()
+    if step != 1 and size[2] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return (t.data_ptr(), pitch if size[1] > 1 else max(size[2], 1),
+            apart if size[0] > 1 else max(size[1] * size[2], 1), _kind(t, name))
 
 
-def _step_of(t):
-    """Distance between the matrices of a 3-D tensor."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1] * t.shape[2], 1)
+def _row_floats(t, rows, name):
+    """Pointer of a contiguous float32 CUDA vector of `rows` elements (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.shape != (rows,) or not t.is_contiguous() \
+            or _kind(t, name) != MUON_DTYPE_F32:
+        raise ValueError(f"{name}: must be {rows} contiguous float32 values on the GPU")
+    return t.data_ptr()
 
 
 def _offsets(t, n_experts):
     import torch
-    if not t.is_cuda or t.dtype != torch.int64 or t.dim() != 1 or not t.is_contiguous() \
-            or t.shape[0] != n_experts + 1:
+    if not t.is_cuda or t.dtype != torch.int64 or t.shape != (n_experts + 1,) \
+            or not t.is_contiguous():
         raise ValueError(f"offsets: must be {n_experts + 1} contiguous int64 values on the GPU")
+    return t.data_ptr()
 
 
-_16BIT = ("bfloat16", "float16")
+def _stream_of(stream, like):
+    """The handle of `stream`, or of the current stream of like's device."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _workspace(workspace, nbytes, like, stream):
-    """The caller's workspace, or one from torch's allocator, kept from reuse until the work
-    enqueued on `stream` is done with it."""
-    if workspace is not None or nbytes == 0:
-        return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _workspace(workspace, nbytes, align, like, stream):
+    """(pointer, bytes, owner) of the caller's workspace, or of one from torch's allocator, which
+    is kept from reuse until the work enqueued on `stream` is done with it."""
+    if workspace is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if nbytes == 0:
+        return None, 0, None
     import torch
-    raw = torch.empty(nbytes + WORKSPACE_ALIGN, dtype=torch.uint8, device=like.device)
+    raw = torch.empty(nbytes + align, dtype=torch.uint8, device=like.device)
     if stream is not None:
         raw.record_stream(stream if not isinstance(stream, int)
                           else torch.cuda.ExternalStream(stream, device=like.device))
-    return raw[(-raw.data_ptr()) % WORKSPACE_ALIGN:][:nbytes], nbytes
+    at = raw.data_ptr()
+    return at + (-at) % align, nbytes, raw
 
 
 def muon_grouped_mm(x, w, offsets, y, trans_w=False, workspace=None, stream=None):
@@ -468,29 +492,27 @@ def muon_grouped_mm(x, w, offsets, y, trans_w=False, workspace=None, stream=None
     (rows, n) is of their type or float32, offsets holds experts + 1 int64 values on the GPU.
     Any strides with a contiguous last dimension; operands whose rows do not start on 16 bytes
     are copied to the workspace first (allocated when None is given)."""
+    wp, ldw, apart, dtype = _matrices(w, "w")
     e, k, n = w.shape
     if trans_w:
         k, n = n, k
     rows = x.shape[0]
-    dtype = _device_tensor(x, "x", _16BIT, (rows, k))
-    if _device_tensor(w, "w", _16BIT) != dtype:
-        raise ValueError("x and w must have the same type")
-    out = _device_tensor(y, "y", ("float32",) + _16BIT, (rows, n))
-    if out not in (dtype, MUON_DTYPE_F32):
-        raise ValueError("y must have x's type or be float32")
-    _offsets(offsets, e)
-    xp, wp, ldx, ldw, ws = x.data_ptr(), w.data_ptr(), _pitch(x), _pitch(w), _step_of(w)
+    xp, ldx, xkind = _matrix(x, "x", (rows, k))
+    yp, ldy, out = _matrix(y, "y", (rows, n))
+    if xkind != dtype or dtype == MUON_DTYPE_F32 or out not in (dtype, MUON_DTYPE_F32):
+        raise ValueError("x and w must both be bfloat16 or both float16, y of their type or float32")
     nbytes = 0
-    if (xp | wp) & 15 or (ldx | ldw | ws) & 7:
+    if (xp | wp) & 15 or (ldx | ldw | apart) & 7:
         need = _SZ()
-        _check(lib.muon_grouped_mm_workspace_bytes(xp, ldx, wp, ldw, ws, rows, e, k, n,
+        _check(lib.muon_grouped_mm_workspace_bytes(xp, ldx, wp, ldw, apart, rows, e, k, n,
                                                    1 if trans_w else 0, ctypes.byref(need)),
                "muon_grouped_mm_workspace_bytes")
         nbytes = need.value
-    workspace, nbytes = _workspace(workspace, nbytes, x, stream)
-    _check(lib.muon_grouped_mm(xp, ldx, wp, ldw, ws, offsets.data_ptr(), y.data_ptr(), _pitch(y),
-                               rows, e, k, n, 1 if trans_w else 0, dtype, out, _ptr(workspace),
-                               nbytes, _stream_handle(stream)), "muon_grouped_mm")
+    ws, nbytes, owner = _workspace(workspace, nbytes, WORKSPACE_ALIGN, x, stream)
+    st = lib.muon_grouped_mm(xp, ldx, wp, ldw, apart, _offsets(offsets, e), yp, ldy, rows, e, k, n,
+                             1 if trans_w else 0, dtype, out, ws, nbytes, _stream_of(stream, x))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_grouped_mm")
 
 
 def muon_grouped_wgrad(a, b, offsets, dw, accumulate=False, workspace=None, stream=None):
@@ -498,14 +520,13 @@ def muon_grouped_wgrad(a, b, offsets, dw, accumulate=False, workspace=None, stre
     dw[e] += that.  a (rows, m) and b (rows, n) are bfloat16 or float16; dw (experts, m, n) is
     float32 with any strides of its first two dimensions, e.g. a view of the flat gradient
     buffer."""
+    dp, lddw, apart, out = _matrices(dw, "dw")
     e, m, n = dw.shape
     rows = a.shape[0]
-    dtype = _device_tensor(a, "a", _16BIT, (rows, m))
-    if _device_tensor(b, "b", _16BIT, (rows, n)) != dtype:
-        raise ValueError("a and b must have the same type")
-    _device_tensor(dw, "dw", ("float32",))
-    _offsets(offsets, e)
-    ap, bp, lda, ldb = a.data_ptr(), b.data_ptr(), _pitch(a), _pitch(b)
+    ap, lda, dtype = _matrix(a, "a", (rows, m))
+    bp, ldb, bkind = _matrix(b, "b", (rows, n))
+    if bkind != dtype or dtype == MUON_DTYPE_F32 or out != MUON_DTYPE_F32:
+        raise ValueError("a and b must both be bfloat16 or both float16, and dw float32")
     nbytes = 0
     if (ap | bp) & 15 or (lda | ldb) & 7:
         need = _SZ()
@@ -513,77 +534,79 @@ def muon_grouped_wgrad(a, b, offsets, dw, accumulate=False, workspace=None, stre
                                                       ctypes.byref(need)),
                "muon_grouped_wgrad_workspace_bytes")
         nbytes = need.value
-    workspace, nbytes = _workspace(workspace, nbytes, a, stream)
-    _check(lib.muon_grouped_wgrad(ap, lda, bp, ldb, offsets.data_ptr(), dw.data_ptr(), _pitch(dw),
-                                  _step_of(dw), rows, e, m, n, 1 if accumulate else 0, dtype,
-                                  _ptr(workspace), nbytes, _stream_handle(stream)),
-           "muon_grouped_wgrad")
-
-
-_ANY = ("float32",) + _16BIT
-
-
-def _row_weight(t, rows, name):
-    if t is None:
-        return None
-    _device_tensor(t, name, ("float32",), (rows,))
-    return t.data_ptr()
+    ws, nbytes, owner = _workspace(workspace, nbytes, WORKSPACE_ALIGN, a, stream)
+    st = lib.muon_grouped_wgrad(ap, lda, bp, ldb, _offsets(offsets, e), dp, lddw, apart, rows, e, m,
+                                n, 1 if accumulate else 0, dtype, ws, nbytes, _stream_of(stream, a))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_grouped_wgrad")
 
 
 def muon_swiglu(gate, up, out, row_weight=None, stream=None):
     """out = row_weight[:, None] * silu(gate) * up, row by row; all (rows, cols) of one type."""
-    dtype = _device_tensor(gate, "gate", _ANY)
-    for t, name in ((up, "up"), (out, "out")):
-        if _device_tensor(t, name, _ANY, gate.shape) != dtype:
-            raise ValueError(f"{name} must have gate's type")
-    rows, cols = gate.shape
-    _check(lib.muon_swiglu(gate.data_ptr(), _pitch(gate), up.data_ptr(), _pitch(up),
-                           _row_weight(row_weight, rows, "row_weight"), out.data_ptr(),
-                           _pitch(out), rows, cols, dtype, _stream_handle(stream)), "muon_swiglu")
+    g, ldg, dtype = _matrix(gate, "gate")
+    shape = gate.shape
+    u, ldu, ukind = _matrix(up, "up", shape)
+    o, ldo, okind = _matrix(out, "out", shape)
+    if ukind != dtype or okind != dtype:
+        raise ValueError("gate, up and out must have the same type")
+    st = lib.muon_swiglu(g, ldg, u, ldu, _row_floats(row_weight, shape[0], "row_weight"), o, ldo,
+                         shape[0], shape[1], dtype, _stream_of(stream, gate))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_swiglu")
 
 
 def muon_swiglu_grad(dout, gate, up, dgate, dup, row_weight=None, d_row_weight=None, stream=None):
     """The gradient of muon_swiglu: writes dgate, dup and, where given, d_row_weight."""
-    dtype = _device_tensor(gate, "gate", _ANY)
-    for t, name in ((dout, "dout"), (up, "up"), (dgate, "dgate"), (dup, "dup")):
-        if _device_tensor(t, name, _ANY, gate.shape) != dtype:
-            raise ValueError(f"{name} must have gate's type")
-    rows, cols = gate.shape
-    _check(lib.muon_swiglu_grad(dout.data_ptr(), _pitch(dout), gate.data_ptr(), _pitch(gate),
-                                up.data_ptr(), _pitch(up),
-                                _row_weight(row_weight, rows, "row_weight"), dgate.data_ptr(),
-                                _pitch(dgate), dup.data_ptr(), _pitch(dup),
-                                _row_weight(d_row_weight, rows, "d_row_weight"), rows, cols, dtype,
-                                _stream_handle(stream)), "muon_swiglu_grad")
+    g, ldg, dtype = _matrix(gate, "gate")
+    shape = gate.shape
+    d, ldd, dkind = _matrix(dout, "dout", shape)
+    u, ldu, ukind = _matrix(up, "up", shape)
+    dg, lddg, dgkind = _matrix(dgate, "dgate", shape)
+    du, lddu, dukind = _matrix(dup, "dup", shape)
+    if not dtype == dkind == ukind == dgkind == dukind:
+        raise ValueError("dout, gate, up, dgate and dup must have the same type")
+    st = lib.muon_swiglu_grad(d, ldd, g, ldg, u, ldu,
+                              _row_floats(row_weight, shape[0], "row_weight"), dg, lddg, du, lddu,
+                              _row_floats(d_row_weight, shape[0], "d_row_weight"), shape[0],
+                              shape[1], dtype, _stream_of(stream, gate))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_swiglu_grad")
 
 
 # ------------------------------------------------------------------ gradient norm, clipping
 def _tensor_list(tensors, name):
-    """A host array of muon_tensor from contiguous CUDA tensors."""
-    arr = (Tensor * max(1, len(tensors)))()
-    for r, t in zip(arr, tensors):
+    """A host array of muon_tensor (pointer, length, type as three 64-bit words; the machine is
+    little-endian) from contiguous CUDA tensors."""
+    flat = []
+    for t in tensors:
+        k = _KINDS.get(t.dtype)
+        if k is None:
+            k = _kind(t, name)
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous CUDA tensors")
-        r.data, r.numel, r.dtype = t.data_ptr(), t.numel(), _dtype_code(t, name)
-    return arr
+        flat += (t.data_ptr(), t.numel(), k)
+    return (ctypes.c_uint64 * max(3, len(flat)))(*flat)
 
 
-def _norm_call(grads, norm, workspace, stream):
-    _device_tensor(norm, "norm", ("float32",), (2,))
+def _clip_call(grads, norm, workspace, stream):
+    """(host array of grads, norm's pointer, workspace pointer, bytes and owner, stream)."""
+    np = _row_floats(norm, 2, "norm")
     g = _tensor_list(grads, "grads")
-    need = _SZ()
-    _check(lib.muon_clip_workspace_bytes(g, len(grads), ctypes.byref(need)),
-           "muon_clip_workspace_bytes")
-    workspace, nbytes = _workspace(workspace, need.value, norm, stream)
-    return g, workspace, nbytes
+    nbytes = 0
+    if workspace is None:
+        need = _SZ()
+        _check(lib.muon_clip_workspace_bytes(g, len(grads), ctypes.byref(need)),
+               "muon_clip_workspace_bytes")
+        nbytes = need.value
+    ws, nbytes, owner = _workspace(workspace, nbytes, 8, norm, stream)
+    return g, np, ws, nbytes, owner, _stream_of(stream, norm)
 
 
 def muon_grad_norm(grads, max_norm, norm, workspace=None, stream=None):
     """norm[0] = the 2-norm of all gradients together, norm[1] = min(1, max_norm / (norm[0] +
     1e-6)).  grads: a sequence of contiguous CUDA tensors; norm: 2 float32 on the GPU."""
-    g, workspace, nbytes = _norm_call(grads, norm, workspace, stream)
-    _check(lib.muon_grad_norm(g, len(grads), float(max_norm), norm.data_ptr(), _ptr(workspace),
-                              nbytes, _stream_handle(stream)), "muon_grad_norm")
+    g, np, ws, nbytes, owner, st = _clip_call(grads, norm, workspace, stream)
+    _check(lib.muon_grad_norm(g, len(grads), max_norm, np, ws, nbytes, st), "muon_grad_norm")
 
 
 def muon_clip_grads(grads, outs, max_norm, norm, workspace=None, stream=None):
@@ -591,10 +614,9 @@ def muon_clip_grads(grads, outs, max_norm, norm, workspace=None, stream=None):
     of its length and of its type or float32."""
     if len(outs) != len(grads):
         raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
-    g, workspace, nbytes = _norm_call(grads, norm, workspace, stream)
-    _check(lib.muon_clip_grads(g, _tensor_list(outs, "outs"), len(grads), float(max_norm),
-                               norm.data_ptr(), _ptr(workspace), nbytes, _stream_handle(stream)),
-           "muon_clip_grads")
+    o = _tensor_list(outs, "outs")
+    g, np, ws, nbytes, owner, st = _clip_call(grads, norm, workspace, stream)
+    _check(lib.muon_clip_grads(g, o, len(grads), max_norm, np, ws, nbytes, st), "muon_clip_grads")
 
 
 def layout_grads(layout, flat_grads):

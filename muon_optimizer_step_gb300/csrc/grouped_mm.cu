@@ -407,15 +407,22 @@ __device__ __forceinline__ MmTile mm_tile(int64_t t, int f_tiles, int n_experts,
     const int mid = (lo + hi) >> 1;
     if (first[mid + 1] > rt) hi = mid; else lo = mid + 1;
   }
+  // Within the expert: groups of kGroup row tiles, in each every column tile of y, in each the
+  // group's row tiles.  The CTAs at work at a time then share a few column tiles of the weight
+  // and a group's rows, and the weight comes from HBM once per group.
+  constexpr int kGroup = 8;
+  const int rows = off[lo + 1] - off[lo], tiles = first[lo + 1] - first[lo];
+  const int64_t in = t - (int64_t)first[lo] * f_tiles;
+  const int group = (int)(in / ((int64_t)kGroup * f_tiles)) * kGroup;
+  const int size = min(kGroup, tiles - group), rest = (int)(in - (int64_t)group * f_tiles);
+  const int width = ((rows + tiles - 1) / tiles + kStep - 1) / kStep * kStep;
+  const int begin = (group + rest % size) * width;
   MmTile m;
   m.expert = lo;
-  const int rows = off[lo + 1] - off[lo], tiles = first[lo + 1] - first[lo];
-  const int width = ((rows + tiles - 1) / tiles + kStep - 1) / kStep * kStep;
-  const int begin = (rt - first[lo]) * width;
   m.row = off[lo] + begin;
   m.rows = min(width, rows - begin);
   m.n = (m.rows + kStep - 1) / kStep * kStep;
-  m.f0 = (int)(t % f_tiles) * Shape<V>::kM;
+  m.f0 = rest / size * Shape<V>::kM;
   return m;
 }
 
