@@ -55,7 +55,7 @@ constexpr int kBK = 64;             // k-block: 128 bytes of a 16-bit row
 constexpr int kABytes = kBM * 128;  // 16 KB
 constexpr int kBox = 64 * 128;      // an MN-major box: 64 k-rows of 128 bytes
 constexpr int kAccCols = 256;       // TMEM columns of one accumulator
-constexpr int kSegment = 8;         // k-blocks per segment of an fp32 result
+constexpr int kSegment = 12;        // most k-blocks per segment of an fp32 result
 constexpr int kMaxStages = 8;
 constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 
@@ -92,7 +92,9 @@ struct MmParams {
 
 struct WgradParams {
   CUtensorMap a, b;  // (columns, rows): boxes of 64 x 64
+  CUtensorMap dw;    // (column, row, expert) of the result: boxes of 32 x 32
   GroupedWgrad g;
+  bool bulk;         // dw is written by TMA
 };
 
 // Barriers and flags of one CTA.
@@ -239,6 +241,12 @@ __device__ __forceinline__ void drain_ring(Control& c, int64_t fills, uint32_t r
     if (rank == 0) drain(&c.full[stage], phase, err);
     if (*reinterpret_cast<volatile int*>(&c.abort) == 0) drain(&c.empty[stage], phase, err);
   }
+}
+
+// k-blocks of each of a sum's segments, of equal length up to the last one.
+__device__ __forceinline__ int segment(int k_blocks) {
+  const int n = (k_blocks + kSegment - 1) / kSegment;
+  return n > 1 ? (k_blocks + n - 1) / n : k_blocks;
 }
 
 // Position in the ring of operand stages.
@@ -475,7 +483,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
   __syncthreads();
   sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
-  const int f_tiles = (g.n - 1) / S::kM + 1, k_blocks = (g.k - 1) / kBK + 1;
+  const int f_tiles = (g.n - 1) / S::kM + 1, k_blocks = (g.k - 1) / kBK + 1, seg = segment(k_blocks);
   const int64_t tiles = (int64_t)first[g.n_experts] * f_tiles;
   const int64_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
 
@@ -532,7 +540,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, m.n, a_mn, 0);
       for (int kb = 0; kb < k_blocks;) {
         // One accumulator: all k-blocks, or a segment of them.
-        const int end = kFp32 ? min(k_blocks, kb + kSegment) : k_blocks;
+        const int end = kFp32 ? min(k_blocks, kb + seg) : k_blocks;
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
@@ -576,7 +584,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
       const int f = m.f0 + kBM * (int)rank + 32 * q;
       if constexpr (kFp32) {
         float sum[S::kBlocks][32];
-        for (int kb = 0; kb < k_blocks; kb += kSegment, ++use) {
+        for (int kb = 0; kb < k_blocks; kb += seg, ++use) {
           ok = wait_acc(c, use, g.err);
           if (!ok) break;
 #pragma unroll
@@ -613,6 +621,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
 
 // ---------------------------------------------------------------------------- wgrad
 constexpr int kWgradStaging = 4096;  // per epilogue warp: a block of 32 x 32 floats
+constexpr int kWgradStep = 32;       // tiles are whole blocks wide, but for the matrix's edge
 
 struct WgradTile {
   int expert, row, rows;  // the expert's rows
@@ -626,11 +635,10 @@ struct WgradGrid {
 
 template <typename V>
 __host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g) {
-  constexpr int kStep = Shape<V>::kStepN;
   WgradGrid w;
   w.m_tiles = (g.m - 1) / Shape<V>::kM + 1;
   w.n_tiles = (g.n - 1) / V::kMaxN + 1;
-  w.width = ((g.n - 1) / w.n_tiles + kStep) / kStep * kStep;  // columns dealt evenly
+  w.width = ((g.n - 1) / w.n_tiles + kWgradStep) / kWgradStep * kWgradStep;  // columns dealt evenly
   w.tiles = (int64_t)g.n_experts * w.m_tiles * w.n_tiles;
   return w;
 }
@@ -638,7 +646,6 @@ __host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g) 
 template <typename V>
 __device__ __forceinline__ WgradTile wgrad_tile(const GroupedWgrad& g, const WgradGrid& w, int64_t t,
                                                 bool bad) {
-  constexpr int kStep = Shape<V>::kStepN;
   const int64_t per = (int64_t)w.m_tiles * w.n_tiles;
   const int e = (int)(t / per);
   const int64_t r = t - e * per;
@@ -649,7 +656,7 @@ __device__ __forceinline__ WgradTile wgrad_tile(const GroupedWgrad& g, const Wgr
   x.i0 = (int)(r / w.n_tiles) * Shape<V>::kM;
   x.j0 = (int)(r % w.n_tiles) * w.width;
   x.cols = min(w.width, g.n - x.j0);
-  x.n = (x.cols + kStep - 1) / kStep * kStep;
+  x.n = (x.cols + kWgradStep - 1) / kWgradStep * kWgradStep;
   return x;
 }
 
@@ -693,6 +700,26 @@ __device__ __forceinline__ void wgrad_store(const GroupedWgrad& g, float* dw, in
     }
   }
   __syncwarp();
+}
+
+// The same block (=) by TMA, which drops what lies outside the matrix: the warp's only waits are
+// for the previous block to have left `stage`.  dw must start on 16 bytes in every row.
+__device__ __forceinline__ void wgrad_store_bulk(const CUtensorMap* map, int expert, int row, int col,
+                                                 int lane, const float (&v)[32], float4* stage) {
+  if (lane == 0) bulk_wait_read();
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k)  // the 128-byte swizzle of the map
+    stage[8 * lane + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+        "r"(col), "r"(row), "r"(expert), "r"(smem_u32(stage))
+        : "memory");
+    bulk_commit();
+  }
 }
 
 template <typename V>
@@ -777,13 +804,14 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     for (int64_t t = unit; t < w.tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, x.n, 1, 1);
+      const int seg = segment((x.rows + kBK - 1) / kBK);
       for (int left = x.rows; left > 0;) {
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (use & 1) * kAccCols;
         uint32_t add = 0;
-        for (int in = 0; in < kSegment && left > 0; ++in, left -= kBK) {
+        for (int in = 0; in < seg && left > 0; ++in, left -= kBK) {
           ok = wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
           if (!ok) break;
           if (left < kBK && left % 16 != 0) {
@@ -853,7 +881,8 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
         for (int i = 0; i < S::kBlocks; ++i)
 #pragma unroll
           for (int k = 0; k < 32; ++k) sum[i][k] = 0.f;
-      for (int r = 0; r < x.rows; r += kSegment * kBK, ++use) {
+      const int seg = segment((x.rows + kBK - 1) / kBK);
+      for (int r = 0; r < x.rows; r += seg * kBK, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
 #pragma unroll
@@ -868,10 +897,14 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
 #pragma unroll
       for (int i = 0; i < S::kBlocks; ++i) {
         const int col = (2 * i + half) * 32;
-        if (col < x.cols && row < g.m)
-          wgrad_store(g, dw + col, g.m - row, x.cols - col, lane, sum[i], stage);
+        if (col >= x.cols || row >= g.m) continue;
+        if (p.bulk) wgrad_store_bulk(&p.dw, x.expert, row, x.j0 + col, lane, sum[i], stage);
+        else wgrad_store(g, dw + col, g.m - row, x.cols - col, lane, sum[i], stage);
       }
     }
+    // Shared memory must outlive the stores that read it.
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   teardown<V::kPair>(c, warp);
 }
@@ -940,17 +973,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// A tensor map over an aligned operand with boxes of 64 columns x box_rows rows (128-byte
-// swizzle); batched operands get a third dimension.
+// A tensor map with boxes of 128 bytes x box_rows rows (128-byte swizzle) over an operand whose
+// rows start on 16 bytes; batched operands get a third dimension.
 cudaError_t encode(CUtensorMap* map, const Operand& o, int32_t dtype, bool batched, uint32_t box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
   if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t size = dtype == kF32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.batch};
-  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2,
-                                 (cuuint64_t)(o.batch == 1 ? o.rows * o.ld : o.stride) * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1}, unit[3] = {1, 1, 1};
-  const CUresult r = fn(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * size,
+                                 (cuuint64_t)(o.batch == 1 ? o.rows * o.ld : o.stride) * size};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), box_rows, 1}, unit[3] = {1, 1, 1};
+  const CUresult r = fn(map, dtype == kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                             : dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         batched ? 3 : 2, const_cast<void*>(o.ptr), dims, strides, box, unit,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1050,6 +1085,11 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
     if (e == cudaSuccess) e = encode(&p.a, a, g.dtype, false, 64);
     if (e == cudaSuccess) e = encode(&p.b, b, g.dtype, false, 64);
   }
+  // Written by TMA where every row of dw starts on 16 bytes; adding needs the old values.
+  p.bulk = !g.accumulate && reinterpret_cast<uintptr_t>(g.dw) % 16 == 0 && g.lddw % 4 == 0 &&
+           (g.n_experts == 1 || g.dw_stride % 4 == 0);
+  if (e == cudaSuccess && p.bulk)
+    e = encode(&p.dw, {g.dw, g.m, g.n, g.lddw, g.n_experts, g.dw_stride}, kF32, true, 32);
   if (e != cudaSuccess) return e;
   const bool pair = g.m > kBM && wgrad_grid<Pair>(g).tiles >= sms / 2;
   return pair ? launch_wgrad<Pair>(p, sms, st) : launch_wgrad<Wide>(p, sms, st);
