@@ -7,6 +7,7 @@ and raises if it has not been built: there is no other code path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -575,23 +576,24 @@ def muon_swiglu_grad(dout, gate, up, dgate, dup, row_weight=None, d_row_weight=N
 
 # ------------------------------------------------------------------ gradient norm, clipping
 def _tensor_list(tensors, name):
-    """A host array of muon_tensor (pointer, length, type as three 64-bit words; the machine is
-    little-endian) from contiguous CUDA tensors."""
-    flat = []
-    for t in tensors:
-        k = _KINDS.get(t.dtype)
-        if k is None:
-            k = _kind(t, name)
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous CUDA tensors")
-        flat += (t.data_ptr(), t.numel(), k)
-    return (ctypes.c_uint64 * max(3, len(flat)))(*flat)
+    """(array that owns it, address) of muon_tensor records (pointer, length, type as three
+    64-bit words; the machine is little-endian) of contiguous CUDA tensors."""
+    kinds = _KINDS or _kinds()
+    try:
+        flat = [v for t in tensors for v in (t.data_ptr(), t.numel(), kinds[t.dtype])]
+    except KeyError as e:
+        raise ValueError(f"{name}: type {e.args[0]}; float32, bfloat16 or float16 is needed") from None
+    if not all([t.is_cuda and t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name}: must be contiguous CUDA tensors")
+    words = array.array("Q", flat)
+    return words, words.buffer_info()[0]
 
 
 def _clip_call(grads, norm, workspace, stream):
-    """(host array of grads, norm's pointer, workspace pointer, bytes and owner, stream)."""
+    """(grads' records and their owner, norm's pointer, workspace pointer, bytes and owner,
+    stream)."""
     np = _row_floats(norm, 2, "norm")
-    g = _tensor_list(grads, "grads")
+    words, g = _tensor_list(grads, "grads")
     nbytes = 0
     if workspace is None:
         need = _SZ()
@@ -599,13 +601,13 @@ def _clip_call(grads, norm, workspace, stream):
                "muon_clip_workspace_bytes")
         nbytes = need.value
     ws, nbytes, owner = _workspace(workspace, nbytes, 8, norm, stream)
-    return g, np, ws, nbytes, owner, _stream_of(stream, norm)
+    return g, words, np, ws, nbytes, owner, _stream_of(stream, norm)
 
 
 def muon_grad_norm(grads, max_norm, norm, workspace=None, stream=None):
     """norm[0] = the 2-norm of all gradients together, norm[1] = min(1, max_norm / (norm[0] +
     1e-6)).  grads: a sequence of contiguous CUDA tensors; norm: 2 float32 on the GPU."""
-    g, np, ws, nbytes, owner, st = _clip_call(grads, norm, workspace, stream)
+    g, words, np, ws, nbytes, owner, st = _clip_call(grads, norm, workspace, stream)
     _check(lib.muon_grad_norm(g, len(grads), max_norm, np, ws, nbytes, st), "muon_grad_norm")
 
 
@@ -614,8 +616,8 @@ def muon_clip_grads(grads, outs, max_norm, norm, workspace=None, stream=None):
     of its length and of its type or float32."""
     if len(outs) != len(grads):
         raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
-    o = _tensor_list(outs, "outs")
-    g, np, ws, nbytes, owner, st = _clip_call(grads, norm, workspace, stream)
+    out_words, o = _tensor_list(outs, "outs")
+    g, words, np, ws, nbytes, owner, st = _clip_call(grads, norm, workspace, stream)
     _check(lib.muon_clip_grads(g, o, len(grads), max_norm, np, ws, nbytes, st), "muon_clip_grads")
 
 

@@ -56,31 +56,44 @@ constexpr int kABytes = kBM * 128;  // 16 KB
 constexpr int kBox = 64 * 128;      // an MN-major box: 64 k-rows of 128 bytes
 constexpr int kAccCols = 256;       // TMEM columns of one accumulator
 constexpr int kSegment = 12;        // most k-blocks per segment of an fp32 result
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 6;
 constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 
 // mm tile variants: kMaxN rows of one expert per tile at most, on single CTAs or pairs.
 // Narrow: smaller stages leave room for more of the weight in flight, for experts with few
-// rows, whose product is bound by streaming it.
+// rows, whose product is bound by streaming it, and stages of two k-blocks under one pair of
+// barriers: a wait, an elected lane and a commit cost the issuing warps 250-400 cycles, more than
+// the loads or MMAs of one narrow k-block (one token 12.5 -> 9.2 us).  Where the MMAs take 500
+// cycles a k-block, the finer stages are ahead (Pair: 328 against 335 us on 98304 x 1408 -> 2048).
 struct Pair {
-  static constexpr bool kPair = true;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6;
+  static constexpr bool kPair = true, kSplit = false;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1;
 };
 struct Wide {
-  static constexpr bool kPair = false;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4;
+  static constexpr bool kPair = false, kSplit = false;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
 };
 struct Narrow {
-  static constexpr bool kPair = false;
-  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 8;
+  static constexpr bool kPair = false, kSplit = false;
+  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2;
 };
+// Split: a cluster of CTAs shares one tile, each taking a part of k; the first one adds the
+// parts up, in order, out of the others' shared memory.  For products of so few tiles that most
+// SMs would have none: a k-block costs a CTA about 0.27 us whatever the tile's width (the MMA
+// reads 128 rows of the weight), so 6 tokens through 2048 -> 1408 took 13.8 us on 66 CTAs.
+struct Split {
+  static constexpr bool kPair = false, kSplit = true;
+  static constexpr int kMaxN = 32, kBoxRows = 16, kStages = 4, kSub = 2;
+};
+constexpr int kMostParts = 8;  // portable cluster size
 // What follows from a variant (wgrad uses Pair and Wide).
 template <typename V>
 struct Shape {
   static constexpr int kCtas = V::kPair ? 2 : 1;
   static constexpr int kM = kBM * kCtas;                   // M of the MMA
   static constexpr int kStepN = 16 * kCtas;                // N goes in steps of this
-  static constexpr int kStage = kABytes + V::kMaxN / kCtas * 128;
+  static constexpr int kBlock = kABytes + V::kMaxN / kCtas * 128;  // bytes of a k-block
+  static constexpr int kStage = kBlock * V::kSub;
   static constexpr int kBlocks = (V::kMaxN + 63) / 64;     // 32-column blocks per epilogue warp
 };
 
@@ -100,7 +113,7 @@ struct WgradParams {
 // Barriers and flags of one CTA.
 struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  // wgrad on pairs, last k-block of a tile: the second CTA's own operands have landed, and it
+  // wgrad on pairs, last stage of a tile: the second CTA's own operands have landed, and it
   // has zeroed the rows that are not its expert's.
   uint64_t tail[kMaxStages], fixed[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
@@ -178,9 +191,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Bounded wait of a whole warp.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* err, int* abort) {
+// Bounded wait of a whole warp.  The polling stays out of line: the kernels' code is large
+// enough for instruction fetches to matter in short launches.
+__device__ __noinline__ bool wait_warp_slow(uint64_t* bar, uint32_t parity, int* err, int* abort) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitBudget, err, abort));
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* err, int* abort) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_warp_slow(bar, parity, err, abort);
 }
 
 // Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far complete.
@@ -243,10 +260,12 @@ __device__ __forceinline__ void drain_ring(Control& c, int64_t fills, uint32_t r
   }
 }
 
-// k-blocks of each of a sum's segments, of equal length up to the last one.
+// k-blocks of each of a sum's segments, whole stages of equal number up to the last segment.
+template <typename V>
 __device__ __forceinline__ int segment(int k_blocks) {
-  const int n = (k_blocks + kSegment - 1) / kSegment;
-  return n > 1 ? (k_blocks + n - 1) / n : k_blocks;
+  const uint32_t n = (uint32_t)(k_blocks + kSegment - 1) / kSegment;
+  const int len = n > 1 ? (int)((uint32_t)(k_blocks + n - 1) / n) : k_blocks;
+  return (len + V::kSub - 1) / V::kSub * V::kSub;
 }
 
 // Position in the ring of operand stages.
@@ -290,19 +309,20 @@ __device__ __forceinline__ void setup(Control& c, int warp) {
   }
 }
 
-// Barriers and TMEM are ready in every CTA that may signal them.
-template <bool kPair>
+// Barriers and TMEM are ready in every CTA that may signal them; or every CTA is done with the
+// others' shared memory.
+template <bool kCluster>
 __device__ __forceinline__ void sync_ctas() {
   tc_fence_before();
-  if constexpr (kPair) cluster_sync(); else __syncthreads();
+  if constexpr (kCluster) cluster_sync(); else __syncthreads();
   tc_fence_after();
 }
 
-template <bool kPair>
+template <typename V>
 __device__ __forceinline__ void teardown(Control& c, int warp) {
-  sync_ctas<kPair>();
+  sync_ctas<V::kPair || V::kSplit>();
   if (warp == 2) {
-    if constexpr (kPair) tmem_dealloc_pair(c.tmem, 2 * kAccCols);
+    if constexpr (V::kPair) tmem_dealloc_pair(c.tmem, 2 * kAccCols);
     else tmem_dealloc(c.tmem, 2 * kAccCols);
   }
 }
@@ -320,8 +340,7 @@ __device__ __forceinline__ void release_acc(Control& c, int ab, uint32_t rank, i
 
 // Waits for accumulator use number `use` (epilogue warp).
 __device__ __forceinline__ bool wait_acc(Control& c, int use, int* err) {
-  const bool ok = mbar_wait_bounded(&c.acc_full[use & 1], (use >> 1) & 1, kWaitBudget, err, &c.abort);
-  if (!__all_sync(0xffffffffu, ok)) return false;
+  if (!wait_warp(&c.acc_full[use & 1], (use >> 1) & 1, err, &c.abort)) return false;
   tc_fence_after();
   return true;
 }
@@ -397,8 +416,6 @@ __device__ __forceinline__ void count_tiles(const int32_t* off, int n_experts, i
 }
 
 // ---------------------------------------------------------------------------- mm
-constexpr int kMmStaging = 2048;  // per epilogue warp
-
 struct MmTile {
   int expert, row, rows;  // rows row .. row + rows - 1 of x and y, all of `expert`
   int n;                  // the MMA's N: rows in steps of kStepN
@@ -406,8 +423,8 @@ struct MmTile {
 };
 
 template <typename V>
-__device__ __forceinline__ MmTile mm_tile(int64_t t, int f_tiles, int n_experts, const int32_t* off,
-                                          const int32_t* first) {
+__device__ __forceinline__ MmTile mm_tile(uint32_t t, uint32_t f_tiles, int n_experts,
+                                          const int32_t* off, const int32_t* first) {
   constexpr int kStep = Shape<V>::kStepN;
   const int rt = (int)(t / f_tiles);
   int lo = 0, hi = n_experts - 1;  // the expert with first[e] <= rt < first[e + 1]
@@ -415,61 +432,73 @@ __device__ __forceinline__ MmTile mm_tile(int64_t t, int f_tiles, int n_experts,
     const int mid = (lo + hi) >> 1;
     if (first[mid + 1] > rt) hi = mid; else lo = mid + 1;
   }
+  const int rows = off[lo + 1] - off[lo], tiles = first[lo + 1] - first[lo];
   // Within the expert: groups of kGroup row tiles, in each every column tile of y, in each the
   // group's row tiles.  The CTAs at work at a time then share a few column tiles of the weight
   // and a group's rows, and the weight comes from HBM once per group.
   constexpr int kGroup = 8;
-  const int rows = off[lo + 1] - off[lo], tiles = first[lo + 1] - first[lo];
-  const int64_t in = t - (int64_t)first[lo] * f_tiles;
-  const int group = (int)(in / ((int64_t)kGroup * f_tiles)) * kGroup;
-  const int size = min(kGroup, tiles - group), rest = (int)(in - (int64_t)group * f_tiles);
-  const int width = ((rows + tiles - 1) / tiles + kStep - 1) / kStep * kStep;
-  const int begin = (group + rest % size) * width;
+  uint32_t rest = t - (uint32_t)first[lo] * f_tiles;
+  int group = 0, size = tiles;
+  if (tiles > kGroup) {
+    group = (int)(rest / (kGroup * f_tiles)) * kGroup;
+    rest -= (uint32_t)group * f_tiles;
+    size = min(kGroup, tiles - group);
+  }
+  int row_tile = 0, f_tile = (int)rest, width = rows;
+  if (tiles > 1) {
+    f_tile = (int)(rest / (uint32_t)size);
+    row_tile = group + (int)rest - f_tile * size;
+    width = (int)((uint32_t)(rows + tiles - 1) / (uint32_t)tiles);
+  }
+  width = (width + kStep - 1) / kStep * kStep;
+  const int begin = row_tile * width;
   MmTile m;
   m.expert = lo;
   m.row = off[lo] + begin;
   m.rows = min(width, rows - begin);
   m.n = (m.rows + kStep - 1) / kStep * kStep;
-  m.f0 = rest / size * Shape<V>::kM;
+  m.f0 = f_tile * Shape<V>::kM;
   return m;
 }
 
 // Stores accumulator columns 32 c .. 32 c + 31 (rows of y) of this warp's 32 lanes (columns
-// f .. f + 31 of y): the block is turned around in `stage` (2 KB), so that 64 or 128
-// consecutive bytes of a row of y leave together.
+// f .. f + 31 of y): one coalesced access per row, whatever y's alignment.
 template <typename O>
 __device__ __forceinline__ void mm_store(const GroupedMm& g, const MmTile& m, int c, int f, int lane,
-                                         const float (&v)[32], O* stage) {
-  constexpr int kRows = kMmStaging / (32 * sizeof(O));  // rows staged at a time
-  constexpr int kPer = 16 / sizeof(O), kChunks = 32 / kPer, kPass = 32 / kChunks;
+                                         const float (&v)[32]) {
+  if (f + lane >= g.n) return;
+  O* dst = static_cast<O*>(g.y) + (int64_t)(m.row + 32 * c) * g.ldy + f + lane;
+  const int left = m.rows - 32 * c;
+  if (left >= 32) {
 #pragma unroll
-  for (int h = 0; h < 32 / kRows; ++h) {
-    if (c * 32 + h * kRows >= m.rows) break;
+    for (int t = 0; t < 32; ++t) put(dst + t * g.ldy, v[t]);
+  } else {
 #pragma unroll
-    for (int t = 0; t < kRows; ++t) put(&stage[t * 32 + lane], v[h * kRows + t]);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kRows / kPass; ++i) {
-      const int t = i * kPass + lane / kChunks, q = lane % kChunks * kPer;
-      const int r = c * 32 + h * kRows + t, col = f + q;
-      if (r < m.rows && col < g.n) {
-        O* dst = static_cast<O*>(g.y) + (int64_t)(m.row + r) * g.ldy + col;
-        const O* src = stage + t * 32 + q;
-        if (col + kPer <= g.n && reinterpret_cast<uintptr_t>(dst) % 16 == 0)
-          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-        else
-          for (int e = 0; e < kPer && col + e < g.n; ++e) dst[e] = src[e];
-      }
-    }
-    __syncwarp();
+    for (int t = 0; t < 32; ++t)
+      if (t < left) put(dst + t * g.ldy, v[t]);
   }
 }
 
+// Index of the CTA in its cluster of `parts`, for Split.
+struct Part {
+  int index, parts;
+};
+template <typename V>
+__device__ __forceinline__ Part split_part() {
+  Part p{0, 1};
+  if constexpr (V::kSplit) {
+    p.index = (int)cluster_ctarank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(p.parts));
+  }
+  return p;
+}
+
 template <typename V, typename O>
-__global__ void __cluster_dims__(Shape<V>::kCtas, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 grouped_mm_kernel(const __grid_constant__ MmParams p) {
   using S = Shape<V>;
-  constexpr bool kFp32 = sizeof(O) == 4;  // summed in segments
+  // Summed in segments, in registers.
+  constexpr bool kSums = sizeof(O) == 4 || V::kSplit;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
   __shared__ int32_t off[kMaxExperts + 1], first[kMaxExperts + 1];
@@ -477,15 +506,29 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
   const GroupedMm& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = V::kPair ? cluster_ctarank() : 0u;
+  const Part part_k = split_part<V>();
+  if (threadIdx.x == 96) {  // warp 3: off the other warps' way
+    prefetch_tmap(&p.w);
+    prefetch_tmap(&p.x);
+  }
   setup<V::kPair>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kMaxN, lane, first);
   __syncthreads();
   sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
-  const int f_tiles = (g.n - 1) / S::kM + 1, k_blocks = (g.k - 1) / kBK + 1, seg = segment(k_blocks);
-  const int64_t tiles = (int64_t)first[g.n_experts] * f_tiles;
-  const int64_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
+  const uint32_t f_tiles = (uint32_t)(g.n - 1) / S::kM + 1, tiles = (uint32_t)first[g.n_experts] * f_tiles;
+  int kb0 = 0, kb1 = (g.k - 1) / kBK + 1;  // this CTA's k-blocks
+  uint32_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
+  if constexpr (V::kSplit) {
+    const int all = kb1;  // parts is a power of two
+    const int shift = 31 - __clz(part_k.parts);
+    kb0 = (int)((int64_t)all * part_k.index >> shift);
+    kb1 = (int)((int64_t)all * (part_k.index + 1) >> shift);
+    unit >>= shift;
+    units >>= shift;
+  }
+  const int seg = segment<V>(kb1 - kb0);
 
   if (warp == 0) {
     Ring<V::kStages> ring;
@@ -494,31 +537,37 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
     const uint32_t full0 = smem_u32(c.full), dst0 = smem_u32(smem);
     // A pair's second CTA signals the first one's barriers.
     const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
-    for (int64_t t = unit; t < tiles && ok; t += units) {
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
       const int part = m.n / S::kCtas;  // rows of x this CTA brings
       const int boxes = (part + V::kBoxRows - 1) / V::kBoxRows;
       const uint32_t bytes = S::kCtas * (kABytes + boxes * V::kBoxRows * 128);
       const int f = m.f0 + kBM * (int)rank, row = m.row + part * (int)rank;
-      for (int kb = 0; kb < k_blocks; ++kb, ++fills) {
+      for (int kb = kb0; kb < kb1; kb += V::kSub, ++fills) {
         ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
         if (!ok) break;
         const uint32_t sig = sig0 + 8 * ring.stage, a = dst0 + ring.stage * S::kStage;
-        const int k0 = kb * kBK;
+        const int blocks = min(V::kSub, kb1 - kb);
         if (elect_one()) {
           // Only the first CTA of a pair arrives, announcing both CTAs' bytes.
-          if (rank == 0) expect(full0 + 8 * ring.stage, bytes);
-          if (g.trans) {
-            load_3d<V::kPair>(a, &p.w, k0, f, m.expert, sig);
-          } else {
-            load_3d<V::kPair>(a, &p.w, f, k0, m.expert, sig);
-            load_3d<V::kPair>(a + kBox, &p.w, f + 64, k0, m.expert, sig);
-          }
+          if (rank == 0) expect(full0 + 8 * ring.stage, blocks * bytes);
 #pragma unroll
-          for (int b = 0; b < V::kMaxN / S::kCtas / V::kBoxRows; ++b)
-            if (b < boxes)
-              load_2d<V::kPair>(a + kABytes + b * V::kBoxRows * 128, &p.x, k0, row + b * V::kBoxRows,
-                                sig);
+          for (int j = 0; j < V::kSub; ++j) {
+            if (j >= blocks) break;
+            const int k0 = (kb + j) * kBK;
+            const uint32_t aj = a + j * S::kBlock;
+            if (g.trans) {
+              load_3d<V::kPair>(aj, &p.w, k0, f, m.expert, sig);
+            } else {
+              load_3d<V::kPair>(aj, &p.w, f, k0, m.expert, sig);
+              load_3d<V::kPair>(aj + kBox, &p.w, f + 64, k0, m.expert, sig);
+            }
+#pragma unroll
+            for (int b = 0; b < V::kMaxN / S::kCtas / V::kBoxRows; ++b)
+              if (b < boxes)
+                load_2d<V::kPair>(aj + kABytes + b * V::kBoxRows * 128, &p.x, k0,
+                                  row + b * V::kBoxRows, sig);
+          }
         }
         __syncwarp();
         ring.next();
@@ -535,27 +584,33 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
     const uint32_t a_mn = g.trans ? 0 : 1, a_step = a_mn ? 16 * 128 / 16 : 32 / 16;
     const uint32_t a0 = desc_lo(smem_u32(smem), a_mn ? kBox : 16);
     const uint32_t b0 = desc_lo(smem_u32(smem) + kABytes, 16);
-    for (int64_t t = unit; t < tiles && ok; t += units) {
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, m.n, a_mn, 0);
-      for (int kb = 0; kb < k_blocks;) {
+      for (int kb = kb0; kb < kb1;) {
         // One accumulator: all k-blocks, or a segment of them.
-        const int end = kFp32 ? min(k_blocks, kb + seg) : k_blocks;
+        const int end = kSums ? min(kb1, kb + seg) : kb1;
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (use & 1) * kAccCols;
         uint32_t add = 0;
-        for (; kb < end; ++kb) {
+        for (; kb < end; kb += V::kSub) {
           ok = wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
           if (!ok) break;
           const uint32_t a = a0 + ring.stage * (S::kStage / 16), b = b0 + ring.stage * (S::kStage / 16);
+          const int blocks = min(V::kSub, kb1 - kb);
           if (elect_one()) {
             // Columns past k are zeros in both operands.
-            mma<V::kPair>(d, a, b, idesc, add);
-            mma<V::kPair>(d, a + a_step, b + 2, idesc, 1);
-            mma<V::kPair>(d, a + 2 * a_step, b + 4, idesc, 1);
-            mma<V::kPair>(d, a + 3 * a_step, b + 6, idesc, 1);
+#pragma unroll
+            for (int j = 0; j < V::kSub; ++j) {
+              if (j >= blocks) break;
+              const uint32_t aj = a + j * (S::kBlock / 16), bj = b + j * (S::kBlock / 16);
+              mma<V::kPair>(d, aj, bj, idesc, j == 0 ? add : 1);
+              mma<V::kPair>(d, aj + a_step, bj + 2, idesc, 1);
+              mma<V::kPair>(d, aj + 2 * a_step, bj + 4, idesc, 1);
+              mma<V::kPair>(d, aj + 3 * a_step, bj + 6, idesc, 1);
+            }
             commit<V::kPair>(&c.empty[ring.stage]);
           }
           __syncwarp();
@@ -576,34 +631,41 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
     __syncwarp();
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;  // a quarter of the lanes, every second block
-    O* stage = reinterpret_cast<O*>(smem + V::kStages * S::kStage + (warp - 4) * kMmStaging);
     int use = 0;
     bool ok = true;
-    for (int64_t t = unit; t < tiles && ok; t += units) {
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
       const int f = m.f0 + kBM * (int)rank + 32 * q;
-      if constexpr (kFp32) {
+      if constexpr (kSums) {
         float sum[S::kBlocks][32];
-        for (int kb = 0; kb < k_blocks; kb += seg, ++use) {
+        for (int kb = kb0; kb < kb1; kb += seg, ++use) {
           ok = wait_acc(c, use, g.err);
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < S::kBlocks; ++i)
             if ((2 * i + half) * 32 < m.n)
-              add_acc(tmem, use & 1, q, (2 * i + half) * 32, kb == 0, sum[i]);
+              add_acc(tmem, use & 1, q, (2 * i + half) * 32, kb == kb0, sum[i]);
           release_acc<V::kPair>(c, use & 1, rank, lane);
         }
         if (!ok) break;
+        if constexpr (V::kSplit) {
+          // The operand stages are free: this tile's MMAs were the last.
+          if (half == 0)
 #pragma unroll
-        for (int i = 0; i < S::kBlocks; ++i)
-          if ((2 * i + half) * 32 < m.n) mm_store<O>(g, m, 2 * i + half, f, lane, sum[i], stage);
+            for (int k = 0; k < 32; ++k)
+              reinterpret_cast<float*>(smem)[(q * 32 + k) * 32 + lane] = sum[0][k];
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::kBlocks; ++i)
+            if ((2 * i + half) * 32 < m.n) mm_store<O>(g, m, 2 * i + half, f, lane, sum[i]);
+        }
       } else {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
         for (int b = half; b * 32 < m.n; b += 2) {
           float v[32];
           add_acc(tmem, use & 1, q, 32 * b, true, v);
-          mm_store<O>(g, m, b, f, lane, v, stage);
+          mm_store<O>(g, m, b, f, lane, v);
         }
         release_acc<V::kPair>(c, use & 1, rank, lane);
         ++use;
@@ -616,7 +678,47 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
       for (int64_t f = threadIdx.x - 128; f < g.n; f += kEpiWarps * 32) put(&row[f], 0.f);
     }
   }
-  teardown<V::kPair>(c, warp);
+  if constexpr (V::kSplit) {
+    // The parts of the tile are in the CTAs' shared memory, as [quarter][row of y][column]:
+    // every CTA adds and stores a share, 8 columns per thread, the parts in order.
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 4 && unit < tiles) {
+      const MmTile m = mm_tile<V>(unit, f_tiles, g.n_experts, off, first);
+      const int cols = g.n - m.f0;
+      for (int i = threadIdx.x - 128 + part_k.index * kEpiWarps * 32; i < m.rows * 16;
+           i += part_k.parts * kEpiWarps * 32) {
+        const int r = i / 16, col = i % 16 * 8;
+        const uint32_t at = smem_u32(smem) + ((col / 32 * 32 + r) * 32 + col % 32) * 4;
+        float sum[8] = {};
+        for (int q = 0; q < part_k.parts; ++q) {
+          float v[8];
+          const uint32_t from = mapa_shared(at, q);
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(from) : "memory");
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "r"(from + 16) : "memory");
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[k] += v[k];
+        }
+        O* dst = static_cast<O*>(g.y) + (int64_t)(m.row + r) * g.ldy + m.f0 + col;
+        if (col + 8 <= cols && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
+          __align__(16) O o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) put(&o[k], sum[k]);
+#pragma unroll
+          for (int k = 0; k < (int)sizeof(O) / 2; ++k)
+            reinterpret_cast<uint4*>(dst)[k] = reinterpret_cast<const uint4*>(o)[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (col + k < cols) put(&dst[k], sum[k]);
+        }
+      }
+    }
+    __syncwarp();
+  }
+  teardown<V>(c, warp);
 }
 
 // ---------------------------------------------------------------------------- wgrad
@@ -629,7 +731,8 @@ struct WgradTile {
 };
 
 struct WgradGrid {
-  int m_tiles, n_tiles, width;
+  uint32_t m_tiles, n_tiles;
+  int width;
   int64_t tiles;
 };
 
@@ -638,23 +741,21 @@ __host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g) 
   WgradGrid w;
   w.m_tiles = (g.m - 1) / Shape<V>::kM + 1;
   w.n_tiles = (g.n - 1) / V::kMaxN + 1;
-  w.width = ((g.n - 1) / w.n_tiles + kWgradStep) / kWgradStep * kWgradStep;  // columns dealt evenly
+  w.width = (int)((uint32_t)(g.n - 1) / w.n_tiles + kWgradStep) / kWgradStep * kWgradStep;  // columns dealt evenly
   w.tiles = (int64_t)g.n_experts * w.m_tiles * w.n_tiles;
   return w;
 }
 
 template <typename V>
-__device__ __forceinline__ WgradTile wgrad_tile(const GroupedWgrad& g, const WgradGrid& w, int64_t t,
+__device__ __forceinline__ WgradTile wgrad_tile(const GroupedWgrad& g, const WgradGrid& w, uint32_t t,
                                                 bool bad) {
-  const int64_t per = (int64_t)w.m_tiles * w.n_tiles;
-  const int e = (int)(t / per);
-  const int64_t r = t - e * per;
+  const uint32_t per = w.m_tiles * w.n_tiles, e = t / per, r = t - e * per, i = r / w.n_tiles;
   WgradTile x;
   x.expert = e;
   x.row = bad ? 0 : (int)g.offsets[e];
   x.rows = bad ? 0 : (int)(g.offsets[e + 1] - g.offsets[e]);
-  x.i0 = (int)(r / w.n_tiles) * Shape<V>::kM;
-  x.j0 = (int)(r % w.n_tiles) * w.width;
+  x.i0 = (int)i * Shape<V>::kM;
+  x.j0 = (int)(r - i * w.n_tiles) * w.width;
   x.cols = min(w.width, g.n - x.j0);
   x.n = (x.cols + kWgradStep - 1) / kWgradStep * kWgradStep;
   return x;
@@ -670,40 +771,42 @@ __device__ __forceinline__ void zero_rows(uint8_t* stage, int left, int boxes, i
   __syncwarp();
 }
 
-// dw[row .. row + 31, col .. col + 31] (=, +=) the block whose row `lane` the warp's lane holds.
+// The 32 values from dst on that lane's row of a block holds (n of them inside the matrix).
+__device__ __forceinline__ void wgrad_load(const float* dst, int n, float (&v)[32]) {
+  if (n >= 32 && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(dst + k);
+      v[k] = q.x;
+      v[k + 1] = q.y;
+      v[k + 2] = q.z;
+      v[k + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = k < n ? dst[k] : 0.f;
+  }
+}
+
+// Writes the block dw[row .. row + 31, col .. col + 31] whose row `lane` the warp's lane holds.
 // The block is turned around in `stage` (16-byte chunk k of row r in slot k ^ (r & 7), free of
-// bank conflicts both ways), so that four whole 128-byte rows leave per access.
-__device__ __forceinline__ void wgrad_store(const GroupedWgrad& g, float* dw, int rows, int cols,
-                                            int lane, const float (&v)[32], float4* stage) {
+// bank conflicts on the way in), so that every access covers one row.
+__device__ __forceinline__ void wgrad_store(float* dw, int64_t lddw, int rows, int cols, int lane,
+                                            const float (&v)[32], float4* stage) {
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     stage[8 * lane + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
   __syncwarp();
-  const int k = lane & 7, left = cols - 4 * k;
-  float* dst = dw + (int64_t)(lane >> 3) * g.lddw + 4 * k;
-#pragma unroll
-  for (int i = 0; i < 8; ++i, dst += 4 * g.lddw) {
-    const int r = 4 * i + (lane >> 3);
-    if (r >= rows || left <= 0) continue;
-    float4 o = stage[8 * r + (k ^ (r & 7))];
-    if (left >= 4 && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
-      if (g.accumulate) {
-        const float4 d = __ldcs(reinterpret_cast<const float4*>(dst));
-        o = make_float4(d.x + o.x, d.y + o.y, d.z + o.z, d.w + o.w);
-      }
-      __stcs(reinterpret_cast<float4*>(dst), o);
-    } else {
-      const float e[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < left) dst[j] = g.accumulate ? dst[j] + e[j] : e[j];
-    }
-  }
+  if (lane < cols)
+#pragma unroll 8
+    for (int r = 0; r < min(rows, 32); ++r)
+      dw[r * lddw + lane] =
+          reinterpret_cast<const float*>(stage + 8 * r + (lane >> 2 ^ (r & 7)))[lane & 3];
   __syncwarp();
 }
 
-// The same block (=) by TMA, which drops what lies outside the matrix: the warp's only waits are
-// for the previous block to have left `stage`.  dw must start on 16 bytes in every row.
+// The same by TMA, which drops what lies outside the matrix: the warp's only waits are for the
+// previous block to have left `stage`.  dw must start on 16 bytes in every row.
 __device__ __forceinline__ void wgrad_store_bulk(const CUtensorMap* map, int expert, int row, int col,
                                                  int lane, const float (&v)[32], float4* stage) {
   if (lane == 0) bulk_wait_read();
@@ -723,7 +826,7 @@ __device__ __forceinline__ void wgrad_store_bulk(const CUtensorMap* map, int exp
 }
 
 template <typename V>
-__global__ void __cluster_dims__(Shape<V>::kCtas, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
   using S = Shape<V>;
   extern __shared__ uint8_t smem_raw[];
@@ -732,6 +835,10 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
   const GroupedWgrad& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = V::kPair ? cluster_ctarank() : 0u;
+  if (threadIdx.x == 96 && g.rows > 0) {
+    prefetch_tmap(&p.a);
+    prefetch_tmap(&p.b);
+  }
   setup<V::kPair>(c, warp);
   bool bad = false;
   for (int e = threadIdx.x; e <= g.n_experts; e += kThreads) {
@@ -743,7 +850,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
   sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
   const WgradGrid w = wgrad_grid<V>(g);
-  const int64_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
+  const uint32_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas, tiles = (uint32_t)w.tiles;
 
   if (warp == 0) {
     Ring<V::kStages> ring;
@@ -752,24 +859,28 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     bool ok = true;
     const uint32_t full0 = smem_u32(c.full), tail0 = smem_u32(c.tail), dst0 = smem_u32(smem);
     const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
-    for (int64_t t = unit; t < w.tiles && ok; t += units) {
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad);
       const int part = x.n / S::kCtas, boxes = (part + 63) / 64;  // columns of b this CTA brings
       const int i = x.i0 + kBM * (int)rank, j = x.j0 + part * (int)rank;
-      for (int r = 0; r < x.rows; r += kBK, ++fills) {
+      for (int r = 0; r < x.rows; r += kBK * V::kSub, ++fills) {
         ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
         if (!ok) break;
         const uint32_t a = dst0 + ring.stage * S::kStage;
-        const int y = x.row + r;
-        // A last k-block with rows to zero lands on each CTA's own barrier.
-        const bool own = V::kPair && x.rows - r < kBK && (x.rows - r) % 16 != 0;
+        const int left = x.rows - r, y = x.row + r, blocks = min(V::kSub, (left + kBK - 1) / kBK);
+        // A last stage with rows to zero lands on each CTA's own barrier.
+        const bool own = V::kPair && left < kBK * V::kSub && left % 16 != 0;
         if (own) {
           const uint32_t bar = (rank == 0 ? full0 : tail0) + 8 * ring.stage;
           if (elect_one()) {
-            expect(bar, (2 + boxes) * kBox);
-            for (int b = 0; b < 2; ++b) load_2d<false>(a + b * kBox, &p.a, i + 64 * b, y, bar);
-            for (int b = 0; b < boxes; ++b)
-              load_2d<false>(a + kABytes + b * kBox, &p.b, j + 64 * b, y, bar);
+            expect(bar, blocks * (2 + boxes) * kBox);
+            for (int q = 0; q < blocks; ++q) {
+              const uint32_t aq = a + q * S::kBlock;
+              for (int b = 0; b < 2; ++b)
+                load_2d<false>(aq + b * kBox, &p.a, i + 64 * b, y + q * kBK, bar);
+              for (int b = 0; b < boxes; ++b)
+                load_2d<false>(aq + kABytes + b * kBox, &p.b, j + 64 * b, y + q * kBK, bar);
+            }
           }
           if (rank != 0) {
             tails ^= 1u << ring.stage;
@@ -777,12 +888,18 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
           }
         } else if (elect_one()) {
           const uint32_t sig = sig0 + 8 * ring.stage;
-          if (rank == 0) expect(full0 + 8 * ring.stage, S::kCtas * (2 + boxes) * kBox);
-          load_2d<V::kPair>(a, &p.a, i, y, sig);
-          load_2d<V::kPair>(a + kBox, &p.a, i + 64, y, sig);
+          if (rank == 0) expect(full0 + 8 * ring.stage, S::kCtas * blocks * (2 + boxes) * kBox);
 #pragma unroll
-          for (int b = 0; b < V::kMaxN / S::kCtas / 64; ++b)
-            if (b < boxes) load_2d<V::kPair>(a + kABytes + b * kBox, &p.b, j + 64 * b, y, sig);
+          for (int q = 0; q < V::kSub; ++q) {
+            if (q >= blocks) break;
+            const uint32_t aq = a + q * S::kBlock;
+            load_2d<V::kPair>(aq, &p.a, i, y + q * kBK, sig);
+            load_2d<V::kPair>(aq + kBox, &p.a, i + 64, y + q * kBK, sig);
+#pragma unroll
+            for (int b = 0; b < V::kMaxN / S::kCtas / 64; ++b)
+              if (b < boxes)
+                load_2d<V::kPair>(aq + kABytes + b * kBox, &p.b, j + 64 * b, y + q * kBK, sig);
+          }
         }
         __syncwarp();
         ring.next();
@@ -801,22 +918,23 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     bool ok = true;
     constexpr uint32_t kStep = 16 * 128 / 16;
     const uint32_t a0 = desc_lo(smem_u32(smem), kBox), b0 = desc_lo(smem_u32(smem) + kABytes, kBox);
-    for (int64_t t = unit; t < w.tiles && ok; t += units) {
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, x.n, 1, 1);
-      const int seg = segment((x.rows + kBK - 1) / kBK);
+      const int seg = segment<V>((x.rows + kBK - 1) / kBK);
       for (int left = x.rows; left > 0;) {
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (use & 1) * kAccCols;
         uint32_t add = 0;
-        for (int in = 0; in < seg && left > 0; ++in, left -= kBK) {
+        for (int in = 0; in < seg && left > 0; in += V::kSub, left -= kBK * V::kSub) {
           ok = wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
           if (!ok) break;
-          if (left < kBK && left % 16 != 0) {
+          if (left < kBK * V::kSub && left % 16 != 0) {
             // The rows behind the expert's last are the next expert's.
-            zero_rows(smem + ring.stage * S::kStage, left, 2 + (x.n / S::kCtas + 63) / 64, lane);
+            zero_rows(smem + ring.stage * S::kStage + left / kBK * S::kBlock, left % kBK,
+                      2 + (x.n / S::kCtas + 63) / 64, lane);
             if (V::kPair) {
               ok = __all_sync(0xffffffffu, wait_peer(&c.fixed[ring.stage], fixes >> ring.stage & 1,
                                                      g.err, &c.abort));
@@ -826,10 +944,14 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
           }
           const uint32_t a = a0 + ring.stage * (S::kStage / 16), b = b0 + ring.stage * (S::kStage / 16);
           if (elect_one()) {
-            mma<V::kPair>(d, a, b, idesc, add);
-            if (left > 16) mma<V::kPair>(d, a + kStep, b + kStep, idesc, 1);
-            if (left > 32) mma<V::kPair>(d, a + 2 * kStep, b + 2 * kStep, idesc, 1);
-            if (left > 48) mma<V::kPair>(d, a + 3 * kStep, b + 3 * kStep, idesc, 1);
+#pragma unroll
+            for (int j = 0; j < V::kSub; ++j) {
+              const uint32_t aj = a + j * (S::kBlock / 16), bj = b + j * (S::kBlock / 16);
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                if (left > j * kBK + s * 16)
+                  mma<V::kPair>(d, aj + s * kStep, bj + s * kStep, idesc, (j | s) == 0 ? add : 1);
+            }
             commit<V::kPair>(&c.empty[ring.stage]);
           }
           __syncwarp();
@@ -853,17 +975,18 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     // A stage's barriers are used again only after the MMAs that waited for this.
     int64_t fills = 0;
     uint32_t tails = 0;  // per stage: parity of the next use of its `tail` barrier
-    for (int64_t t = unit; t < w.tiles; t += units) {
+    for (uint32_t t = unit; t < tiles; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad);
-      fills += (x.rows + kBK - 1) / kBK;
-      const int left = x.rows % kBK;
+      fills += (x.rows + kBK * V::kSub - 1) / (kBK * V::kSub);
+      const int left = x.rows % (kBK * V::kSub);
       if (left % 16 == 0) continue;
       const int stage = (int)((fills - 1) % V::kStages);
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c.tail[stage], tails >> stage & 1, kWaitBudget,
                                                      g.err, &c.abort)))
         break;
       tails ^= 1u << stage;
-      zero_rows(smem + stage * S::kStage, left, 2 + (x.n / S::kCtas + 63) / 64, lane);
+      zero_rows(smem + stage * S::kStage + left / kBK * S::kBlock, left % kBK,
+                2 + (x.n / S::kCtas + 63) / 64, lane);
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&c.fixed[stage]), 0));
     }
   } else if (warp >= 4) {
@@ -872,61 +995,72 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
         reinterpret_cast<float4*>(smem + V::kStages * S::kStage + (warp - 4) * kWgradStaging);
     int use = 0;
     bool ok = true;
-    for (int64_t t = unit; t < w.tiles && ok; t += units) {
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad);
       if (x.rows == 0 && g.accumulate) continue;
+      const int row = x.i0 + kBM * (int)rank + 32 * q;
+      float* dw = g.dw + x.expert * g.dw_stride + (int64_t)row * g.lddw + x.j0;
+      // The sums start from the old values, which arrive while the MMAs run.
       float sum[S::kBlocks][32];
-      if (x.rows == 0)
+      if (g.accumulate || x.rows == 0)
 #pragma unroll
         for (int i = 0; i < S::kBlocks; ++i)
-#pragma unroll
-          for (int k = 0; k < 32; ++k) sum[i][k] = 0.f;
-      const int seg = segment((x.rows + kBK - 1) / kBK);
+          wgrad_load(dw + lane * g.lddw + (2 * i + half) * 32,
+                     g.accumulate && row + lane < g.m ? x.cols - (2 * i + half) * 32 : 0, sum[i]);
+      const int seg = segment<V>((x.rows + kBK - 1) / kBK);
       for (int r = 0; r < x.rows; r += seg * kBK, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < S::kBlocks; ++i)
           if ((2 * i + half) * 32 < x.n)
-            add_acc(tmem, use & 1, q, (2 * i + half) * 32, r == 0, sum[i]);
+            add_acc(tmem, use & 1, q, (2 * i + half) * 32, r == 0 && !g.accumulate, sum[i]);
         release_acc<V::kPair>(c, use & 1, rank, lane);
       }
       if (!ok) break;
-      const int row = x.i0 + kBM * (int)rank + 32 * q;
-      float* dw = g.dw + x.expert * g.dw_stride + (int64_t)row * g.lddw + x.j0;
 #pragma unroll
       for (int i = 0; i < S::kBlocks; ++i) {
         const int col = (2 * i + half) * 32;
         if (col >= x.cols || row >= g.m) continue;
         if (p.bulk) wgrad_store_bulk(&p.dw, x.expert, row, x.j0 + col, lane, sum[i], stage);
-        else wgrad_store(g, dw + col, g.m - row, x.cols - col, lane, sum[i], stage);
+        else wgrad_store(dw + col, g.lddw, g.m - row, x.cols - col, lane, sum[i], stage);
       }
     }
     // Shared memory must outlive the stores that read it.
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
-  teardown<V::kPair>(c, warp);
+  teardown<V>(c, warp);
 }
 
 // ---------------------------------------------------------------------------- operand copies
-// Copies a batch of row-major 16-bit matrices to rows that start on 16 bytes (TMA wants its
+// Copies batches of row-major 16-bit matrices to rows that start on 16 bytes (TMA wants its
 // pointers and strides in units of 16 bytes), zeros behind each row's last element.
-__global__ void __launch_bounds__(256)
-align_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t stride, int64_t rows,
-                  int64_t cols, int64_t chunks, int64_t total, uint4* __restrict__ dst) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / chunks, c0 = (i - row * chunks) * 8;
-    const int64_t batch = row / rows;
-    const uint16_t* s = src + batch * stride + (row - batch * rows) * ld + c0;
+struct AlignCopy {
+  const uint16_t* src;
+  int64_t ld, stride, rows, cols, chunks, total;  // total 16-byte chunks; 0: nothing to copy
+  uint4* dst;
+};
+
+__device__ __forceinline__ void align_rows(const AlignCopy& c) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < c.total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / c.chunks, c0 = (i - row * c.chunks) * 8;
+    const int64_t batch = row / c.rows;
+    const uint16_t* s = c.src + batch * c.stride + (row - batch * c.rows) * c.ld + c0;
     uint32_t v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = c0 + 2 * e < cols ? s[2 * e] : 0, hi = c0 + 2 * e + 1 < cols ? s[2 * e + 1] : 0;
+      const uint32_t lo = c0 + 2 * e < c.cols ? s[2 * e] : 0;
+      const uint32_t hi = c0 + 2 * e + 1 < c.cols ? s[2 * e + 1] : 0;
       v[e] = lo | hi << 16;
     }
-    dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    c.dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
   }
+}
+
+__global__ void __launch_bounds__(256) align_rows_kernel(const AlignCopy a, const AlignCopy b) {
+  align_rows(a);
+  align_rows(b);
 }
 
 // One operand as the tensor maps see it: `batch` matrices of rows x cols.
@@ -945,19 +1079,30 @@ size_t copy_bytes(const Operand& o) {
   return (size_t)split_part_bytes(o.batch * o.rows * ((o.cols + 7) / 8) * 16);
 }
 
-// Replaces an operand by its aligned copy at *at in the workspace, if it needs one.
-cudaError_t align_operand(Operand* o, uint8_t** at, int sms, cudaStream_t st) {
+// Replaces an operand by its aligned copy at *at in the workspace, if it needs one; returns the
+// copy to make.
+AlignCopy align_operand(Operand* o, uint8_t** at) {
+  AlignCopy c{};
   const size_t bytes = copy_bytes(*o);
-  if (bytes == 0) return cudaSuccess;
-  const int64_t chunks = (o->cols + 7) / 8, total = o->batch * o->rows * chunks;
-  const int64_t blocks = (total + 255) / 256, cap = (int64_t)sms * 8;
-  align_rows_kernel<<<(int)(blocks < cap ? blocks : cap), 256, 0, st>>>(
-      static_cast<const uint16_t*>(o->ptr), o->ld, o->stride, o->rows, o->cols, chunks, total,
-      reinterpret_cast<uint4*>(*at));
+  if (bytes == 0) return c;
+  const int64_t chunks = (o->cols + 7) / 8;
+  c = {static_cast<const uint16_t*>(o->ptr), o->ld, o->stride, o->rows, o->cols, chunks,
+       o->batch * o->rows * chunks, reinterpret_cast<uint4*>(*at)};
   o->ptr = *at;
   o->ld = chunks * 8;
   o->stride = o->rows * o->ld;
   *at += bytes;
+  return c;
+}
+
+// Makes both operands' rows start on 16 bytes.
+cudaError_t align_operands(Operand* a, Operand* b, void* workspace, int sms, cudaStream_t st) {
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  const AlignCopy ca = align_operand(a, &at), cb = align_operand(b, &at);
+  const int64_t total = ca.total > cb.total ? ca.total : cb.total;
+  if (total == 0) return cudaSuccess;
+  const int64_t blocks = (total + 255) / 256, cap = (int64_t)sms * 8;
+  align_rows_kernel<<<(int)(blocks < cap ? blocks : cap), 256, 0, st>>>(ca, cb);
   return cudaGetLastError();
 }
 
@@ -992,8 +1137,8 @@ cudaError_t encode(CUtensorMap* map, const Operand& o, int32_t dtype, bool batch
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Launches a persistent kernel of `ctas`-CTA units; its shared-memory size is set once per
-// device.
+// Launches at most one CTA per SM, in clusters of `ctas`, for `tiles` tiles; the kernel's
+// shared-memory size is set once per device.
 template <typename P>
 cudaError_t launch(void (*kernel)(P), const P& p, int64_t tiles, int ctas, int sms, int smem,
                    std::atomic<uint64_t>* ready, cudaStream_t st) {
@@ -1006,8 +1151,18 @@ cudaError_t launch(void (*kernel)(P), const P& p, int64_t tiles, int ctas, int s
     ready->fetch_or(1ull << dev, std::memory_order_release);
   }
   const int64_t most = sms / ctas, units = tiles < 1 ? 1 : tiles < most ? tiles : most;
-  kernel<<<(unsigned)(units * ctas), kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * ctas), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // At least as many tiles as the offsets can make of the rows.
@@ -1018,17 +1173,17 @@ int64_t mm_tiles(const GroupedMm& g) {
 }
 
 template <typename V, typename O>
-cudaError_t launch_mm(const MmParams& p, int sms, cudaStream_t st) {
+cudaError_t launch_mm(const MmParams& p, int parts, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  return launch(grouped_mm_kernel<V, O>, p, mm_tiles<V>(p.g), Shape<V>::kCtas, sms,
-                V::kStages * Shape<V>::kStage + kEpiWarps * kMmStaging + 1024, &ready, st);
+  return launch(grouped_mm_kernel<V, O>, p, mm_tiles<V>(p.g), Shape<V>::kCtas * parts, sms,
+                V::kStages * Shape<V>::kStage + 1024, &ready, st);
 }
 
 template <typename V>
-cudaError_t launch_mm_as(const MmParams& p, int sms, cudaStream_t st) {
-  return p.g.out_dtype == kF32 ? launch_mm<V, float>(p, sms, st)
-         : p.g.out_dtype == kBf16 ? launch_mm<V, __nv_bfloat16>(p, sms, st)
-                                  : launch_mm<V, __half>(p, sms, st);
+cudaError_t launch_mm_as(const MmParams& p, int parts, int sms, cudaStream_t st) {
+  return p.g.out_dtype == kF32 ? launch_mm<V, float>(p, parts, sms, st)
+         : p.g.out_dtype == kBf16 ? launch_mm<V, __nv_bfloat16>(p, parts, sms, st)
+                                  : launch_mm<V, __half>(p, parts, sms, st);
 }
 
 template <typename V>
@@ -1059,38 +1214,43 @@ cudaError_t launch_grouped_mm(const GroupedMm& g, void* workspace, int sms, cuda
   MmParams p;
   p.g = g;
   Operand x = x_of(g), w = w_of(g);
-  uint8_t* at = static_cast<uint8_t*>(workspace);
-  cudaError_t e = align_operand(&x, &at, sms, st);
-  if (e == cudaSuccess) e = align_operand(&w, &at, sms, st);
+  cudaError_t e = align_operands(&x, &w, workspace, sms, st);
+  // (Row tiles are whole or an expert's last; the device counts tiles in 32 bits.)
+  if ((g.rows / Narrow::kMaxN + g.n_experts) * (int64_t)((g.n - 1) / kBM + 1) > INT32_MAX)
+    return cudaErrorInvalidConfiguration;
+  // A k-split where every cluster gets an SM for each of its CTAs, and one tile.
+  int parts = 1;
+  while (parts < kMostParts && mm_tiles<Split>(g) * parts * 2 <= sms && g.k >= 4 * kBK * parts * 2)
+    parts *= 2;
   // Few rows per expert: streaming the weights is the whole cost.
   const bool narrow = g.rows <= 64 || g.rows <= 32 * (int64_t)g.n_experts;
   const bool pair = !narrow && g.n > kBM && mm_tiles<Pair>(g) >= sms / 2;
   if (e == cudaSuccess)
-    e = encode(&p.x, x, g.dtype, false, narrow ? Narrow::kBoxRows : Wide::kBoxRows);
+    e = encode(&p.x, x, g.dtype, false, parts > 1 || narrow ? Narrow::kBoxRows : Wide::kBoxRows);
   if (e == cudaSuccess) e = encode(&p.w, w, g.dtype, true, g.trans ? kBM : 64);
   if (e != cudaSuccess) return e;
-  return narrow ? launch_mm_as<Narrow>(p, sms, st)
-         : pair ? launch_mm_as<Pair>(p, sms, st) : launch_mm_as<Wide>(p, sms, st);
+  return parts > 1 ? launch_mm_as<Split>(p, parts, sms, st)
+         : narrow  ? launch_mm_as<Narrow>(p, 1, sms, st)
+         : pair    ? launch_mm_as<Pair>(p, 1, sms, st) : launch_mm_as<Wide>(p, 1, sms, st);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms, cudaStream_t st) {
   WgradParams p;
   p.g = g;
   Operand a = a_of(g), b = b_of(g);
-  uint8_t* at = static_cast<uint8_t*>(workspace);
   cudaError_t e = cudaSuccess;
   if (g.rows > 0) {  // without rows nothing is loaded: the maps stay unused
-    e = align_operand(&a, &at, sms, st);
-    if (e == cudaSuccess) e = align_operand(&b, &at, sms, st);
+    e = align_operands(&a, &b, workspace, sms, st);
     if (e == cudaSuccess) e = encode(&p.a, a, g.dtype, false, 64);
     if (e == cudaSuccess) e = encode(&p.b, b, g.dtype, false, 64);
   }
-  // Written by TMA where every row of dw starts on 16 bytes; adding needs the old values.
-  p.bulk = !g.accumulate && reinterpret_cast<uintptr_t>(g.dw) % 16 == 0 && g.lddw % 4 == 0 &&
+  // Written by TMA where every row of dw starts on 16 bytes.
+  p.bulk = reinterpret_cast<uintptr_t>(g.dw) % 16 == 0 && g.lddw % 4 == 0 &&
            (g.n_experts == 1 || g.dw_stride % 4 == 0);
   if (e == cudaSuccess && p.bulk)
     e = encode(&p.dw, {g.dw, g.m, g.n, g.lddw, g.n_experts, g.dw_stride}, kF32, true, 32);
   if (e != cudaSuccess) return e;
+  if (wgrad_grid<Wide>(g).tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   const bool pair = g.m > kBM && wgrad_grid<Pair>(g).tiles >= sms / 2;
   return pair ? launch_wgrad<Pair>(p, sms, st) : launch_wgrad<Wide>(p, sms, st);
 }
