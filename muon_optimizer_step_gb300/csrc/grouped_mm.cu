@@ -107,6 +107,7 @@ struct WgradParams {
   CUtensorMap a, b;  // (columns, rows): boxes of 64 x 64
   CUtensorMap dw;    // (column, row, expert) of the result: boxes of 32 x 32
   GroupedWgrad g;
+  int32_t max_n;     // widest tile
   bool bulk;         // dw is written by TMA
 };
 
@@ -737,10 +738,10 @@ struct WgradGrid {
 };
 
 template <typename V>
-__host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g) {
+__host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g, int max_n) {
   WgradGrid w;
   w.m_tiles = (g.m - 1) / Shape<V>::kM + 1;
-  w.n_tiles = (g.n - 1) / V::kMaxN + 1;
+  w.n_tiles = (uint32_t)(g.n - 1) / (uint32_t)max_n + 1;
   w.width = (int)((uint32_t)(g.n - 1) / w.n_tiles + kWgradStep) / kWgradStep * kWgradStep;  // columns dealt evenly
   w.tiles = (int64_t)g.n_experts * w.m_tiles * w.n_tiles;
   return w;
@@ -849,7 +850,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
   if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(g.err, kErrRowOffsets);
   sync_ctas<V::kPair>();
   const uint32_t tmem = c.tmem;
-  const WgradGrid w = wgrad_grid<V>(g);
+  const WgradGrid w = wgrad_grid<V>(g, p.max_n);
   const uint32_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas, tiles = (uint32_t)w.tiles;
 
   if (warp == 0) {
@@ -1189,7 +1190,7 @@ cudaError_t launch_mm_as(const MmParams& p, int parts, int sms, cudaStream_t st)
 template <typename V>
 cudaError_t launch_wgrad(const WgradParams& p, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  return launch(grouped_wgrad_kernel<V>, p, wgrad_grid<V>(p.g).tiles, Shape<V>::kCtas, sms,
+  return launch(grouped_wgrad_kernel<V>, p, wgrad_grid<V>(p.g, p.max_n).tiles, Shape<V>::kCtas, sms,
                 V::kStages * Shape<V>::kStage + kEpiWarps * kWgradStaging + 1024, &ready, st);
 }
 
@@ -1222,8 +1223,8 @@ cudaError_t launch_grouped_mm(const GroupedMm& g, void* workspace, int sms, cuda
   int parts = 1;
   while (parts < kMostParts && mm_tiles<Split>(g) * parts * 2 <= sms && g.k >= 4 * kBK * parts * 2)
     parts *= 2;
-  // Few rows per expert: streaming the weights is the whole cost.
-  const bool narrow = g.rows <= 64 || g.rows <= 32 * (int64_t)g.n_experts;
+  // Few rows per expert: streaming the weights is the whole cost.  Few tiles: the more SMs work.
+  const bool narrow = g.rows <= 64 || g.rows <= 32 * (int64_t)g.n_experts || mm_tiles<Narrow>(g) <= sms;
   const bool pair = !narrow && g.n > kBM && mm_tiles<Pair>(g) >= sms / 2;
   if (e == cudaSuccess)
     e = encode(&p.x, x, g.dtype, false, parts > 1 || narrow ? Narrow::kBoxRows : Wide::kBoxRows);
@@ -1250,9 +1251,13 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
   if (e == cudaSuccess && p.bulk)
     e = encode(&p.dw, {g.dw, g.m, g.n, g.lddw, g.n_experts, g.dw_stride}, kF32, true, 32);
   if (e != cudaSuccess) return e;
-  if (wgrad_grid<Wide>(g).tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const bool pair = g.m > kBM && wgrad_grid<Pair>(g).tiles >= sms / 2;
-  return pair ? launch_wgrad<Pair>(p, sms, st) : launch_wgrad<Wide>(p, sms, st);
+  if (wgrad_grid<Wide>(g, 64).tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  p.max_n = 256;
+  if (g.m > kBM && wgrad_grid<Pair>(g, 256).tiles >= sms / 2) return launch_wgrad<Pair>(p, sms, st);
+  // Few tiles: narrower ones, while every SM gets at most one (13 experts of 130 x 520, 154 rows
+  // each: 15 -> 12 us).
+  while (p.max_n > 64 && wgrad_grid<Wide>(g, p.max_n / 2).tiles <= sms) p.max_n /= 2;
+  return launch_wgrad<Wide>(p, sms, st);
 }
 
 }  // namespace muon
