@@ -750,13 +750,15 @@ __host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g, 
 template <typename V>
 __device__ __forceinline__ WgradTile wgrad_tile(const GroupedWgrad& g, const WgradGrid& w, uint32_t t,
                                                 bool bad) {
-  const uint32_t per = w.m_tiles * w.n_tiles, e = t / per, r = t - e * per, i = r / w.n_tiles;
+  // Row tiles first: the CTAs at work at a time share column panels of b (446 against 450 us on
+  // 64 x 2048 x 1408 in a long run, 407 against 414 in a short one).
+  const uint32_t per = w.m_tiles * w.n_tiles, e = t / per, r = t - e * per, j = r / w.m_tiles;
   WgradTile x;
   x.expert = e;
   x.row = bad ? 0 : (int)g.offsets[e];
   x.rows = bad ? 0 : (int)(g.offsets[e + 1] - g.offsets[e]);
-  x.i0 = (int)i * Shape<V>::kM;
-  x.j0 = (int)(r - i * w.n_tiles) * w.width;
+  x.i0 = (int)(r - j * w.m_tiles) * Shape<V>::kM;
+  x.j0 = (int)j * w.width;
   x.cols = min(w.width, g.n - x.j0);
   x.n = (x.cols + kWgradStep - 1) / kWgradStep * kWgradStep;
   return x;
