@@ -8,9 +8,9 @@
 // block of the second launch adds those sums in the same fixed order (about ten kilobytes
 // from L2), so no block waits on another, no atomic decides an order, and the result does
 // not depend on timing.  Both are bound by HBM: the gradients are read twice unless L2
-// still holds them, which is why the second launch walks the chunks backwards.
+// still holds them, which is why the second launch walks each block's chunks backwards.
 //
-// Sums: a thread adds at most kChunk / kThreads squares in fp32, then goes on in double.
+// Sums: a thread adds at most 32 squares in fp32 (in four sums), then goes on in double.
 // A thread whose fp32 sum overflowed, or is so small that squares may have been flushed,
 // takes those elements again in double, so the whole fp32 range is covered.
 #include "device_common.cuh"
@@ -22,12 +22,13 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 8;
-constexpr int kChunk = 8192;  // elements: 32 per thread, every load of which is in flight at once
+constexpr int kBlocksPerSm = 4;
+constexpr int kChunkBytes = 16384;  // 64 per thread, every load of which is in flight at once
+constexpr int kIter = kChunkBytes / 16 / kThreads;
 
-// One tensor of a launch.  Chunk j of the tensor covers elements j * kChunk - mis to
-// (j + 1) * kChunk - mis, where mis elements separate its start from the 16-byte boundary
-// below: every chunk's vectors are aligned wherever the tensor starts.
+// One tensor of a launch.  Chunk j of the tensor covers bytes j * kChunkBytes to
+// (j + 1) * kChunkBytes counted from the 16-byte boundary below its start, mis elements before
+// it: every chunk's vectors are aligned wherever the tensor starts.
 struct TensorRec {
   const void* g;
   void* out;
@@ -43,27 +44,35 @@ struct TensorArgs {
   int32_t n, n_chunks;
 };
 
+// Index of the tensor that holds a chunk.
 template <int N>
-__device__ __forceinline__ const TensorRec& find_tensor(const TensorArgs<N>& a, int chunk) {
+__device__ __forceinline__ int find_tensor(const TensorArgs<N>& a, int chunk) {
   int lo = 0, hi = a.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (a.t[mid].chunk_begin <= chunk) lo = mid; else hi = mid - 1;
   }
-  return a.t[lo];
+  return lo;
+}
+
+// Block b's chunks: an equal share in one run, so that the tensor is looked up once.
+template <int N>
+__device__ __forceinline__ int2 chunk_range(const TensorArgs<N>& a) {
+  return make_int2((int)((int64_t)a.n_chunks * blockIdx.x / gridDim.x),
+                   (int)((int64_t)a.n_chunks * (blockIdx.x + 1) / gridDim.x));
 }
 
 // This thread's elements of a chunk: kIter vectors of kVec.
 template <typename T>
 struct ChunkIter {
   static constexpr int kVec = 16 / sizeof(T);
-  static constexpr int kIter = kChunk / kThreads / kVec;
+  // First element of vector u (before or behind the tensor's elements, or across its ends, in
+  // its first and last chunk).
   __device__ static int64_t first(const TensorRec& t, int64_t j, int u) {
-    return j * kChunk + (int64_t)(threadIdx.x + u * kThreads) * kVec - t.mis;
+    return j * (kChunkBytes / (int)sizeof(T)) + (threadIdx.x + u * kThreads) * kVec - t.mis;
   }
-  // Loads vector u of chunk j; elements outside the tensor read as zero.
-  __device__ static void load(const TensorRec& t, int64_t j, int u, T (&v)[kVec]) {
-    const int64_t i = first(t, j, u);
+  // Elements outside the tensor read as zero.
+  __device__ static void load(const TensorRec& t, int64_t i, T (&v)[kVec]) {
     const T* g = static_cast<const T*>(t.g);
     if (i >= 0 && i + kVec <= t.numel) {
       const uint4 q = *reinterpret_cast<const uint4*>(g + i);
@@ -79,13 +88,13 @@ struct ChunkIter {
 template <typename T>
 __device__ __forceinline__ double chunk_sum(const TensorRec& t, int64_t j) {
   using C = ChunkIter<T>;
-  T v[C::kIter][C::kVec];
+  T v[kIter][C::kVec];
 #pragma unroll
-  for (int u = 0; u < C::kIter; ++u) C::load(t, j, u, v[u]);
+  for (int u = 0; u < kIter; ++u) C::load(t, C::first(t, j, u), v[u]);
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   bool nonzero = false;
 #pragma unroll
-  for (int u = 0; u < C::kIter; ++u)
+  for (int u = 0; u < kIter; ++u)
 #pragma unroll
     for (int e = 0; e < C::kVec; ++e) {
       const float f = cvt(v[u][e]);
@@ -95,15 +104,18 @@ __device__ __forceinline__ double chunk_sum(const TensorRec& t, int64_t j) {
   const float sum = (s[0] + s[1]) + (s[2] + s[3]);
   if (nonzero && !(sum >= 0x1p-100f && sum <= 0x1p126f)) {
     double d = 0.0;
-    for (int u = 0; u < C::kIter; ++u)
-      for (int e = 0; e < C::kVec; ++e) {
-        const double f = (double)cvt(v[u][e]);
-        d = fma(f, f, d);
-      }
+#pragma unroll 1
+    for (int u = 0; u < kIter; ++u) {  // read again: rare
+      T w[C::kVec];
+      C::load(t, C::first(t, j, u), w);
+#pragma unroll
+      for (int e = 0; e < C::kVec; ++e) d = fma((double)cvt(w[e]), (double)cvt(w[e]), d);
+    }
     return d;
   }
   return (double)sum;
 }
+static_assert(kIter == 4, "chunk_sum and the bound on a thread's squares");
 
 // The same order every run; the result is valid in every thread.
 __device__ __forceinline__ double block_sum(double v, double* red) {
@@ -119,12 +131,15 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 sum_squares_kernel(const __grid_constant__ TensorArgs<N> a, double* __restrict__ partials) {
   __shared__ double red[kThreads / 32];
   double s = 0.0;
-  for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-    const TensorRec& t = find_tensor(a, c);
+  const int2 r = chunk_range(a);
+  int i = r.x < r.y ? find_tensor(a, r.x) : 0;
+  for (int c = r.x; c < r.y; ++c) {
+    while (i + 1 < a.n && a.t[i + 1].chunk_begin <= c) ++i;
+    const TensorRec& t = a.t[i];
     const int64_t j = c - t.chunk_begin;
     s += t.dtype == kF32 ? chunk_sum<float>(t, j)
          : t.dtype == kBf16 ? chunk_sum<__nv_bfloat16>(t, j) : chunk_sum<__half>(t, j);
@@ -157,49 +172,47 @@ norm_kernel(const double* __restrict__ partials, int n, float max_norm, float* _
 template <typename T, typename O>
 __device__ __forceinline__ void scale_chunk(const TensorRec& t, int64_t j, float c) {
   using C = ChunkIter<T>;
-  T v[C::kIter][C::kVec];
+  constexpr int kVec = C::kVec, kPieces = kVec * sizeof(O) / 16;  // 16-byte pieces out
+  T v[kIter][kVec];
+#pragma unroll
+  for (int u = 0; u < kIter; ++u) C::load(t, C::first(t, j, u), v[u]);
   O* out = static_cast<O*>(t.out);
 #pragma unroll
-  for (int u = 0; u < C::kIter; ++u) C::load(t, j, u, v[u]);
-#pragma unroll
-  for (int u = 0; u < C::kIter; ++u) {
+  for (int u = 0; u < kIter; ++u) {
     const int64_t i = C::first(t, j, u);
-    __align__(16) O r[C::kVec];
+    O r[kVec];
 #pragma unroll
-    for (int e = 0; e < C::kVec; ++e) put(&r[e], cvt(v[u][e]) * c);
-    constexpr int kBytes = C::kVec * sizeof(O);
-    constexpr int kPiece = kBytes < 16 ? kBytes : 16;
-    if (i >= 0 && i + C::kVec <= t.numel && reinterpret_cast<uintptr_t>(out + i) % kPiece == 0) {
+    for (int e = 0; e < kVec; ++e) put(&r[e], cvt(v[u][e]) * c);
+    if (i >= 0 && i + kVec <= t.numel && reinterpret_cast<uintptr_t>(out + i) % 16 == 0) {
 #pragma unroll
-      for (int b = 0; b < kBytes; b += kPiece) {
-        if constexpr (kPiece == 16)
-          *reinterpret_cast<uint4*>(reinterpret_cast<char*>(out + i) + b) =
-              *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(r) + b);
-        else
-          *reinterpret_cast<uint2*>(reinterpret_cast<char*>(out + i) + b) =
-              *reinterpret_cast<const uint2*>(reinterpret_cast<const char*>(r) + b);
+      for (int b = 0; b < kPieces; ++b) {
+        uint4 q;
+        memcpy(&q, r + b * (kVec / kPieces), 16);
+        reinterpret_cast<uint4*>(out + i)[b] = q;
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < C::kVec; ++e)
+      for (int e = 0; e < kVec; ++e)
         if (i + e >= 0 && i + e < t.numel) out[i + e] = r[e];
     }
   }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 clip_kernel(const __grid_constant__ TensorArgs<N> a, const double* __restrict__ partials,
             int n_partials, float max_norm, float* __restrict__ norm) {
   __shared__ double red[kThreads / 32];
+  const int2 r = chunk_range(a);
+  int i = r.x < r.y ? find_tensor(a, r.y - 1) : 0;
   const float2 nc = norm_and_coef(partials, n_partials, max_norm, red);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     norm[0] = nc.x;
     norm[1] = nc.y;
   }
-  for (int b = blockIdx.x; b < a.n_chunks; b += gridDim.x) {
-    const int c = a.n_chunks - 1 - b;
-    const TensorRec& t = find_tensor(a, c);
+  for (int c = r.y - 1; c >= r.x; --c) {
+    while (a.t[i].chunk_begin > c) --i;
+    const TensorRec& t = a.t[i];
     if (nc.y == 1.f && t.out == t.g) continue;  // in place and not clipped: already there
     const int64_t j = c - t.chunk_begin;
     if (t.dtype == kF32) scale_chunk<float, float>(t, j, nc.y);
@@ -211,8 +224,8 @@ clip_kernel(const __grid_constant__ TensorArgs<N> a, const double* __restrict__ 
 }
 
 // Kernel arguments hold up to kMany records by value (they must stay below 32,764 bytes);
-// calls with few tensors take the small form, whose launch copies less.
-constexpr int kFew = 32, kMany = 960;
+// calls with fewer tensors take smaller forms, whose launches copy less.
+constexpr int kFew = 32, kSome = 256, kMany = 960;
 static_assert(sizeof(TensorArgs<kMany>) + 64 < 32764, "kernel arguments too large");
 
 int esize(int dtype) { return dtype == kF32 ? 4 : 2; }
@@ -222,7 +235,8 @@ int64_t misalign(const TensorSpec& g) {
 }
 
 int64_t chunks_of(const TensorSpec& g) {
-  return g.numel == 0 ? 0 : (g.numel + misalign(g) + kChunk - 1) / kChunk;
+  const int64_t chunk = kChunkBytes / esize(g.dtype);
+  return g.numel == 0 ? 0 : (g.numel + misalign(g) + chunk - 1) / chunk;
 }
 
 // The tensors from *at on that one launch takes; outs may be null (norm only).
@@ -291,7 +305,7 @@ size_t clip_workspace_bytes(const TensorSpec* grads, int n, int sms) {
   // One double per block of the summing launches (kMany tensors each, or all in one); a
   // bound that holds wherever the tensors start.
   int64_t chunks = 0;
-  for (int i = 0; i < n; ++i) chunks += grads[i].numel > 0 ? grads[i].numel / kChunk + 2 : 0;
+  for (int i = 0; i < n; ++i) chunks += grads[i].numel > 0 ? grads[i].numel * 4 / kChunkBytes + 2 : 0;
   const int64_t slots = (int64_t)((n + kMany - 1) / kMany) * sms * kBlocksPerSm;
   return (size_t)(chunks < slots ? chunks : slots) * sizeof(double);
 }
@@ -300,7 +314,8 @@ cudaError_t launch_clip(const TensorSpec* grads, const TensorSpec* outs, int n, 
                         float* norm, void* ws, int sms, cudaStream_t st) {
   double* partials = static_cast<double*>(ws);
   return n <= kFew ? run_clip<kFew>(grads, outs, n, max_norm, norm, partials, sms, st)
-                   : run_clip<kMany>(grads, outs, n, max_norm, norm, partials, sms, st);
+         : n <= kSome ? run_clip<kSome>(grads, outs, n, max_norm, norm, partials, sms, st)
+                      : run_clip<kMany>(grads, outs, n, max_norm, norm, partials, sms, st);
 }
 
 }  // namespace muon

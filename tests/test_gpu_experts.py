@@ -261,6 +261,25 @@ def test_wgrad_long_reduction_and_no_rows(capi):
     assert (dw == 0).all()
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("sizes,m,n,dstart", [
+    ([5000], 32, 216, 0),              # one tile, its rows split over a cluster
+    ([2300, 0, 4097, 1], 72, 136, 0),  # shares of very different lengths, one without rows
+    ([3001, 2], 130, 40, 3),           # two row tiles, dw off the 16-byte grid
+    ([9, 1500], 256, 65, 0),
+])
+def test_wgrad_rows_split_over_a_cluster(capi, sizes, m, n, dstart, accumulate):
+    _check_wgrad(capi, sizes, m, n, "bf16", accumulate, first=3, tail=5, dstart=dstart)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("sizes,k,n", [([1], 2048, 256), ([0, 3, 1, 0], 1600, 264),
+                                       ([33], 1090, 130), ([2], 4099, 77)])
+def test_mm_k_split_over_a_cluster(capi, sizes, k, n, trans):
+    for dtype, out in (("bf16", "bf16"), ("fp16", "fp32")):
+        _check_mm(capi, sizes, k, n, trans, dtype, out, first=1, tail=2)
+
+
 def test_wgrad_special_values_stay_with_their_expert(capi):
     gen = _gen(9)
     sizes = [20, 30, 91, 7]

@@ -1,7 +1,7 @@
 """The global gradient norm, clipping, and the step that takes the coefficient, on the GPU.
 
-Bounds (derived): a thread adds at most 32 squares in fp32 (each square and each addition
-rounds by 2^-24) and goes on in fp64, so the sum of squares is within 34 * 2^-24 of itself,
+Bounds (derived): a square passes at most 32 additions in fp32 (each square and each addition
+rounds by 2^-24) and the sums go on in fp64, so the sum of squares is within 34 * 2^-24 of itself,
 the norm within 17 * 2^-24 plus its own rounding (18 * 2^-24 in all), the coefficient within
 19 * 2^-24, and a clipped fp32 element within 20 * 2^-24 of coefficient * element."""
 import math
