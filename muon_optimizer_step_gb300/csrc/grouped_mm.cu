@@ -804,12 +804,13 @@ __device__ __forceinline__ void wgrad_load(const float* dst, int n, float (&v)[3
   }
 }
 
-// Writes, or adds to, the block dw[row .. row + 31, col .. col + 31] whose row `lane` the warp's
+// Writes, or (kAdd) adds to, the block dw[row .. row + 31, col .. col + 31] whose row `lane` the warp's
 // lane holds.
 // The block is turned around in `stage` (16-byte chunk k of row r in slot k ^ (r & 7), free of
 // bank conflicts on the way in), so that every access covers one row.
-__device__ __forceinline__ void wgrad_store(float* dw, int64_t lddw, int rows, int cols, bool add,
-                                            int lane, const float (&v)[32], float4* stage) {
+template <bool kAdd>
+__device__ __forceinline__ void wgrad_store(float* dw, int64_t lddw, int rows, int cols, int lane,
+                                            const float (&v)[32], float4* stage) {
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     stage[8 * lane + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -820,7 +821,7 @@ __device__ __forceinline__ void wgrad_store(float* dw, int64_t lddw, int rows, i
   };
   if (lane < cols) {
     dw += lane;
-    if (rows >= 32 && !add) {
+    if (rows >= 32 && !kAdd) {
 #pragma unroll
       for (int r = 0; r < 32; ++r, dw += lddw) *dw = at(r);
     } else {
@@ -829,7 +830,7 @@ __device__ __forceinline__ void wgrad_store(float* dw, int64_t lddw, int rows, i
       for (int r0 = 0; r0 < rows; r0 += 8, dw += 8 * lddw) {
         float o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = add && r0 + k < rows ? dw[k * lddw] : 0.f;
+        for (int k = 0; k < 8; ++k) o[k] = kAdd && r0 + k < rows ? dw[k * lddw] : 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (r0 + k < rows) dw[k * lddw] = o[k] + at(r0 + k);
@@ -890,7 +891,8 @@ __device__ __forceinline__ void wgrad_join(const WgradParams& p, uint8_t* smem, 
     }
     float* dw = g.dw + x.expert * g.dw_stride + (int64_t)row * g.lddw + x.j0 + col;
     if (p.bulk && !g.accumulate) wgrad_store_bulk(&p.dw, x.expert, row, x.j0 + col, lane, sum, stage);
-    else wgrad_store(dw, g.lddw, g.m - row, x.cols - col, g.accumulate, lane, sum, stage);
+    else if (g.accumulate) wgrad_store<true>(dw, g.lddw, g.m - row, x.cols - col, lane, sum, stage);
+    else wgrad_store<false>(dw, g.lddw, g.m - row, x.cols - col, lane, sum, stage);
   }
 }
 
@@ -1071,9 +1073,8 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
       if (x.rows == 0 && g.accumulate && !V::kSplit) continue;
       const int row = x.i0 + kBM * (int)rank + 32 * q;
       float* dw = g.dw + x.expert * g.dw_stride + (int64_t)row * g.lddw + x.j0;
-      // Where rows start on 16 bytes the sums start from the old values, which arrive while the
-      // MMAs run.
-      const bool old = g.accumulate && p.bulk && !V::kSplit;
+      // The sums start from the old values, which arrive while the MMAs run.
+      const bool old = g.accumulate && !V::kSplit;
       float sum[S::kBlocks][32];
       if (old || x.rows == 0)
 #pragma unroll
@@ -1102,7 +1103,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
         } else if (p.bulk) {
           wgrad_store_bulk(&p.dw, x.expert, row, x.j0 + col, lane, sum[i], stage);
         } else {
-          wgrad_store(dw + col, g.lddw, g.m - row, x.cols - col, g.accumulate, lane, sum[i], stage);
+          wgrad_store<false>(dw + col, g.lddw, g.m - row, x.cols - col, lane, sum[i], stage);
         }
       }
     }
@@ -1157,7 +1158,8 @@ __device__ __forceinline__ void align_rows(const AlignCopy& c) {
     const int64_t batch = row / c.rows;
     if (c.offsets != nullptr && c.offsets[batch + 1] <= c.offsets[batch]) continue;
     const uint16_t* s = c.src + batch * c.stride + (row - batch * c.rows) * c.ld;
-    for (int64_t q = lane; q < c.chunks; q += c.lanes) {
+    for (int64_t q = lane + (int64_t)blockIdx.y * c.lanes; q < c.chunks;
+         q += (int64_t)gridDim.y * c.lanes) {
       const int64_t c0 = q * 8;
       uint4 v;
       if (c0 + 8 <= c.cols) {
@@ -1226,8 +1228,12 @@ cudaError_t align_operands(Operand* a, Operand* b, const int64_t* offsets, void*
   const int64_t need = ca.total * ca.lanes > cb.total * cb.lanes ? ca.total * ca.lanes
                                                                  : cb.total * cb.lanes;
   if (need == 0) return cudaSuccess;
-  const int64_t blocks = (need + 255) / 256, cap = (int64_t)sms * 8;
-  align_rows_kernel<<<(int)(blocks < cap ? blocks : cap), 256, 0, st>>>(ca, cb);
+  // A thread takes one chunk of a row, more only where that is more than 8 blocks per SM.
+  const int64_t chunks = ca.chunks > cb.chunks ? ca.chunks : cb.chunks;
+  const int64_t cap = (int64_t)sms * 8, blocks = (need + 255) / 256 < cap ? (need + 255) / 256 : cap;
+  const int64_t across = (chunks + 31) / 32, room = cap / blocks;
+  align_rows_kernel<<<dim3((unsigned)blocks, (unsigned)(across < room ? across : room)), 256, 0, st>>>(
+      ca, cb);
   return cudaGetLastError();
 }
 
@@ -1380,14 +1386,14 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
   p.max_n = 256;
   if (g.m > kBM && wgrad_grid<Pair>(g, 256).tiles >= sms / 2)
     return launch_wgrad<Pair>(p, 1, sms, st);
-  // Few tiles: narrower ones, while every SM gets at most one (13 experts of 130 x 520, 154 rows
-  // each: 16.3 -> 14.2 us); then, with many rows, several CTAs for each.
-  while (p.max_n > 64 && wgrad_grid<Wide>(g, p.max_n / 2).tiles <= sms) p.max_n /= 2;
-  const int64_t tiles = wgrad_grid<Wide>(g, p.max_n).tiles;
+  // Few tiles: with many rows several CTAs for each (32 x 216 from 7855 rows 33.6 -> 12.6 us),
+  // then narrower ones, while every SM gets at most one (13 experts of 130 x 520 from 154 rows
+  // each 16.3 -> 10.5 us).
   int parts = 1;
-  while (parts < kMostParts && tiles * parts * 2 <= sms &&
-         g.rows >= (int64_t)g.n_experts * parts * 2 * 4 * kBK)
+  while (parts < kMostParts && wgrad_grid<Wide>(g, 256).tiles * parts * 2 <= sms &&
+         g.rows >= (int64_t)g.n_experts * parts * 8 * kBK)
     parts *= 2;
+  while (p.max_n > 64 && wgrad_grid<Wide>(g, p.max_n / 2).tiles * parts <= sms) p.max_n /= 2;
   return parts > 1 ? launch_wgrad<SplitWide>(p, parts, sms, st) : launch_wgrad<Wide>(p, 1, sms, st);
 }
 
