@@ -305,6 +305,8 @@ muon_status muon_orthogonalize_full_noalloc(const muon_layout* layout, const flo
  * row pitches in elements (at least the row length); *_stride is the distance in elements
  * between two experts' matrices, so they may lie in a flat buffer among others.
  * Pointers need their element's alignment only.  Outputs must not overlap inputs.
+ * The first of these calls on a device allocates its error word: make it before any CUDA-graph
+ * capture.  The calls keep nothing between them and may be used from several threads.
  * Arithmetic.  Products of the 16-bit inputs are summed in fp32 and rounded once, at the
  * store. */
 typedef enum muon_dtype {

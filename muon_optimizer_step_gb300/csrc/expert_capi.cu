@@ -23,7 +23,10 @@ muon_status fail(muon_status s, const char* fmt, ...) {
   va_start(ap, fmt);
   std::vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  set_last_error(buf);
+  try {
+    set_last_error(buf);
+  } catch (...) {  // no memory for the message: the status still goes back
+  }
   return s;
 }
 
@@ -123,6 +126,7 @@ muon_status check_mm(const GroupedMm& g) {
   EXPERT_TRY(check_pitch(g.ldw, g.trans ? g.k : g.n, "ldw"));
   EXPERT_TRY(check_pitch(g.ldy, g.n, "ldy"));
   if (g.n_experts > 1) EXPERT_TRY(check_pitch(g.w_stride, 1, "w_stride"));
+  if (!grouped_mm_fits(g)) return fail(MUON_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles of y");
   if (g.rows > 0) {
     EXPERT_TRY(check_ptr(g.x, 2, "x"));
     EXPERT_TRY(check_ptr(g.w, 2, "w"));
@@ -195,6 +199,8 @@ muon_status clip(const muon_tensor* grads, const muon_tensor* outs, bool scale, 
       if (outs[i].dtype != grads[i].dtype && outs[i].dtype != MUON_DTYPE_F32)
         return fail(MUON_ERR_INVALID_ARG, "outs[%d].dtype=%d: grads[%d]'s (%d) or fp32", i,
                     outs[i].dtype, i, grads[i].dtype);
+      if (outs[i].data == grads[i].data && outs[i].dtype != grads[i].dtype && outs[i].numel > 0)
+        return fail(MUON_ERR_INVALID_ARG, "outs[%d] is grads[%d] in another type", i, i);
     }
   }
   if (!(max_norm >= 0.f) || !std::isfinite(max_norm))

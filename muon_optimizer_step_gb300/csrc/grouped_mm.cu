@@ -1256,8 +1256,9 @@ cudaError_t encode(CUtensorMap* map, const Operand& o, int32_t dtype, bool batch
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t size = dtype == kF32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.batch};
+  // (The stride of a dimension of length 1 means nothing, but has to be a valid one.)
   const cuuint64_t strides[2] = {(cuuint64_t)o.ld * size,
-                                 (cuuint64_t)(o.batch == 1 ? o.rows * o.ld : o.stride) * size};
+                                 (cuuint64_t)(o.batch == 1 ? o.ld : o.stride) * size};
   const cuuint32_t box[3] = {(cuuint32_t)(128 / size), box_rows, 1}, unit[3] = {1, 1, 1};
   const CUresult r = fn(map, dtype == kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                              : dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -1334,6 +1335,15 @@ Operand b_of(const GroupedWgrad& g) { return {g.b, g.rows, g.n, g.ldb, 1, 0}; }
 
 }  // namespace
 
+// The device counts tiles in 32 bits.
+bool grouped_mm_fits(const GroupedMm& g) {
+  return (g.rows / Narrow::kMaxN + g.n_experts) * (int64_t)((g.n - 1) / kBM + 1) <= INT32_MAX;
+}
+
+bool grouped_wgrad_fits(const GroupedWgrad& g) {
+  return (int64_t)g.n_experts * ((g.m - 1) / kBM + 1) * ((g.n - 1) / 64 + 1) <= INT32_MAX;
+}
+
 size_t grouped_mm_workspace(const GroupedMm& g) {
   return g.rows == 0 ? 0 : copy_bytes(x_of(g)) + copy_bytes(w_of(g));
 }
@@ -1347,9 +1357,6 @@ cudaError_t launch_grouped_mm(const GroupedMm& g, void* workspace, int sms, cuda
   p.g = g;
   Operand x = x_of(g), w = w_of(g);
   cudaError_t e = align_operands(&x, &w, g.offsets, workspace, sms, st);
-  // (Row tiles are whole or an expert's last; the device counts tiles in 32 bits.)
-  if ((g.rows / Narrow::kMaxN + g.n_experts) * (int64_t)((g.n - 1) / kBM + 1) > INT32_MAX)
-    return cudaErrorInvalidConfiguration;
   // A k-split where every cluster gets an SM for each of its CTAs, and one tile.
   int parts = 1;
   while (parts < kMostParts && mm_tiles<Split>(g) * parts * 2 <= sms && g.k >= 4 * kBK * parts * 2)
@@ -1382,7 +1389,6 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
   if (e == cudaSuccess && p.bulk)
     e = encode(&p.dw, {g.dw, g.m, g.n, g.lddw, g.n_experts, g.dw_stride}, kF32, true, 32);
   if (e != cudaSuccess) return e;
-  if (wgrad_grid<Wide>(g, 64).tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   p.max_n = 256;
   if (g.m > kBM && wgrad_grid<Pair>(g, 256).tiles >= sms / 2)
     return launch_wgrad<Pair>(p, 1, sms, st);

@@ -118,6 +118,9 @@ struct GroupedWgrad {         // dw_e (+)= a^T b per expert (see muon_grouped_wg
   int32_t n_experts, m, n, accumulate, dtype;
   int* err;
 };
+// Whether the product has few enough tiles for one launch.
+bool grouped_mm_fits(const GroupedMm& g);
+bool grouped_wgrad_fits(const GroupedWgrad& g);
 size_t grouped_wgrad_workspace(const GroupedWgrad& g);
 cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms, cudaStream_t st);
 

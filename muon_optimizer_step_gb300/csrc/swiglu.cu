@@ -66,7 +66,7 @@ swiglu_kernel(const T* __restrict__ g, int64_t ldg, const T* __restrict__ u, int
        r += step) {
     const float w = p != nullptr ? p[r] : 1.f;
 #pragma unroll 2
-    for (int c = t * V; c < cols; c += kTpr * V) {
+    for (uint32_t c = t * V; c < (uint32_t)cols; c += kTpr * V) {
       const Vec<T, V> gv = load_vec<T, V>(g + r * ldg + c), uv = load_vec<T, V>(u + r * ldu + c);
       Vec<T, V> av;
 #pragma unroll
@@ -93,7 +93,7 @@ swiglu_grad_kernel(const T* __restrict__ da, int64_t ldda, const T* __restrict__
     const float w = p != nullptr ? p[r] : 1.f;
     float sum = 0.f;
 #pragma unroll 2
-    for (int c = t * V; c < cols; c += kTpr * V) {
+    for (uint32_t c = t * V; c < (uint32_t)cols; c += kTpr * V) {
       const Vec<T, V> dv = load_vec<T, V>(da + r * ldda + c), gv = load_vec<T, V>(g + r * ldg + c),
                       uv = load_vec<T, V>(u + r * ldu + c);
       Vec<T, V> gr, ur;

@@ -31,6 +31,7 @@ SG = dict(d=0x10000, ldd=8, g=0x20000, ldg=8, u=0x30000, ldu=8, p=None, dg=0x400
         (dict(w_stride=-2048), INV), (dict(ldx=1 << 40), INV), (dict(rows=-1), INV),
         (dict(rows=1 << 31), INV), (dict(experts=0), INV), (dict(experts=1025), INV), (dict(k=0), INV),
         (dict(n=-3), INV), (dict(dtype=F32), INV), (dict(dtype=3), INV), (dict(out=F16), INV),
+        (dict(rows=(1 << 31) - 1, n=(1 << 31) - 1, ldw=1 << 31, ldy=1 << 31), capi.MUON_ERR_UNSUPPORTED),
         (dict(x=0x10002), INV),                           # needs a workspace
         (dict(ldx=65, ws=0x50000, ws_bytes=16), INV),     # too small
         (dict(ldx=65, ws=0x50010, ws_bytes=1 << 20), ALIGN),
@@ -40,6 +41,7 @@ SG = dict(d=0x10000, ldd=8, g=0x20000, ldg=8, u=0x30000, ldu=8, p=None, dg=0x400
         (dict(off=None), INV), (dict(lda=63), INV), (dict(ldb=31), INV), (dict(lddw=31), INV),
         (dict(stride=31), INV), (dict(rows=-1), INV), (dict(experts=0), INV), (dict(m=0), INV),
         (dict(n=0), INV), (dict(dtype=F32), INV), (dict(ldb=33), INV),
+        (dict(m=1 << 30, lda=1 << 30, n=1 << 30, ldb=1 << 30, lddw=1 << 30, stride=1 << 31), capi.MUON_ERR_UNSUPPORTED),
     ]] + [
     (SW, "muon_swiglu", bad, status) for bad, status in [
         (dict(g=None), INV), (dict(u=0x20001), ALIGN), (dict(o=None), INV), (dict(ldg=7), INV),
@@ -70,6 +72,7 @@ def _list(*records):
     (_list((0x1000, 4, F32)), _list((0x1000, 5, F32)), 1, 1.0, 0x9000, INV),
     (_list((0x1000, 4, F32)), _list((0x1000, 4, BF16)), 1, 1.0, 0x9000, INV),
     (_list((0x1000, 4, BF16)), _list((0x1000, 4, F16)), 1, 1.0, 0x9000, INV),
+    (_list((0x1000, 4, BF16)), _list((0x1000, 4, F32)), 1, 1.0, 0x9000, INV),   # in place, wider
     (_list((0x1000, (1 << 64) - 4, F32)), _list((0x1000, (1 << 64) - 4, F32)), 1, 1.0, 0x9000, INV),
     (_list((0x1000, 4, F32)), _list((0x1000, 4, F32)), 1, -0.5, 0x9000, INV),
     (_list((0x1000, 4, F32)), _list((0x1000, 4, F32)), 1, float("nan"), 0x9000, INV),
