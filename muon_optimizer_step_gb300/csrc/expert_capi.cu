@@ -141,6 +141,7 @@ muon_status check_wgrad(const GroupedWgrad& g) {
   EXPERT_TRY(check_pitch(g.ldb, g.n, "ldb"));
   EXPERT_TRY(check_pitch(g.lddw, g.n, "lddw"));
   if (g.n_experts > 1) EXPERT_TRY(check_pitch(g.dw_stride, g.n, "dw_stride"));
+  if (!grouped_wgrad_fits(g)) return fail(MUON_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles of dw");
   if (g.rows > 0) {
     EXPERT_TRY(check_ptr(g.a, 2, "a"));
     EXPERT_TRY(check_ptr(g.b, 2, "b"));

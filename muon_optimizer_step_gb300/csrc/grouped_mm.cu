@@ -747,7 +747,8 @@ __host__ __device__ __forceinline__ WgradGrid wgrad_grid(const GroupedWgrad& g, 
   WgradGrid w;
   w.m_tiles = (g.m - 1) / Shape<V>::kM + 1;
   w.n_tiles = (uint32_t)(g.n - 1) / (uint32_t)max_n + 1;
-  w.width = (int)((uint32_t)(g.n - 1) / w.n_tiles + kWgradStep) / kWgradStep * kWgradStep;  // columns dealt evenly
+  // Columns dealt evenly.
+  w.width = (int)((uint32_t)(g.n - 1) / w.n_tiles + kWgradStep) / kWgradStep * kWgradStep;
   w.tiles = (int64_t)g.n_experts * w.m_tiles * w.n_tiles;
   return w;
 }

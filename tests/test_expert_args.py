@@ -41,7 +41,8 @@ SG = dict(d=0x10000, ldd=8, g=0x20000, ldg=8, u=0x30000, ldu=8, p=None, dg=0x400
         (dict(off=None), INV), (dict(lda=63), INV), (dict(ldb=31), INV), (dict(lddw=31), INV),
         (dict(stride=31), INV), (dict(rows=-1), INV), (dict(experts=0), INV), (dict(m=0), INV),
         (dict(n=0), INV), (dict(dtype=F32), INV), (dict(ldb=33), INV),
-        (dict(m=1 << 30, lda=1 << 30, n=1 << 30, ldb=1 << 30, lddw=1 << 30, stride=1 << 31), capi.MUON_ERR_UNSUPPORTED),
+        (dict(m=1 << 30, lda=1 << 30, n=1 << 30, ldb=1 << 30, lddw=1 << 30, stride=1 << 31),
+         capi.MUON_ERR_UNSUPPORTED),
     ]] + [
     (SW, "muon_swiglu", bad, status) for bad, status in [
         (dict(g=None), INV), (dict(u=0x20001), ALIGN), (dict(o=None), INV), (dict(ldg=7), INV),
