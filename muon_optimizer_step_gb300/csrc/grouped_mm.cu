@@ -788,9 +788,20 @@ __device__ __forceinline__ void zero_rows(uint8_t* stage, int left, int boxes, i
   __syncwarp();
 }
 
-// The 32 values from dst on that lane's row of a block holds (n of them inside the matrix).
+// The 32 values from dst on that lane's row of a block holds (n of them inside the matrix).  A
+// lane's loads cover whole 32-byte sectors where they can: beside the operand stages L1 has no
+// room to keep the rest of one for the next load.
 __device__ __forceinline__ void wgrad_load(const float* dst, int n, float (&v)[32]) {
-  if (n >= 32 && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(dst);
+  if (n >= 32 && at % 32 == 0) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 8)
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(v[k]), "=f"(v[k + 1]), "=f"(v[k + 2]), "=f"(v[k + 3]), "=f"(v[k + 4]),
+                     "=f"(v[k + 5]), "=f"(v[k + 6]), "=f"(v[k + 7])
+                   : "l"(dst + k)
+                   : "memory");
+  } else if (n >= 32 && at % 16 == 0) {
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       const float4 q = *reinterpret_cast<const float4*>(dst + k);
@@ -1076,6 +1087,15 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
       float* dw = g.dw + x.expert * g.dw_stride + (int64_t)row * g.lddw + x.j0;
       // The sums start from the old values, which arrive while the MMAs run.
       const bool old = g.accumulate && !V::kSplit;
+      if (old && p.bulk && t + units < tiles && lane < S::kBlocks) {
+        // The next tile's come to L2, a block per lane.
+        const WgradTile y = wgrad_tile<V>(g, w, t + units, bad, split);
+        const int r = y.i0 + kBM * (int)rank + 32 * q, col = (2 * lane + half) * 32;
+        if (r < g.m && col < y.cols)
+          asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(&p.dw),
+                       "r"(y.j0 + col), "r"(r), "r"(y.expert)
+                       : "memory");
+      }
       float sum[S::kBlocks][32];
       if (old || x.rows == 0)
 #pragma unroll
@@ -1358,13 +1378,20 @@ cudaError_t launch_grouped_mm(const GroupedMm& g, void* workspace, int sms, cuda
   p.g = g;
   Operand x = x_of(g), w = w_of(g);
   cudaError_t e = align_operands(&x, &w, g.offsets, workspace, sms, st);
-  // A k-split where every cluster gets an SM for each of its CTAs, and one tile.
+  // Which tiles (us, by rows of the whole product):
+  //  - A k-split where every cluster gets an SM for each of its CTAs, and one tile (6 rows,
+  //    2048 -> 1408: 13.8 without, 9.2 with; 1 row: 13.5 and 5.9).
+  //  - Few rows per expert, up to a narrow tile's: streaming the weights is the whole cost
+  //    (64 experts, 2048 -> 1408, average rows 32: narrow 58.7, pairs 66.5; 64: 65.0 and 69.1;
+  //    80: 72.5 and 70.1).  Few tiles: the more SMs work (1 expert, 512 rows, 2048 -> 2048:
+  //    narrow 11.0, wide 14.5).
+  //  - Pairs from two tiles for each pair of SMs on (8 experts, 2048 rows: 96 tiles, pairs
+  //    16.8, wide 15.0; 64 experts, 24570 rows: pairs 109, wide 125).
   int parts = 1;
   while (parts < kMostParts && mm_tiles<Split>(g) * parts * 2 <= sms && g.k >= 4 * kBK * parts * 2)
     parts *= 2;
-  // Few rows per expert: streaming the weights is the whole cost.  Few tiles: the more SMs work.
-  const bool narrow = g.rows <= 64 || g.rows <= 32 * (int64_t)g.n_experts || mm_tiles<Narrow>(g) <= sms;
-  const bool pair = !narrow && g.n > kBM && mm_tiles<Pair>(g) >= sms / 2;
+  const bool narrow = g.rows <= Narrow::kMaxN * (int64_t)g.n_experts || mm_tiles<Narrow>(g) <= sms;
+  const bool pair = !narrow && g.n > kBM && mm_tiles<Pair>(g) >= sms;
   if (e == cudaSuccess)
     e = encode(&p.x, x, g.dtype, false, parts > 1 || narrow ? Narrow::kBoxRows : Wide::kBoxRows);
   if (e == cudaSuccess) e = encode(&p.w, w, g.dtype, true, g.trans ? kBM : 64);
@@ -1391,7 +1418,9 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
     e = encode(&p.dw, {g.dw, g.m, g.n, g.lddw, g.n_experts, g.dw_stride}, kF32, true, 32);
   if (e != cudaSuccess) return e;
   p.max_n = 256;
-  if (g.m > kBM && wgrad_grid<Pair>(g, 256).tiles >= sms / 2)
+  // Pairs for many rows (64 experts of 2048 x 1408, average rows 768: pairs 252, wide 277 us;
+  // 384: 192 and 187).
+  if (g.m > kBM && wgrad_grid<Pair>(g, 256).tiles >= sms / 2 && g.rows >= 512 * (int64_t)g.n_experts)
     return launch_wgrad<Pair>(p, 1, sms, st);
   // Few tiles: with many rows several CTAs for each (32 x 216 from 7855 rows 33.6 -> 12.6 us),
   // then narrower ones, while every SM gets at most one (13 experts of 130 x 520 from 154 rows
