@@ -9,6 +9,10 @@
 // from L2), so no block waits on another, no atomic decides an order, and the result does
 // not depend on timing.  Both are bound by HBM: the gradients are read twice unless L2
 // still holds them, which is why the second launch walks each block's chunks backwards.
+// 574 M fp32 elements in 196 tensors: 332 us (6.9 TB/s) and 713 us (6.3 TB/s) alone, 1036 us
+// together; 8.8 us for ten tensors of 0.36 M.  (Where a Muon step follows, muon_step_scaled
+// takes the coefficient, and the second launch is not needed: on the 85 M gradients of 12
+// GPT-2-small layers clipping then costs 67 us instead of 175.)
 //
 // Sums: a thread adds at most 32 squares in fp32 (in four sums), then goes on in double.
 // A thread whose fp32 sum overflowed, or is so small that squares may have been flushed,
@@ -22,8 +26,10 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
+// Four resident blocks per SM, 64 bytes in flight per thread, and chunks fine enough for equal
+// shares (27 M elements: 58 us; with chunks of 32 KB and 8 blocks, three of them resident, 72).
 constexpr int kBlocksPerSm = 4;
-constexpr int kChunkBytes = 16384;  // 64 per thread, every load of which is in flight at once
+constexpr int kChunkBytes = 16384;
 constexpr int kIter = kChunkBytes / 16 / kThreads;
 
 // One tensor of a launch.  Chunk j of the tensor covers bytes j * kChunkBytes to

@@ -22,20 +22,35 @@
 // not issued, and before the one that sees both kinds the issuing warp zeroes them in shared
 // memory, in both operands (0 * NaN is NaN).
 //
-// Tiles run on CTA pairs (a 2-CTA cluster, cta_group::2): each CTA holds 128 of the MMA's 256
-// rows and half of its N columns of operand B, so a k-step brings 32 KB instead of 48 KB into
-// each SM for the same work; on single CTAs the operand traffic from L2 was the bound (53 %
-// tensor pipe on 98304 x 1408 -> 2048, 64 experts).  Single CTAs run where pairs would leave
-// SMs without tiles.
+// Large products run on CTA pairs (a 2-CTA cluster, cta_group::2): each CTA holds 128 of the
+// MMA's 256 rows and half of its N columns of operand B, so a k-block brings 32 KB instead of
+// 48 KB into each SM for the same work (98304 rows, 1408 -> 2048, 64 experts: pairs 332 us,
+// single CTAs 383).  The other tiles, and when they run, stand at the variants and launches below.
 //
 // The tensor core truncates when it adds to its accumulator, always towards zero, so the error
 // of a sum grows with its number of steps (1.8e-6 of the result after 1536 rows).  Results
-// kept in fp32 are therefore summed in segments of kSegment k-blocks, which the epilogue adds
-// up in registers with rounding to nearest.
+// kept in fp32 are therefore summed in segments of up to kSegment k-blocks, which the epilogue
+// adds up in registers with rounding to nearest (6e-7, as a plain fp32 product has).  16-bit
+// results keep the whole sum in the accumulator: their store rounds by 2^-9 or 2^-12 anyway.
 //
 // CTA roles (384 threads): warp 0 issues the TMA loads, warp 1 the MMAs (on the first CTA of a
 // pair), warp 2 owns TMEM, warps 4-11 drain the accumulators (two, in TMEM's 512 columns, so a
 // tile's stores overlap the next one's MMAs).  Every wait is bounded.
+//
+// The issuing warps walk their loops whole and elect a lane for each k-block: with one lane in
+// a divergent loop, descriptors and barrier addresses went through vector registers and issue
+// was the bound (a k-block took 750 cycles to load and 560 + 50 per MMA to multiply; the same
+// product 489 us instead of 322).
+//
+// Measured, per pass (the loads fill the 64 bytes a cycle that an SM takes from L2 to about
+// 90 %; in runs of more than a few ms the 1.4 kW limit lowers the clock to 1.35-1.5 GHz):
+//   98304 rows, 1408 -> 2048, 64 experts  332 us  1.71 PFLOP/s, tensor pipe 82 % busy
+//   4096 rows, 4096 -> 14336, 8 experts   296 us  1.62 PFLOP/s, 85 %
+//   24570 rows, 2048 -> 1408, 64 experts  108 us  1.31 PFLOP/s and 5.0 TB/s
+//   192 rows, 1408 -> 2048, 64 experts     53 us  6.6 TB/s (HBM)
+//   6 rows, 2048 -> 1408, 64 experts      9.2 us  (4.5 us are launch, offsets and first load)
+//   weight gradient of the first          405 us  1.40 PFLOP/s and 3.5 TB/s, 62 %: loads alone
+//                                                 take 343, stores alone 288, MMAs alone 279
 #include <atomic>
 
 #include <cudaTypedefs.h>
@@ -77,10 +92,10 @@ struct Narrow {
   static constexpr bool kPair = false, kSplit = false;
   static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2;
 };
-// Split: a cluster of CTAs shares one tile, each taking a part of k; the first one adds the
-// parts up, in order, out of the others' shared memory.  For products of so few tiles that most
-// SMs would have none: a k-block costs a CTA about 0.27 us whatever the tile's width (the MMA
-// reads 128 rows of the weight), so 6 tokens through 2048 -> 1408 took 13.8 us on 66 CTAs.
+// Split: a cluster of CTAs shares one tile, each taking a part of k; then all of them add up
+// shares of the tile, the parts in order, out of each other's shared memory.  For products of so
+// few tiles that most SMs would have none: a k-block costs a CTA 0.2 us whatever the tile's
+// width (the MMA reads 128 rows of the weight).
 struct Split {
   static constexpr bool kPair = false, kSplit = true;
   static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2;
@@ -91,7 +106,8 @@ struct SplitWide {
   static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
 };
 constexpr int kMostParts = 8;  // portable cluster size
-// What follows from a variant (wgrad uses Pair and Wide).
+
+// What follows from a variant (wgrad uses Pair, Wide and SplitWide).
 template <typename V>
 struct Shape {
   static constexpr int kCtas = V::kPair ? 2 : 1;
@@ -1088,7 +1104,8 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
       // The sums start from the old values, which arrive while the MMAs run.
       const bool old = g.accumulate && !V::kSplit;
       if (old && p.bulk && t + units < tiles && lane < S::kBlocks) {
-        // The next tile's come to L2, a block per lane.
+        // The next tile's come to L2, a block per lane (64 x 2048 x 1408 from 24570 rows: 354
+        // without, 317 us with).
         const WgradTile y = wgrad_tile<V>(g, w, t + units, bad, split);
         const int r = y.i0 + kBM * (int)rank + 32 * q, col = (2 * lane + half) * 32;
         if (r < g.m && col < y.cols)

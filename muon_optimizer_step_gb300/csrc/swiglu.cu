@@ -8,10 +8,13 @@
 // p_r is the router's weight of row r (1 where there is none).  Elementwise work in fp32,
 // one rounding at each store, bound by HBM: 3 (5) values move per element.  For 16-bit tensors
 // s takes the fast exponential and reciprocal, whose few 2^-22 are far below the store's
-// rounding: with expf and an IEEE division the gradient was bound by instructions (264 us for
-// 98304 x 1408, 207 us at the measured copy rate).  kTpr threads
-// share a row: a warp where there are many rows (dp then needs shuffles only), a block
-// where there are few, so that a small batch still fills the machine with loads.
+// rounding: with expf and an IEEE division the gradient was bound by instructions.
+// 98304 x 1408 in bf16, gradient: 231 us (6.0 TB/s; 264 us with expf and the division; other
+// grids, unrolling and streaming stores made no difference).
+//
+// kTpr threads share a row: a warp where there are many rows (dp then needs shuffles only), a
+// block where there are few, so that a small batch still fills the machine with loads
+// (192 x 1408: 1.9 us).
 #include "element.cuh"
 #include "kernels.h"
 
@@ -162,8 +165,10 @@ template <typename T>
 cudaError_t launch_type(const SwigluArgs& s, const float* p, float* dp, int64_t rows, int32_t cols,
                         int sms, cudaStream_t st) {
   constexpr int v = 16 / sizeof(T);
-  // A warp per row once that alone gives every SM its 64 warps.
-  const bool many = rows >= (int64_t)sms * 64;
+  // A warp per row where that gives every SM 32 warps, unless a row is long enough to give each
+  // thread of a block four accesses (gradient in bf16, us by warps and by blocks: 2048 x 1408 7.6
+  // and 6.6, 4864 x 1408 11.5 and 15.3, 19456 x 64 7.0 and 24.8, 9728 x 14336 226 and 213).
+  const bool many = rows >= (int64_t)sms * 32 && cols < 4 * kThreads * (vectors<T>(s, cols) ? v : 1);
   if (vectors<T>(s, cols))
     return many ? launch_as<T, v, 32>(s, p, dp, rows, cols, sms, st)
                 : launch_as<T, v, kThreads>(s, p, dp, rows, cols, sms, st);
