@@ -397,10 +397,13 @@ def muon_export_update(layout, workspace, ns_steps, full_out, stream=None):
 # These calls are short, so their checks are: one look at each tensor's attributes, and torch's
 # stream handle instead of a stream object.
 _KINDS = {}   # torch dtype -> muon_dtype
+_torch = None  # the module, once a tensor has come
 
 
 def _kinds():
+    global _torch
     import torch
+    _torch = torch
     _KINDS.update({torch.float32: MUON_DTYPE_F32, torch.bfloat16: MUON_DTYPE_BF16,
                    torch.float16: MUON_DTYPE_F16})
     return _KINDS
@@ -454,8 +457,7 @@ def _row_floats(t, rows, name):
 
 
 def _offsets(t, n_experts):
-    import torch
-    if not t.is_cuda or t.dtype != torch.int64 or t.shape != (n_experts + 1,) \
+    if not t.is_cuda or t.dtype != _torch.int64 or t.shape != (n_experts + 1,) \
             or not t.is_contiguous():
         raise ValueError(f"offsets: must be {n_experts + 1} contiguous int64 values on the GPU")
     return t.data_ptr()
@@ -464,8 +466,7 @@ def _offsets(t, n_experts):
 def _stream_of(stream, like):
     """The handle of `stream`, or of the current stream of like's device."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(like.get_device())
+        return _torch._C._cuda_getCurrentRawStream(like.get_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -476,11 +477,10 @@ def _workspace(workspace, nbytes, align, like, stream):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if nbytes == 0:
         return None, 0, None
-    import torch
-    raw = torch.empty(nbytes + align, dtype=torch.uint8, device=like.device)
+    raw = _torch.empty(nbytes + align, dtype=_torch.uint8, device=like.device)
     if stream is not None:
         raw.record_stream(stream if not isinstance(stream, int)
-                          else torch.cuda.ExternalStream(stream, device=like.device))
+                          else _torch.cuda.ExternalStream(stream, device=like.device))
     at = raw.data_ptr()
     return at + (-at) % align, nbytes, raw
 

@@ -1170,6 +1170,7 @@ struct AlignCopy {
   uint4* dst;
   const int64_t* offsets;  // batches are experts: those without rows are left out (null: none is)
   int64_t ld, stride, rows, cols, chunks, total;  // 16-byte chunks per row; all rows (0: no copy)
+  int64_t pitch;                                  // of the copy, in chunks
   int32_t lanes;           // threads that share a row
 };
 
@@ -1208,7 +1209,7 @@ __device__ __forceinline__ void align_rows(const AlignCopy& c) {
         for (int k = 0; k < 8; ++k) e[k] = c0 + k < c.cols ? s[c0 + k] : 0;
         v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
       }
-      c.dst[row * c.chunks + q] = v;
+      c.dst[row * c.pitch + q] = v;
     }
   }
 }
@@ -1229,9 +1230,16 @@ bool aligned(const Operand& o) {
          (o.batch == 1 || o.stride % 8 == 0);
 }
 
+// Row pitch of a copy: whole 128-byte lines where a row fills one, so that no 128-byte box row
+// straddles two.
+int64_t copy_pitch(const Operand& o) {
+  const int64_t unit = o.cols >= 64 ? 64 : 8;
+  return (o.cols + unit - 1) / unit * unit;
+}
+
 size_t copy_bytes(const Operand& o) {
   if (aligned(o)) return 0;
-  return (size_t)split_part_bytes(o.batch * o.rows * ((o.cols + 7) / 8) * 16);
+  return (size_t)split_part_bytes(o.batch * o.rows * copy_pitch(o) * 2);
 }
 
 // Replaces an operand by its aligned copy at *at in the workspace, if it needs one; returns the
@@ -1250,9 +1258,10 @@ AlignCopy align_operand(Operand* o, uint8_t** at, const int64_t* offsets) {
   c.cols = o->cols;
   c.chunks = (o->cols + 7) / 8;
   c.total = o->batch * o->rows;
+  c.pitch = copy_pitch(*o) / 8;
   while (c.lanes < 32 && c.lanes < c.chunks) c.lanes *= 2;
   o->ptr = *at;
-  o->ld = c.chunks * 8;
+  o->ld = c.pitch * 8;
   o->stride = o->rows * o->ld;
   *at += bytes;
   return c;
@@ -1364,12 +1373,17 @@ cudaError_t launch_wgrad(const WgradParams& p, int parts, int sms, cudaStream_t 
                 V::kStages * Shape<V>::kStage + kEpiWarps * kWgradStaging + 1024, &ready, st);
 }
 
-Operand x_of(const GroupedMm& g) { return {g.x, g.rows, g.k, g.ldx, 1, 0}; }
-Operand w_of(const GroupedMm& g) {
-  return {g.w, g.trans ? g.n : g.k, g.trans ? g.k : g.n, g.ldw, g.n_experts, g.w_stride};
+// The pitch of a single row means nothing: one that TMA takes.
+Operand operand(const void* ptr, int64_t rows, int64_t cols, int64_t ld, int64_t batch,
+                int64_t stride) {
+  return {ptr, rows, cols, rows == 1 ? (cols + 7) / 8 * 8 : ld, batch, stride};
 }
-Operand a_of(const GroupedWgrad& g) { return {g.a, g.rows, g.m, g.lda, 1, 0}; }
-Operand b_of(const GroupedWgrad& g) { return {g.b, g.rows, g.n, g.ldb, 1, 0}; }
+Operand x_of(const GroupedMm& g) { return operand(g.x, g.rows, g.k, g.ldx, 1, 0); }
+Operand w_of(const GroupedMm& g) {
+  return operand(g.w, g.trans ? g.n : g.k, g.trans ? g.k : g.n, g.ldw, g.n_experts, g.w_stride);
+}
+Operand a_of(const GroupedWgrad& g) { return operand(g.a, g.rows, g.m, g.lda, 1, 0); }
+Operand b_of(const GroupedWgrad& g) { return operand(g.b, g.rows, g.n, g.ldb, 1, 0); }
 
 }  // namespace
 

@@ -102,7 +102,7 @@ def test_scaled_step_refusals():
 
 
 def test_workspace_sizes():
-    """Nothing for operands whose rows start on 16 bytes; else whole copies at rows of 16 bytes."""
+    """Nothing for operands whose rows start on 16 bytes; else whole copies, rows on 16 or 128 bytes."""
     def mm(x=0x1000, ldx=64, w=0x2000, ldw=32, stride=2048, rows=10, e=4, k=64, n=32, trans=0):
         v = ctypes.c_size_t()
         assert capi.lib.muon_grouped_mm_workspace_bytes(x, ldx, w, ldw, stride, rows, e, k, n, trans,
@@ -113,11 +113,13 @@ def test_workspace_sizes():
     assert mm(rows=0, x=None, w=None, ldx=65) == 0
     assert mm(ldx=72, ldw=40, stride=4096) == 0
     assert 10 * 64 * 2 <= mm(ldx=65) <= 10 * 64 * 2 + 1024
+    assert mm(rows=1, ldx=65) == 0 and mm(rows=1, x=0x1002) > 0
+    assert 10 * 128 * 2 <= mm(k=65, ldx=65) <= 10 * 128 * 2 + 1024      # whole 128-byte lines
     assert 10 * 64 * 2 <= mm(x=0x1002) <= 10 * 64 * 2 + 1024
     assert 4 * 64 * 32 * 2 <= mm(ldw=33) <= 4 * 64 * 32 * 2 + 1024
     assert 4 * 64 * 32 * 2 <= mm(stride=2049) <= 4 * 64 * 32 * 2 + 1024
     assert mm(stride=2049, e=1) == 0
-    assert 4 * 5 * 72 * 2 <= mm(trans=1, n=5, k=65, ldw=65, ldx=72, stride=512) <= 4 * 5 * 72 * 2 + 1024
+    assert 4 * 5 * 128 * 2 <= mm(trans=1, n=5, k=65, ldw=65, ldx=72, stride=512) <= 4 * 5 * 128 * 2 + 1024
     v = ctypes.c_size_t()
     assert capi.lib.muon_grouped_wgrad_workspace_bytes(0x1000, 65, 0x2002, 32, 10, 64, 32,
                                                        ctypes.byref(v)) == capi.MUON_OK

@@ -138,6 +138,14 @@ def test_mm_enough_tiles_for_pairs(capi, sizes, k, n, trans, dtype, out):
     _check_mm(capi, sizes, k, n, trans, dtype, out, first=2, tail=5)
 
 
+@pytest.mark.parametrize("k", [1, 7, 65, 771])
+def test_mm_single_row_of_any_length(capi, k):
+    """The pitch of one row means nothing: no copy, and nothing read behind the row."""
+    for n in (1, 24):
+        _check_mm(capi, [0, 1], k, n, True, "bf16", "fp32")
+        _check_mm(capi, [1], k, n, False, "fp16", "fp16")
+
+
 def test_mm_many_experts(capi):
     sizes = [(i * 7) % 5 for i in range(1024)]
     _check_mm(capi, sizes, 64, 64, False, "bf16", "bf16")
@@ -346,16 +354,17 @@ def test_layer_gradients_against_differences(capi):
     assert abs(got - want) <= 1e-5 * mag
 
 
-def test_bad_offsets_are_reported_and_move_nothing(capi):
-    x = torch.randn(10, 16, device="cuda").bfloat16()
-    w = torch.randn(3, 16, 24, device="cuda").bfloat16()
+@pytest.mark.parametrize("k", [16, 1024])   # 1024: split over a cluster
+def test_bad_offsets_are_reported_and_move_nothing(capi, k):
+    x = torch.randn(10, k, device="cuda").bfloat16()
+    w = torch.randn(3, k, 24, device="cuda").bfloat16()
     for bad in ([0, 4, 3, 10], [0, 4, 8, 11], [-1, 4, 8, 10], [0, 2 ** 40, 8, 10]):
         off = torch.tensor(bad, dtype=torch.int64, device="cuda")
         y = torch.full((10, 24), 3.0, device="cuda").bfloat16()
         capi.muon_grouped_mm(x, w, off, y)
         assert capi.muon_check_status() == capi.MUON_ERR_ROW_OFFSETS
         assert (y == 0).all()
-        dw = torch.ones(3, 16, 24, device="cuda")
+        dw = torch.ones(3, k, 24, device="cuda")
         capi.muon_grouped_wgrad(x, y, off, dw)
         assert capi.muon_check_status() == capi.MUON_ERR_ROW_OFFSETS
         assert (dw == 0).all()
@@ -390,6 +399,30 @@ def test_products_on_another_stream_and_in_a_graph(capi):
     capi.muon_grouped_mm(x, w, off, want)
     capi.muon_check()
     assert torch.equal(y, want)
+
+
+def test_products_on_several_streams_at_once(capi):
+    """Launches that share the GPU's SMs: pairs, narrow tiles, clusters and weight gradients."""
+    gen = _gen(31)
+    jobs = []
+    for sizes, k, n in (([700, 300, 0, 900], 512, 2312), ([3, 0, 9, 1], 1024, 264),
+                        ([40, 64, 1, 200], 200, 136), ([2000, 3, 700, 90], 264, 776)):
+        x = _randn(gen, sum(sizes), k, dtype=torch.bfloat16)
+        w = _randn(gen, 4, k, n, dtype=torch.bfloat16)
+        off = _offsets(sizes)
+        y, d = torch.empty(sum(sizes), n, device="cuda").bfloat16(), torch.empty(4, k, n, device="cuda")
+        capi.muon_grouped_mm(x, w, off, y)
+        capi.muon_grouped_wgrad(x, y, off, d)
+        jobs.append((x, w, off, y, d, torch.empty_like(y), torch.empty_like(d), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, w, off, y, d, y2, d2, side in jobs:
+            capi.muon_grouped_mm(x, w, off, y2, stream=side)
+            capi.muon_grouped_wgrad(x, y2, off, d2, stream=side)
+    torch.cuda.synchronize()
+    capi.muon_check()
+    for x, w, off, y, d, y2, d2, side in jobs:
+        assert torch.equal(y, y2) and torch.equal(d, d2)
 
 
 def test_products_past_2_to_the_31_elements(capi):
