@@ -103,7 +103,7 @@ struct Split {
 // The same for weight gradients of few tiles and many rows: the CTAs share the rows.
 struct SplitWide {
   static constexpr bool kPair = false, kSplit = true;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
+  static constexpr int kMaxN = 256, kStages = 4, kSub = 1;
 };
 constexpr int kMostParts = 8;  // portable cluster size
 
@@ -112,7 +112,7 @@ template <typename V>
 struct Shape {
   static constexpr int kCtas = V::kPair ? 2 : 1;
   static constexpr int kM = kBM * kCtas;                   // M of the MMA
-  static constexpr int kStepN = 16 * kCtas;                // N goes in steps of this
+  [[maybe_unused]] static constexpr int kStepN = 16 * kCtas;  // N goes in steps of this (mm)
   static constexpr int kBlock = kABytes + V::kMaxN / kCtas * 128;  // bytes of a k-block
   static constexpr int kStage = kBlock * V::kSub;
   static constexpr int kBlocks = (V::kMaxN + 63) / 64;     // 32-column blocks per epilogue warp
