@@ -28,10 +28,12 @@
 // single CTAs 383).  The other tiles, and when they run, stand at the variants and launches below.
 //
 // The tensor core truncates when it adds to its accumulator, always towards zero, so the error
-// of a sum grows with its number of steps (1.8e-6 of the result after 1536 rows).  Results
-// kept in fp32 are therefore summed in segments of up to kSegment k-blocks, which the epilogue
-// adds up in registers with rounding to nearest (6e-7, as a plain fp32 product has).  16-bit
-// results keep the whole sum in the accumulator: their store rounds by 2^-9 or 2^-12 anyway.
+// of a sum grows with its number of steps (1.8e-6 of the result after 1536 rows).  Results are
+// therefore summed in segments of up to kSegment k-blocks, which the epilogue adds up in
+// registers with rounding to nearest (6e-7).  16-bit results too, in segments of kSegment16: of
+// whole sums of 4096 terms one in 430 is stored in bf16 other than the exact sum would be, of 16384
+// terms one in 110; in segments one in 2000 whatever the length (98304 rows, 1408 -> 2048: 336
+// us in segments, 333 whole; 24570 rows, 2048 -> 1408: 111 and 109).
 //
 // CTA roles (384 threads): warp 0 issues the TMA loads, warp 1 the MMAs (on the first CTA of a
 // pair), warp 2 owns TMEM, warps 4-11 drain the accumulators (two, in TMEM's 512 columns, so a
@@ -80,17 +82,19 @@ constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 // barriers: a wait, an elected lane and a commit cost the issuing warps 250-400 cycles, more than
 // the loads or MMAs of one narrow k-block (one token 12.5 -> 9.2 us).  Where the MMAs take 500
 // cycles a k-block, the finer stages are ahead (Pair: 328 against 335 us on 98304 x 1408 -> 2048).
+// kSegment16: most k-blocks per segment of a sum that is stored in 16 bits.  Pairs pay for shorter
+// ones (24570 rows, 2048 -> 1408: 111 us, 118 with 8), the others do not.
 struct Pair {
   static constexpr bool kPair = true, kSplit = false;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1, kSegment16 = 11;
 };
 struct Wide {
   static constexpr bool kPair = false, kSplit = false;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1, kSegment16 = 8;
 };
 struct Narrow {
   static constexpr bool kPair = false, kSplit = false;
-  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2;
+  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2, kSegment16 = 8;
 };
 // Split: a cluster of CTAs shares one tile, each taking a part of k; then all of them add up
 // shares of the tile, the parts in order, out of each other's shared memory.  For products of so
@@ -98,7 +102,7 @@ struct Narrow {
 // width (the MMA reads 128 rows of the weight).
 struct Split {
   static constexpr bool kPair = false, kSplit = true;
-  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2;
+  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2, kSegment16 = 8;
 };
 // The same for weight gradients of few tiles and many rows: the CTAs share the rows.
 struct SplitWide {
@@ -283,9 +287,9 @@ __device__ __forceinline__ void drain_ring(Control& c, int64_t fills, uint32_t r
 }
 
 // k-blocks of each of a sum's segments, whole stages of equal number up to the last segment.
-template <typename V>
+template <typename V, int kMost>
 __device__ __forceinline__ int segment(int k_blocks) {
-  const uint32_t n = (uint32_t)(k_blocks + kSegment - 1) / kSegment;
+  const uint32_t n = (uint32_t)(k_blocks + kMost - 1) / kMost;
   const int len = n > 1 ? (int)((uint32_t)(k_blocks + n - 1) / n) : k_blocks;
   return (len + V::kSub - 1) / V::kSub * V::kSub;
 }
@@ -519,8 +523,6 @@ template <typename V, typename O>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_mm_kernel(const __grid_constant__ MmParams p) {
   using S = Shape<V>;
-  // Summed in segments, in registers.
-  constexpr bool kSums = sizeof(O) == 4 || V::kSplit;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
   __shared__ int32_t off[kMaxExperts + 1], first[kMaxExperts + 1];
@@ -550,7 +552,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
     unit >>= shift;
     units >>= shift;
   }
-  const int seg = segment<V>(kb1 - kb0);
+  const int seg = segment<V, sizeof(O) == 4 ? kSegment : V::kSegment16>(kb1 - kb0);
 
   if (warp == 0) {
     Ring<V::kStages> ring;
@@ -610,8 +612,8 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
       const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, m.n, a_mn, 0);
       for (int kb = kb0; kb < kb1;) {
-        // One accumulator: all k-blocks, or a segment of them.
-        const int end = kSums ? min(kb1, kb + seg) : kb1;
+        // One accumulator: a segment of the k-blocks.
+        const int end = min(kb1, kb + seg);
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
@@ -658,39 +660,27 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V>(t, f_tiles, g.n_experts, off, first);
       const int f = m.f0 + kBM * (int)rank + 32 * q;
-      if constexpr (kSums) {
-        float sum[S::kBlocks][32];
-        for (int kb = kb0; kb < kb1; kb += seg, ++use) {
-          ok = wait_acc(c, use, g.err);
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < S::kBlocks; ++i)
-            if ((2 * i + half) * 32 < m.n)
-              add_acc(tmem, use & 1, q, (2 * i + half) * 32, kb == kb0, sum[i]);
-          release_acc<V::kPair>(c, use & 1, rank, lane);
-        }
-        if (!ok) break;
-        if constexpr (V::kSplit) {
-          // The operand stages are free: this tile's MMAs were the last.
-          if (half * 32 < m.n)
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              reinterpret_cast<float*>(smem)[(q * V::kMaxN + half * 32 + k) * 32 + lane] = sum[0][k];
-        } else {
-#pragma unroll
-          for (int i = 0; i < S::kBlocks; ++i)
-            if ((2 * i + half) * 32 < m.n) mm_store<O>(g, m, 2 * i + half, f, lane, sum[i]);
-        }
-      } else {
+      float sum[S::kBlocks][32];
+      for (int kb = kb0; kb < kb1; kb += seg, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
-        for (int b = half; b * 32 < m.n; b += 2) {
-          float v[32];
-          add_acc(tmem, use & 1, q, 32 * b, true, v);
-          mm_store<O>(g, m, b, f, lane, v);
-        }
+#pragma unroll
+        for (int i = 0; i < S::kBlocks; ++i)
+          if ((2 * i + half) * 32 < m.n)
+            add_acc(tmem, use & 1, q, (2 * i + half) * 32, kb == kb0, sum[i]);
         release_acc<V::kPair>(c, use & 1, rank, lane);
-        ++use;
+      }
+      if (!ok) break;
+      if constexpr (V::kSplit) {
+        // The operand stages are free: this tile's MMAs were the last.
+        if (half * 32 < m.n)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            reinterpret_cast<float*>(smem)[(q * V::kMaxN + half * 32 + k) * 32 + lane] = sum[0][k];
+      } else {
+#pragma unroll
+        for (int i = 0; i < S::kBlocks; ++i)
+          if ((2 * i + half) * 32 < m.n) mm_store<O>(g, m, 2 * i + half, f, lane, sum[i]);
       }
     }
     // Rows of no expert.
@@ -1022,7 +1012,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, x.n, 1, 1);
-      const int seg = segment<V>((x.rows + kBK - 1) / kBK);
+      const int seg = segment<V, kSegment>((x.rows + kBK - 1) / kBK);
       for (int left = x.rows; left > 0;) {
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
@@ -1119,7 +1109,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
         for (int i = 0; i < S::kBlocks; ++i)
           wgrad_load(dw + lane * g.lddw + (2 * i + half) * 32,
                      old && row + lane < g.m ? x.cols - (2 * i + half) * 32 : 0, sum[i]);
-      const int seg = segment<V>((x.rows + kBK - 1) / kBK);
+      const int seg = segment<V, kSegment>((x.rows + kBK - 1) / kBK);
       for (int r = 0; r < x.rows; r += seg * kBK, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
