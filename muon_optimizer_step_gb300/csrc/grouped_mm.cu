@@ -29,9 +29,9 @@
 //
 // The tensor core truncates when it adds to its accumulator, always towards zero, so the error
 // of a sum grows with its number of steps (1.8e-6 of the result after 1536 rows).  Results are
-// therefore summed in segments of up to kSegment k-blocks, which the epilogue adds up in
-// registers with rounding to nearest (6e-7).  16-bit results too, in segments of kSegment16: of
-// whole sums of 4096 terms one in 430 is stored in bf16 other than the exact sum would be, of 16384
+// therefore summed in short segments, which the epilogue adds up in registers with rounding to
+// nearest: 3.3e-7 whatever the length (3.6e-7 for a plain fp32 product of 1536 rows).  16-bit
+// results in longer ones: of whole sums of 4096 terms one in 430 is stored in bf16 other than the exact sum would be, of 16384
 // terms one in 110; in segments one in 2000 whatever the length (98304 rows, 1408 -> 2048: 336
 // us in segments, 333 whole; 24570 rows, 2048 -> 1408: 111 and 109).
 //
@@ -72,7 +72,6 @@ constexpr int kBK = 64;             // k-block: 128 bytes of a 16-bit row
 constexpr int kABytes = kBM * 128;  // 16 KB
 constexpr int kBox = 64 * 128;      // an MN-major box: 64 k-rows of 128 bytes
 constexpr int kAccCols = 256;       // TMEM columns of one accumulator
-constexpr int kSegment = 12;        // most k-blocks per segment of an fp32 result
 constexpr int kMaxStages = 6;
 constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 
@@ -82,19 +81,25 @@ constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 // barriers: a wait, an elected lane and a commit cost the issuing warps 250-400 cycles, more than
 // the loads or MMAs of one narrow k-block (one token 12.5 -> 9.2 us).  Where the MMAs take 500
 // cycles a k-block, the finer stages are ahead (Pair: 328 against 335 us on 98304 x 1408 -> 2048).
-// kSegment16: most k-blocks per segment of a sum that is stored in 16 bits.  Pairs pay for shorter
-// ones (24570 rows, 2048 -> 1408: 111 us, 118 with 8), the others do not.
+// kSegment16, kSegment32: most k-blocks per segment of a sum that is stored in 16 or 32 bits.  The
+// MMAs wait where a segment ends before the last tile's stores have left the epilogue free:
+// wide tiles pay for short segments (24570 rows, 2048 -> 1408, 16-bit: 111 us with 11, 118 with 8;
+// weight gradient of 98304 rows, 64 x 2048 x 1408: 403 us with 12, 422 with 8, 452 with 6, 523
+// with 4), the others do not.  kSegment32 is the longest whose error is a plain product's.
 struct Pair {
   static constexpr bool kPair = true, kSplit = false;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1, kSegment16 = 11;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1;
+  static constexpr int kSegment16 = 11, kSegment32 = 6;
 };
 struct Wide {
   static constexpr bool kPair = false, kSplit = false;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1, kSegment16 = 8;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
+  static constexpr int kSegment16 = 8, kSegment32 = 6;
 };
 struct Narrow {
   static constexpr bool kPair = false, kSplit = false;
-  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2, kSegment16 = 8;
+  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2;
+  static constexpr int kSegment16 = 8, kSegment32 = 4;
 };
 // Split: a cluster of CTAs shares one tile, each taking a part of k; then all of them add up
 // shares of the tile, the parts in order, out of each other's shared memory.  For products of so
@@ -102,12 +107,13 @@ struct Narrow {
 // width (the MMA reads 128 rows of the weight).
 struct Split {
   static constexpr bool kPair = false, kSplit = true;
-  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2, kSegment16 = 8;
+  static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 4, kSub = 2;
+  static constexpr int kSegment16 = 8, kSegment32 = 4;
 };
 // The same for weight gradients of few tiles and many rows: the CTAs share the rows.
 struct SplitWide {
   static constexpr bool kPair = false, kSplit = true;
-  static constexpr int kMaxN = 256, kStages = 4, kSub = 1;
+  static constexpr int kMaxN = 256, kStages = 4, kSub = 1, kSegment32 = 4;
 };
 constexpr int kMostParts = 8;  // portable cluster size
 
@@ -552,7 +558,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
     unit >>= shift;
     units >>= shift;
   }
-  const int seg = segment<V, sizeof(O) == 4 ? kSegment : V::kSegment16>(kb1 - kb0);
+  const int seg = segment<V, sizeof(O) == 4 ? V::kSegment32 : V::kSegment16>(kb1 - kb0);
 
   if (warp == 0) {
     Ring<V::kStages> ring;
@@ -1012,7 +1018,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, x.n, 1, 1);
-      const int seg = segment<V, kSegment>((x.rows + kBK - 1) / kBK);
+      const int seg = segment<V, V::kSegment32>((x.rows + kBK - 1) / kBK);
       for (int left = x.rows; left > 0;) {
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
@@ -1109,7 +1115,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
         for (int i = 0; i < S::kBlocks; ++i)
           wgrad_load(dw + lane * g.lddw + (2 * i + half) * 32,
                      old && row + lane < g.m ? x.cols - (2 * i + half) * 32 : 0, sum[i]);
-      const int seg = segment<V, kSegment>((x.rows + kBK - 1) / kBK);
+      const int seg = segment<V, V::kSegment32>((x.rows + kBK - 1) / kBK);
       for (int r = 0; r < x.rows; r += seg * kBK, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;

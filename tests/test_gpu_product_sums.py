@@ -56,3 +56,44 @@ def test_long_16_bit_results_are_rounded_right(capi, sizes, n, dtype, bits, k):
     want = torch.cat([a.double() @ b.double() for a, b in zip(x.split(sizes), w)])
     wrong = (y != want.to(DT[dtype])).double().mean().item()
     assert wrong <= 4e-6 * 2.0 ** bits + 2 / y.numel()
+
+
+def _frobenius(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+@pytest.fixture()
+def plain_products():
+    old = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = False
+    yield
+    torch.backends.cuda.matmul.allow_tf32 = old
+
+
+@pytest.mark.parametrize("experts,rows,m,n", [(1, 1536, 520, 1416), (1, 1536, 72, 136), (1, 20000, 72, 136),
+                                              (1, 20000, 776, 1416), (8, 1536, 2048, 1408)])
+def test_weight_gradients_are_as_exact_as_plain_fp32(capi, plain_products, experts, rows, m, n):
+    """At most one rounding (2^-24) more than torch's fp32 product of the same values."""
+    gen = _gen(rows + m)
+    a = torch.randn(experts * rows, m, generator=gen, device="cuda").bfloat16()
+    b = torch.randn(experts * rows, n, generator=gen, device="cuda").bfloat16()
+    dw = torch.empty(experts, m, n, device="cuda")
+    capi.muon_grouped_wgrad(a, b, _offsets([rows] * experts), dw)
+    capi.muon_check()
+    a, b = a.view(experts, rows, m).mT, b.view(experts, rows, n)
+    want = a.double() @ b.double()
+    plain = torch.stack([x @ y for x, y in zip(a.float(), b.float())])
+    assert _frobenius(dw, want) <= _frobenius(plain, want) + 2.0 ** -24
+
+
+@pytest.mark.parametrize("rows,k,n", [(3000, 2048, 1416), (600, 771, 517), (40, 2048, 2056),
+                                      (33, 4104, 264)])
+def test_fp32_products_are_as_exact_as_plain_fp32(capi, plain_products, rows, k, n):
+    gen = _gen(rows + k)
+    x = torch.randn(rows, k, generator=gen, device="cuda").half()
+    w = torch.randn(1, k, n, generator=gen, device="cuda").half()
+    y = torch.empty(rows, n, device="cuda")
+    capi.muon_grouped_mm(x, w, _offsets([rows]), y)
+    capi.muon_check()
+    want = x.double() @ w[0].double()
+    assert _frobenius(y, want) <= _frobenius(x.float() @ w[0].float(), want) + 2.0 ** -24
