@@ -470,17 +470,28 @@ def _stream_of(stream, like):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _torch_stream(stream, device):
+    """`stream` as torch's stream object (a handle of 0 or 1 is the default stream)."""
+    if isinstance(stream, _torch.cuda.Stream):
+        return stream
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    return (_torch.cuda.default_stream(device) if handle in (0, 1)
+            else _torch.cuda.ExternalStream(handle, device=device))
+
+
 def _workspace(workspace, nbytes, align, like, stream):
-    """(pointer, bytes, owner) of the caller's workspace, or of one from torch's allocator, which
-    is kept from reuse until the work enqueued on `stream` is done with it."""
+    """(pointer, bytes, owner) of the caller's workspace, or of one from torch's allocator: a block of
+    `stream` itself, so that nothing pending elsewhere still uses it and work behind this call
+    may have it next."""
     if workspace is not None:
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if nbytes == 0:
         return None, 0, None
-    raw = _torch.empty(nbytes + align, dtype=_torch.uint8, device=like.device)
-    if stream is not None:
-        raw.record_stream(stream if not isinstance(stream, int)
-                          else _torch.cuda.ExternalStream(stream, device=like.device))
+    if stream is None:
+        raw = _torch.empty(nbytes + align, dtype=_torch.uint8, device=like.device)
+    else:
+        with _torch.cuda.stream(_torch_stream(stream, like.device)):
+            raw = _torch.empty(nbytes + align, dtype=_torch.uint8, device=like.device)
     at = raw.data_ptr()
     return at + (-at) % align, nbytes, raw
 
