@@ -60,6 +60,7 @@
 #include "device_common.cuh"
 #include "element.cuh"
 #include "kernels.h"
+#include "row_blocks.h"
 
 namespace muon {
 
@@ -68,7 +69,6 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kBM = 128;            // rows of operand A: M of the MMA
-constexpr int kBK = 64;             // k-block: 128 bytes of a 16-bit row
 constexpr int kABytes = kBM * 128;  // 16 KB
 constexpr int kBox = 64 * 128;      // an MN-major box: 64 k-rows of 128 bytes
 constexpr int kAccCols = 256;       // TMEM columns of one accumulator
@@ -292,14 +292,6 @@ __device__ __forceinline__ void drain_ring(Control& c, int64_t fills, uint32_t r
   }
 }
 
-// k-blocks of each of a sum's segments, whole stages of equal number up to the last segment.
-template <typename V, int kMost>
-__device__ __forceinline__ int segment(int k_blocks) {
-  const uint32_t n = (uint32_t)(k_blocks + kMost - 1) / kMost;
-  const int len = n > 1 ? (int)((uint32_t)(k_blocks + n - 1) / n) : k_blocks;
-  return (len + V::kSub - 1) / V::kSub * V::kSub;
-}
-
 // Position in the ring of operand stages.
 template <int kStages>
 struct Ring {
@@ -480,7 +472,7 @@ __device__ __forceinline__ MmTile mm_tile(uint32_t t, uint32_t f_tiles, int n_ex
   if (tiles > 1) {
     f_tile = (int)(rest / (uint32_t)size);
     row_tile = group + (int)rest - f_tile * size;
-    width = (int)((uint32_t)(rows + tiles - 1) / (uint32_t)tiles);
+    width = (int)(((uint32_t)rows + (uint32_t)tiles - 1) / (uint32_t)tiles);
   }
   width = (width + kStep - 1) / kStep * kStep;
   const int begin = row_tile * width;
@@ -499,7 +491,7 @@ template <typename O>
 __device__ __forceinline__ void mm_store(const GroupedMm& g, const MmTile& m, int c, int f, int lane,
                                          const float (&v)[32]) {
   if (f + lane >= g.n) return;
-  O* dst = static_cast<O*>(g.y) + (int64_t)(m.row + 32 * c) * g.ldy + f + lane;
+  O* dst = static_cast<O*>(g.y) + ((int64_t)m.row + 32 * c) * g.ldy + f + lane;
   const int left = m.rows - 32 * c;
   if (left >= 32) {
 #pragma unroll
@@ -558,7 +550,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
     unit >>= shift;
     units >>= shift;
   }
-  const int seg = segment<V, sizeof(O) == 4 ? V::kSegment32 : V::kSegment16>(kb1 - kb0);
+  const int seg = segment_blocks(kb1 - kb0, sizeof(O) == 4 ? V::kSegment32 : V::kSegment16, V::kSub);
 
   if (warp == 0) {
     Ring<V::kStages> ring;
@@ -572,7 +564,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
       const int part = m.n / S::kCtas;  // rows of x this CTA brings
       const int boxes = (part + V::kBoxRows - 1) / V::kBoxRows;
       const uint32_t bytes = S::kCtas * (kABytes + boxes * V::kBoxRows * 128);
-      const int f = m.f0 + kBM * (int)rank, row = m.row + part * (int)rank;
+      const int f = m.f0 + kBM * (int)rank, row = (int)((uint32_t)m.row + part * rank);
       for (int kb = kb0; kb < kb1; kb += V::kSub, ++fills) {
         ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
         if (!ok) break;
@@ -596,7 +588,7 @@ grouped_mm_kernel(const __grid_constant__ MmParams p) {
             for (int b = 0; b < V::kMaxN / S::kCtas / V::kBoxRows; ++b)
               if (b < boxes)
                 load_2d<V::kPair>(aj + kABytes + b * V::kBoxRows * 128, &p.x, k0,
-                                  row + b * V::kBoxRows, sig);
+                                  (int)((uint32_t)row + b * V::kBoxRows), sig);
           }
         }
         __syncwarp();
@@ -781,11 +773,9 @@ __device__ __forceinline__ WgradTile wgrad_tile(const GroupedWgrad& g, const Wgr
   x.cols = min(w.width, g.n - x.j0);
   x.n = (x.cols + kWgradStep - 1) / kWgradStep * kWgradStep;
   if (V::kSplit && part.parts > 1) {
-    const int64_t blocks = (x.rows + kBK - 1) / kBK;
-    const int shift = 31 - __clz(part.parts);  // a power of two
-    const int first = (int)(blocks * part.index >> shift) * kBK;
-    x.rows = min(x.rows, (int)(blocks * (part.index + 1) >> shift) * kBK) - first;
-    x.row += first;
+    const RowShare s = row_share(x.rows, part.index, 31 - __clz(part.parts));  // a power of two
+    x.rows = s.rows;
+    x.row += s.first;
   }
   return x;
 }
@@ -960,11 +950,11 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
       const int part = x.n / S::kCtas, boxes = (part + 63) / 64;  // columns of b this CTA brings
       const int i = x.i0 + kBM * (int)rank, j = x.j0 + part * (int)rank;
-      for (int r = 0; r < x.rows; r += kBK * V::kSub, ++fills) {
+      for (int left = x.rows; left > 0; left -= kBK * V::kSub, ++fills) {
         ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
         if (!ok) break;
         const uint32_t a = dst0 + ring.stage * S::kStage;
-        const int left = x.rows - r, y = x.row + r, blocks = min(V::kSub, (left + kBK - 1) / kBK);
+        const int y = x.row + (x.rows - left), blocks = min(V::kSub, row_blocks(left));
         // A last stage with rows to zero lands on each CTA's own barrier.
         const bool own = V::kPair && left < kBK * V::kSub && left % 16 != 0;
         if (own) {
@@ -1018,7 +1008,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, x.n, 1, 1);
-      const int seg = segment<V, V::kSegment32>((x.rows + kBK - 1) / kBK);
+      const int seg = segment_blocks(row_blocks(x.rows), V::kSegment32, V::kSub);
       for (int left = x.rows; left > 0;) {
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
@@ -1074,7 +1064,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     uint32_t tails = 0;  // per stage: parity of the next use of its `tail` barrier
     for (uint32_t t = unit; t < tiles; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
-      fills += (x.rows + kBK * V::kSub - 1) / (kBK * V::kSub);
+      fills += (row_blocks(x.rows) + V::kSub - 1) / V::kSub;
       const int left = x.rows % (kBK * V::kSub);
       if (left % 16 == 0) continue;
       const int stage = (int)((fills - 1) % V::kStages);
@@ -1115,14 +1105,14 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
         for (int i = 0; i < S::kBlocks; ++i)
           wgrad_load(dw + lane * g.lddw + (2 * i + half) * 32,
                      old && row + lane < g.m ? x.cols - (2 * i + half) * 32 : 0, sum[i]);
-      const int seg = segment<V, V::kSegment32>((x.rows + kBK - 1) / kBK);
-      for (int r = 0; r < x.rows; r += seg * kBK, ++use) {
+      const int blocks = row_blocks(x.rows), seg = segment_blocks(blocks, V::kSegment32, V::kSub);
+      for (int b = 0; b < blocks; b += seg, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < S::kBlocks; ++i)
           if ((2 * i + half) * 32 < x.n)
-            add_acc(tmem, use & 1, q, (2 * i + half) * 32, r == 0 && !old, sum[i]);
+            add_acc(tmem, use & 1, q, (2 * i + half) * 32, b == 0 && !old, sum[i]);
         release_acc<V::kPair>(c, use & 1, rank, lane);
       }
       if (!ok) break;
