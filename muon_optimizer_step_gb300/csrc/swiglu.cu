@@ -7,10 +7,10 @@
 //
 // p_r is the router's weight of row r (1 where there is none).  Elementwise work in fp32,
 // one rounding at each store, bound by HBM: 3 (5) values move per element.  For 16-bit tensors
-// s takes the fast exponential and reciprocal, whose few 2^-22 are far below the store's
-// rounding: with expf and an IEEE division the gradient was bound by instructions.
-// 98304 x 1408 in bf16, gradient: 231 us (6.0 TB/s; 264 us with expf and the division; other
-// grids, unrolling and streaming stores made no difference).
+// s takes the fast exponential, whose error of about |g| 2^-24 is far below the store's rounding,
+// and the fast division: with expf and an IEEE division the gradient was bound by instructions.
+// 98304 x 1408 in bf16, gradient: 224 us (6.2 TB/s; 232 us unrolled by two, which the compiler
+// makes of fewer loads in flight; other grids and streaming stores made no difference).
 //
 // kTpr threads share a row: a warp where there are many rows (dp then needs shuffles only), a
 // block where there are few, so that a small batch still fills the machine with loads
@@ -52,14 +52,17 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& r) {
   }
 }
 
+// With e = exp(-|x|), 1 / (1 + e) for x >= 0 and e / (1 + e) below: no power overflows and no
+// reciprocal is flushed to 0, as that of 1 + exp(-x) would be from x = -87.3 down.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float x) {
-  if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
-  else return __fdividef(1.f, 1.f + __expf(-x));
+  const float e = sizeof(T) == 4 ? expf(-fabsf(x)) : __expf(-fabsf(x));
+  const float r = sizeof(T) == 4 ? 1.f / (1.f + e) : __fdividef(1.f, 1.f + e);
+  return x < 0.f ? e * r : r;
 }
 
 template <typename T, int V, int kTpr>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
 swiglu_kernel(const T* __restrict__ g, int64_t ldg, const T* __restrict__ u, int64_t ldu,
               T* __restrict__ a, int64_t lda, const float* __restrict__ p, int64_t rows,
               int32_t cols) {
@@ -95,7 +98,7 @@ swiglu_grad_kernel(const T* __restrict__ da, int64_t ldda, const T* __restrict__
        r += step) {
     const float w = p != nullptr ? p[r] : 1.f;
     float sum = 0.f;
-#pragma unroll 2
+#pragma unroll 1
     for (uint32_t c = t * V; c < (uint32_t)cols; c += kTpr * V) {
       const Vec<T, V> dv = load_vec<T, V>(da + r * ldda + c), gv = load_vec<T, V>(g + r * ldg + c),
                       uv = load_vec<T, V>(u + r * ldu + c);
