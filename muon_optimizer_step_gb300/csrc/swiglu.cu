@@ -8,9 +8,10 @@
 // p_r is the router's weight of row r (1 where there is none).  Elementwise work in fp32,
 // one rounding at each store, bound by HBM: 3 (5) values move per element.  For 16-bit tensors
 // s takes the fast exponential, whose error of about |g| 2^-24 is far below the store's rounding,
-// and the fast division: with expf and an IEEE division the gradient was bound by instructions.
-// 98304 x 1408 in bf16, gradient: 224 us (6.2 TB/s; 232 us unrolled by two, which the compiler
-// makes of fewer loads in flight; other grids and streaming stores made no difference).
+// and the fast division (2 ulp): with expf and an IEEE division the gradient was bound by
+// instructions.  Where dp, an fp32 result, is asked for, it takes expf.
+// 98304 x 1408 in bf16, gradient: 222 us without dp, 227 with it (6.1 TB/s; 10 us more unrolled by
+// two, with fewer loads in flight; other grids and streaming stores made no difference).
 //
 // kTpr threads share a row: a warp where there are many rows (dp then needs shuffles only), a
 // block where there are few, so that a small batch still fills the machine with loads
@@ -54,9 +55,10 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& r) {
 
 // With e = exp(-|x|), 1 / (1 + e) for x >= 0 and e / (1 + e) below: no power overflows and no
 // reciprocal is flushed to 0, as that of 1 + exp(-x) would be from x = -87.3 down.
-template <typename T>
+// kFast: what follows from it is rounded to 16 bits.
+template <typename T, bool kFast>
 __device__ __forceinline__ float sigmoid(float x) {
-  const float e = sizeof(T) == 4 ? expf(-fabsf(x)) : __expf(-fabsf(x));
+  const float e = kFast ? __expf(-fabsf(x)) : expf(-fabsf(x));
   const float r = sizeof(T) == 4 ? 1.f / (1.f + e) : __fdividef(1.f, 1.f + e);
   return x < 0.f ? e * r : r;
 }
@@ -78,14 +80,14 @@ swiglu_kernel(const T* __restrict__ g, int64_t ldg, const T* __restrict__ u, int
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float x = cvt(gv.v[e]);
-        put(&av.v[e], x * sigmoid<T>(x) * cvt(uv.v[e]) * w);
+        put(&av.v[e], x * sigmoid<T, sizeof(T) == 2>(x) * cvt(uv.v[e]) * w);
       }
       store_vec<T, V>(a + r * lda + c, av);
     }
   }
 }
 
-template <typename T, int V, int kTpr>
+template <typename T, int V, int kTpr, bool kDp>
 __global__ void __launch_bounds__(kThreads)
 swiglu_grad_kernel(const T* __restrict__ da, int64_t ldda, const T* __restrict__ g, int64_t ldg,
                    const T* __restrict__ u, int64_t ldu, T* __restrict__ dg, int64_t lddg,
@@ -107,7 +109,7 @@ swiglu_grad_kernel(const T* __restrict__ da, int64_t ldda, const T* __restrict__
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float d = cvt(dv.v[e]), x = cvt(gv.v[e]), y = cvt(uv.v[e]);
-        const float s = sigmoid<T>(x), silu = x * s;
+        const float s = sigmoid<T, sizeof(T) == 2 && !kDp>(x), silu = x * s;
         part = fmaf(d * silu, y, part);
         put(&ur.v[e], d * w * silu);
         put(&gr.v[e], d * w * y * (s * (1.f + x * (1.f - s))));
@@ -116,7 +118,7 @@ swiglu_grad_kernel(const T* __restrict__ da, int64_t ldda, const T* __restrict__
       store_vec<T, V>(dg + r * lddg + c, gr);
       store_vec<T, V>(du + r * lddu + c, ur);
     }
-    if (dp != nullptr) {
+    if constexpr (kDp) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if constexpr (kTpr == 32) {
@@ -157,10 +159,11 @@ cudaError_t launch_as(const SwigluArgs& s, const float* p, float* dp, int64_t ro
         static_cast<const T*>(s.ptr[0]), s.ld[0], static_cast<const T*>(s.ptr[1]), s.ld[1],
         static_cast<T*>(s.ptr[2]), s.ld[2], p, rows, cols);
   else
-    swiglu_grad_kernel<T, V, kTpr><<<grid, kThreads, 0, st>>>(
-        static_cast<const T*>(s.ptr[0]), s.ld[0], static_cast<const T*>(s.ptr[1]), s.ld[1],
-        static_cast<const T*>(s.ptr[2]), s.ld[2], static_cast<T*>(s.ptr[3]), s.ld[3],
-        static_cast<T*>(s.ptr[4]), s.ld[4], p, dp, rows, cols);
+    (dp != nullptr ? swiglu_grad_kernel<T, V, kTpr, true> : swiglu_grad_kernel<T, V, kTpr, false>)
+        <<<grid, kThreads, 0, st>>>(
+            static_cast<const T*>(s.ptr[0]), s.ld[0], static_cast<const T*>(s.ptr[1]), s.ld[1],
+            static_cast<const T*>(s.ptr[2]), s.ld[2], static_cast<T*>(s.ptr[3]), s.ld[3],
+            static_cast<T*>(s.ptr[4]), s.ld[4], p, dp, rows, cols);
   return cudaGetLastError();
 }
 

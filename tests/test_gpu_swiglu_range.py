@@ -1,4 +1,5 @@
-"""The gated activation where its exponential leaves the ordinary range, against plain 64-bit forms.
+"""The gated activation where its exponential leaves the ordinary range, and the exactness of the
+gradient of the row weights, against plain 64-bit forms.
 
 Bounds (derived): the sigmoid is e / (1 + e) or 1 / (1 + e) with e = exp(-|g|) of at most 2 ulp, a
 division of at most 2 ulp and two roundings more; with the products around it 2^-19 of the value
@@ -55,3 +56,21 @@ def test_gates_from_minus_110_to_110(capi, dtype, cols):
     terms = (D * G * U).abs()
     err = (dp.double() - (D * G * U * s).sum(1)).abs()
     assert (err <= (terms * off).sum(1) + cols * 2.0 ** -24 * (terms * s).sum(1) + 2.0 ** -149).all(), "dp"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_row_weight_gradients_are_fp32_results(capi, dtype):
+    """A row of equal gates and terms of one sign: 2 ulp for the exponential and for the division
+    (2^-22 each), four more roundings in a term and one for each addition (2^-24)."""
+    rows, cols, t = 4096, 8, DT[dtype]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    g = torch.linspace(-80, 20, rows, device="cuda")[:, None].expand(rows, cols).to(t).contiguous()
+    u, da = ((torch.rand(rows, cols, generator=gen, device="cuda") + 0.5).to(t) for _ in range(2))
+    dg, du, dp = torch.empty_like(g), torch.empty_like(g), torch.empty(rows, device="cuda")
+    capi.muon_swiglu_grad(da, g, u, dg, du, d_row_weight=dp)
+    capi.muon_check()
+    want = (da.double() * g.double() * torch.sigmoid(g.double()) * u.double()).sum(1)
+    err = ((dp.double() - want) / want).abs()
+    ok = want != 0
+    assert err[ok].max() <= 2 * 2.0 ** -22 + (4 + cols) * 2.0 ** -24
