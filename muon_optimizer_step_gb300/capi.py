@@ -277,9 +277,9 @@ def muon_step_scaled(flat_params, flat_grads, flat_momentum, layout, workspace, 
     """muon_step_grouped with the gradients multiplied by grad_scale, a CUDA tensor of one
     float32 (norm[1:] of muon_grad_norm: the step then clips by the global norm)."""
     if not isinstance(grad_scale, int):
-        if not grad_scale.is_cuda or grad_scale.numel() < 1 \
-                or _kind(grad_scale, "grad_scale") != MUON_DTYPE_F32:
-            raise ValueError("grad_scale: must be a float32 value on the GPU")
+        _device_of(grad_scale, "grad_scale")
+        if grad_scale.numel() < 1 or _kind(grad_scale, "grad_scale") != MUON_DTYPE_F32:
+            raise ValueError("grad_scale: must be a float32 value")
     arr = (GroupHparams * max(1, len(groups)))(
         *[GroupHparams(float(lr), float(wd), float(mu), 1 if nest else 0)
           for lr, wd, mu, nest in groups])
@@ -419,12 +419,29 @@ def _kind(t, name):
     return k
 
 
-def _matrix(t, name, shape=None):
-    """(pointer, row pitch, muon_dtype) of a 2-D CUDA tensor with contiguous rows.  Strides of
+def _device_of(t, name):
+    """The device that a call's tensors all have to be on: that of t, which has to be the current
+    one, where the library launches."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if _torch is None:
+        _kinds()
+    if device != _torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{device}, but cuda:{_torch.cuda.current_device()} is current")
+    return device
+
+
+def _on(t, name, device):
+    if t.get_device() != device:
+        raise ValueError(f"{name}: must be a CUDA tensor on cuda:{device}, as the call's others")
+
+
+def _matrix(t, name, device, shape=None):
+    """(pointer, row pitch, muon_dtype) of a 2-D tensor with contiguous rows.  Strides of
     dimensions of length 1 mean nothing."""
     size = t.shape
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
+    _on(t, name, device)
     if len(size) != 2 or (shape is not None and size != shape):
         raise ValueError(f"{name}: shape {tuple(size)}, expected "
                          f"{'two dimensions' if shape is None else tuple(shape)}")
@@ -434,11 +451,12 @@ def _matrix(t, name, shape=None):
     return t.data_ptr(), pitch if size[0] > 1 else max(size[1], 1), _kind(t, name)
 
 
-def _matrices(t, name):
-    """(pointer, pitch, distance between matrices, muon_dtype) of a 3-D CUDA tensor."""
+def _matrices(t, name, device):
+    """(pointer, pitch, distance between matrices, muon_dtype) of a 3-D tensor."""
     size = t.shape
-    if not t.is_cuda or len(size) != 3:
-        raise ValueError(f"{name}: must be a CUDA tensor of three dimensions")
+    _on(t, name, device)
+    if len(size) != 3:
+        raise ValueError(f"{name}: must have three dimensions")
     apart, pitch, step = t.stride()
     if step != 1 and size[2] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -446,27 +464,28 @@ def _matrices(t, name):
             apart if size[0] > 1 else max(size[1] * size[2], 1), _kind(t, name))
 
 
-def _row_floats(t, rows, name):
-    """Pointer of a contiguous float32 CUDA vector of `rows` elements (None stays None)."""
+def _row_floats(t, rows, name, device):
+    """Pointer of a contiguous float32 vector of `rows` elements (None stays None)."""
     if t is None:
         return None
-    if not t.is_cuda or t.shape != (rows,) or not t.is_contiguous() \
+    _on(t, name, device)
+    if t.shape != (rows,) or not t.is_contiguous() \
             or _kind(t, name) != MUON_DTYPE_F32:
-        raise ValueError(f"{name}: must be {rows} contiguous float32 values on the GPU")
+        raise ValueError(f"{name}: must be {rows} contiguous float32 values")
     return t.data_ptr()
 
 
-def _offsets(t, n_experts):
-    if not t.is_cuda or t.dtype != _torch.int64 or t.shape != (n_experts + 1,) \
-            or not t.is_contiguous():
-        raise ValueError(f"offsets: must be {n_experts + 1} contiguous int64 values on the GPU")
+def _offsets(t, n_experts, device):
+    _on(t, "offsets", device)
+    if t.dtype != _torch.int64 or t.shape != (n_experts + 1,) or not t.is_contiguous():
+        raise ValueError(f"offsets: must be {n_experts + 1} contiguous int64 values")
     return t.data_ptr()
 
 
-def _stream_of(stream, like):
-    """The handle of `stream`, or of the current stream of like's device."""
+def _stream_of(stream, device):
+    """The handle of `stream`, or of the device's current stream."""
     if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(like.get_device())
+        return _torch._C._cuda_getCurrentRawStream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -484,6 +503,9 @@ def _workspace(workspace, nbytes, align, like, stream):
     `stream` itself, so that nothing pending elsewhere still uses it and work behind this call
     may have it next."""
     if workspace is not None:
+        _on(workspace, "workspace", like.get_device())
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if nbytes == 0:
         return None, 0, None
@@ -504,13 +526,14 @@ def muon_grouped_mm(x, w, offsets, y, trans_w=False, workspace=None, stream=None
     (rows, n) is of their type or float32, offsets holds experts + 1 int64 values on the GPU.
     Any strides with a contiguous last dimension; operands whose rows do not start on 16 bytes
     are copied to the workspace first (allocated when None is given)."""
-    wp, ldw, apart, dtype = _matrices(w, "w")
+    device = _device_of(w, "w")
+    wp, ldw, apart, dtype = _matrices(w, "w", device)
     e, k, n = w.shape
     if trans_w:
         k, n = n, k
     rows = x.shape[0]
-    xp, ldx, xkind = _matrix(x, "x", (rows, k))
-    yp, ldy, out = _matrix(y, "y", (rows, n))
+    xp, ldx, xkind = _matrix(x, "x", device, (rows, k))
+    yp, ldy, out = _matrix(y, "y", device, (rows, n))
     if xkind != dtype or dtype == MUON_DTYPE_F32 or out not in (dtype, MUON_DTYPE_F32):
         raise ValueError("x and w must both be bfloat16 or both float16, y of their type or float32")
     nbytes = 0
@@ -521,8 +544,9 @@ def muon_grouped_mm(x, w, offsets, y, trans_w=False, workspace=None, stream=None
                "muon_grouped_mm_workspace_bytes")
         nbytes = need.value
     ws, nbytes, owner = _workspace(workspace, nbytes, WORKSPACE_ALIGN, x, stream)
-    st = lib.muon_grouped_mm(xp, ldx, wp, ldw, apart, _offsets(offsets, e), yp, ldy, rows, e, k, n,
-                             1 if trans_w else 0, dtype, out, ws, nbytes, _stream_of(stream, x))
+    st = lib.muon_grouped_mm(xp, ldx, wp, ldw, apart, _offsets(offsets, e, device), yp, ldy, rows, e, k,
+                             n, 1 if trans_w else 0, dtype, out, ws, nbytes,
+                             _stream_of(stream, device))
     if st != MUON_OK:
         raise MuonError(st, "muon_grouped_mm")
 
@@ -532,11 +556,12 @@ def muon_grouped_wgrad(a, b, offsets, dw, accumulate=False, workspace=None, stre
     dw[e] += that.  a (rows, m) and b (rows, n) are bfloat16 or float16; dw (experts, m, n) is
     float32 with any strides of its first two dimensions, e.g. a view of the flat gradient
     buffer."""
-    dp, lddw, apart, out = _matrices(dw, "dw")
+    device = _device_of(dw, "dw")
+    dp, lddw, apart, out = _matrices(dw, "dw", device)
     e, m, n = dw.shape
     rows = a.shape[0]
-    ap, lda, dtype = _matrix(a, "a", (rows, m))
-    bp, ldb, bkind = _matrix(b, "b", (rows, n))
+    ap, lda, dtype = _matrix(a, "a", device, (rows, m))
+    bp, ldb, bkind = _matrix(b, "b", device, (rows, n))
     if bkind != dtype or dtype == MUON_DTYPE_F32 or out != MUON_DTYPE_F32:
         raise ValueError("a and b must both be bfloat16 or both float16, and dw float32")
     nbytes = 0
@@ -547,55 +572,58 @@ def muon_grouped_wgrad(a, b, offsets, dw, accumulate=False, workspace=None, stre
                "muon_grouped_wgrad_workspace_bytes")
         nbytes = need.value
     ws, nbytes, owner = _workspace(workspace, nbytes, WORKSPACE_ALIGN, a, stream)
-    st = lib.muon_grouped_wgrad(ap, lda, bp, ldb, _offsets(offsets, e), dp, lddw, apart, rows, e, m,
-                                n, 1 if accumulate else 0, dtype, ws, nbytes, _stream_of(stream, a))
+    st = lib.muon_grouped_wgrad(ap, lda, bp, ldb, _offsets(offsets, e, device), dp, lddw, apart, rows, e,
+                                m, n, 1 if accumulate else 0, dtype, ws, nbytes,
+                                _stream_of(stream, device))
     if st != MUON_OK:
         raise MuonError(st, "muon_grouped_wgrad")
 
 
 def muon_swiglu(gate, up, out, row_weight=None, stream=None):
     """out = row_weight[:, None] * silu(gate) * up, row by row; all (rows, cols) of one type."""
-    g, ldg, dtype = _matrix(gate, "gate")
+    device = _device_of(gate, "gate")
+    g, ldg, dtype = _matrix(gate, "gate", device)
     shape = gate.shape
-    u, ldu, ukind = _matrix(up, "up", shape)
-    o, ldo, okind = _matrix(out, "out", shape)
+    u, ldu, ukind = _matrix(up, "up", device, shape)
+    o, ldo, okind = _matrix(out, "out", device, shape)
     if ukind != dtype or okind != dtype:
         raise ValueError("gate, up and out must have the same type")
-    st = lib.muon_swiglu(g, ldg, u, ldu, _row_floats(row_weight, shape[0], "row_weight"), o, ldo,
-                         shape[0], shape[1], dtype, _stream_of(stream, gate))
+    st = lib.muon_swiglu(g, ldg, u, ldu, _row_floats(row_weight, shape[0], "row_weight", device), o, ldo,
+                         shape[0], shape[1], dtype, _stream_of(stream, device))
     if st != MUON_OK:
         raise MuonError(st, "muon_swiglu")
 
 
 def muon_swiglu_grad(dout, gate, up, dgate, dup, row_weight=None, d_row_weight=None, stream=None):
     """The gradient of muon_swiglu: writes dgate, dup and, where given, d_row_weight."""
-    g, ldg, dtype = _matrix(gate, "gate")
+    device = _device_of(gate, "gate")
+    g, ldg, dtype = _matrix(gate, "gate", device)
     shape = gate.shape
-    d, ldd, dkind = _matrix(dout, "dout", shape)
-    u, ldu, ukind = _matrix(up, "up", shape)
-    dg, lddg, dgkind = _matrix(dgate, "dgate", shape)
-    du, lddu, dukind = _matrix(dup, "dup", shape)
+    d, ldd, dkind = _matrix(dout, "dout", device, shape)
+    u, ldu, ukind = _matrix(up, "up", device, shape)
+    dg, lddg, dgkind = _matrix(dgate, "dgate", device, shape)
+    du, lddu, dukind = _matrix(dup, "dup", device, shape)
     if not dtype == dkind == ukind == dgkind == dukind:
         raise ValueError("dout, gate, up, dgate and dup must have the same type")
     st = lib.muon_swiglu_grad(d, ldd, g, ldg, u, ldu,
-                              _row_floats(row_weight, shape[0], "row_weight"), dg, lddg, du, lddu,
-                              _row_floats(d_row_weight, shape[0], "d_row_weight"), shape[0],
-                              shape[1], dtype, _stream_of(stream, gate))
+                              _row_floats(row_weight, shape[0], "row_weight", device), dg, lddg, du, lddu,
+                              _row_floats(d_row_weight, shape[0], "d_row_weight", device), shape[0],
+                              shape[1], dtype, _stream_of(stream, device))
     if st != MUON_OK:
         raise MuonError(st, "muon_swiglu_grad")
 
 
 # ------------------------------------------------------------------ gradient norm, clipping
-def _tensor_list(tensors, name):
+def _tensor_list(tensors, name, device):
     """(array that owns it, address) of muon_tensor records (pointer, length, type as three
-    64-bit words; the machine is little-endian) of contiguous CUDA tensors."""
+    64-bit words; the machine is little-endian) of contiguous tensors."""
     kinds = _KINDS or _kinds()
     try:
         flat = [v for t in tensors for v in (t.data_ptr(), t.numel(), kinds[t.dtype])]
     except KeyError as e:
         raise ValueError(f"{name}: type {e.args[0]}; float32, bfloat16 or float16 is needed") from None
-    if not all([t.is_cuda and t.is_contiguous() for t in tensors]):
-        raise ValueError(f"{name}: must be contiguous CUDA tensors")
+    if not all([t.get_device() == device and t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name}: must be contiguous CUDA tensors on cuda:{device}, as norm")
     words = array.array("Q", flat)
     return words, words.buffer_info()[0]
 
@@ -603,8 +631,9 @@ def _tensor_list(tensors, name):
 def _clip_call(grads, norm, workspace, stream):
     """(grads' records and their owner, norm's pointer, workspace pointer, bytes and owner,
     stream)."""
-    np = _row_floats(norm, 2, "norm")
-    words, g = _tensor_list(grads, "grads")
+    device = _device_of(norm, "norm")
+    np = _row_floats(norm, 2, "norm", device)
+    words, g = _tensor_list(grads, "grads", device)
     nbytes = 0
     if workspace is None:
         need = _SZ()
@@ -612,7 +641,7 @@ def _clip_call(grads, norm, workspace, stream):
                "muon_clip_workspace_bytes")
         nbytes = need.value
     ws, nbytes, owner = _workspace(workspace, nbytes, 8, norm, stream)
-    return g, words, np, ws, nbytes, owner, _stream_of(stream, norm)
+    return g, words, np, ws, nbytes, owner, _stream_of(stream, device)
 
 
 def muon_grad_norm(grads, max_norm, norm, workspace=None, stream=None):
@@ -627,7 +656,7 @@ def muon_clip_grads(grads, outs, max_norm, norm, workspace=None, stream=None):
     of its length and of its type or float32."""
     if len(outs) != len(grads):
         raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
-    out_words, o = _tensor_list(outs, "outs")
+    out_words, o = _tensor_list(outs, "outs", _device_of(norm, "norm"))
     g, words, np, ws, nbytes, owner, st = _clip_call(grads, norm, workspace, stream)
     _check(lib.muon_clip_grads(g, o, len(grads), max_norm, np, ws, nbytes, st), "muon_clip_grads")
 
