@@ -855,7 +855,7 @@ __device__ __forceinline__ void wgrad_store(float* dw, int64_t lddw, int rows, i
 }
 
 // The same by TMA, which drops what lies outside the matrix: the warp's only waits are for the
-// previous block to have left `stage`.  dw must start on 16 bytes in every row.
+// previous block to have left `stage`.  Every row of dw must start and end on 16 bytes.
 __device__ __forceinline__ void wgrad_store_bulk(const CUtensorMap* map, int expert, int row, int col,
                                                  int lane, const float (&v)[32], float4* stage) {
   if (lane == 0) bulk_wait_read();
@@ -1428,8 +1428,9 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
     if (e == cudaSuccess) e = encode(&p.a, a, g.dtype, false, 64);
     if (e == cudaSuccess) e = encode(&p.b, b, g.dtype, false, 64);
   }
-  // Written by TMA where every row of dw starts on 16 bytes.
-  p.bulk = reinterpret_cast<uintptr_t>(g.dw) % 16 == 0 && g.lddw % 4 == 0 &&
+  // Written by TMA where every row of dw starts and ends on 16 bytes: a store fills the last 16
+  // bytes of a row whole, with what lies behind the row's end in them.
+  p.bulk = reinterpret_cast<uintptr_t>(g.dw) % 16 == 0 && g.lddw % 4 == 0 && g.n % 4 == 0 &&
            (g.n_experts == 1 || g.dw_stride % 4 == 0);
   if (e == cudaSuccess && p.bulk)
     e = encode(&p.dw, {g.dw, g.m, g.n, g.lddw, g.n_experts, g.dw_stride}, kF32, true, 32);
