@@ -336,7 +336,8 @@ muon_status muon_grouped_mm_workspace_bytes(const void* x, int64_t ldx, const vo
  * matrix in fp32, or (accumulate != 0) dw_e += that sum.  a: rows x m, b: rows x n, both of
  * type dtype (MUON_DTYPE_BF16 or _F16).  With x and dy this is the gradient of a k x n weight,
  * with dy and x that of an n x k one; dw may point into the flat gradient buffer of an
- * unsharded layout.  An expert without rows gets zeros (accumulate: is left as it is).
+ * unsharded layout.  Rows of dw must not overlap: experts lie one behind the other, or their
+ * rows side by side.  An expert without rows gets zeros (accumulate: is left as it is).
  * workspace as for muon_grouped_mm. */
 muon_status muon_grouped_wgrad(const void* a, int64_t lda, const void* b, int64_t ldb,
                                const int64_t* row_offsets, float* dw, int64_t lddw,

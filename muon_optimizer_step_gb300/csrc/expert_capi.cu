@@ -134,6 +134,18 @@ muon_status check_mm(const GroupedMm& g) {
   return MUON_OK;
 }
 
+// Whether no two rows of dw share an element: experts one behind the other, rows of all experts
+// side by side, or every distance between rows of two experts looked at.
+bool rows_apart(const GroupedWgrad& g) {
+  if (g.m - 1 <= (g.dw_stride - g.n) / g.lddw || g.n_experts - 1 <= (g.lddw - g.n) / g.dw_stride)
+    return true;
+  for (int64_t e = 1; e < g.n_experts; ++e) {
+    const int64_t q = e * g.dw_stride / g.lddw, r = e * g.dw_stride - q * g.lddw;
+    if ((q < g.m && r < g.n) || (q + 1 < g.m && g.lddw - r < g.n)) return false;
+  }
+  return true;
+}
+
 muon_status check_wgrad(const GroupedWgrad& g) {
   EXPERT_TRY(check_dim(g.m, "m"));
   EXPERT_TRY(check_dim(g.n, "n"));
@@ -142,6 +154,9 @@ muon_status check_wgrad(const GroupedWgrad& g) {
   EXPERT_TRY(check_pitch(g.lddw, g.n, "lddw"));
   if (g.n_experts > 1) EXPERT_TRY(check_pitch(g.dw_stride, g.n, "dw_stride"));
   if (!grouped_wgrad_fits(g)) return fail(MUON_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles of dw");
+  if (g.n_experts > 1 && !rows_apart(g))
+    return fail(MUON_ERR_INVALID_ARG, "lddw=%lld and dw_stride=%lld: rows of dw overlap",
+                (long long)g.lddw, (long long)g.dw_stride);
   if (g.rows > 0) {
     EXPERT_TRY(check_ptr(g.a, 2, "a"));
     EXPERT_TRY(check_ptr(g.b, 2, "b"));
