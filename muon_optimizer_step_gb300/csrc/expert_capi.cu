@@ -184,7 +184,11 @@ muon_status check_swiglu(const SwigluArgs& s, const char* const* names, const fl
   return MUON_OK;
 }
 
+// Lists of up to 2^45 elements (more than any device holds), so that their chunks and bytes count in
+// 64 bits.
 muon_status check_tensors(const muon_tensor* t, int32_t n, const char* name) {
+  constexpr int64_t kMost = (int64_t)1 << 45;
+  int64_t all = 0;
   if (n < 0) return fail(MUON_ERR_INVALID_ARG, "n=%d is negative", n);
   if (n > 0 && t == nullptr) return fail(MUON_ERR_INVALID_ARG, "%s is NULL", name);
   for (int32_t i = 0; i < n; ++i) {
@@ -193,6 +197,8 @@ muon_status check_tensors(const muon_tensor* t, int32_t n, const char* name) {
     if (t[i].numel < 0)
       return fail(MUON_ERR_INVALID_ARG, "%s[%d].numel=%lld is negative", name, i,
                   (long long)t[i].numel);
+    if (t[i].numel > kMost || (all += t[i].numel) > kMost)
+      return fail(MUON_ERR_UNSUPPORTED, "%s: more elements than one call takes", name);
     if (t[i].numel == 0) continue;
     if (t[i].data == nullptr) return fail(MUON_ERR_INVALID_ARG, "%s[%d].data is NULL", name, i);
     if (reinterpret_cast<uintptr_t>(t[i].data) % dtype_size(t[i].dtype) != 0)

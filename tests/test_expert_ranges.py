@@ -1,5 +1,6 @@
 """Arguments of the expert-layer entry points that used to get past the checks, on the host.  The
 pointers are made up; no call here passes its checks."""
+import ctypes
 import itertools
 
 import pytest
@@ -43,3 +44,17 @@ def test_overlapping_rows_of_a_weight_gradient():
 ])
 def test_overlap_of_large_matrices(experts, m, n, lddw, stride, word):
     assert word in _wgrad(experts, m, n, lddw, stride)
+
+
+@pytest.mark.parametrize("numels", [[2 ** 63 - 1], [2 ** 62], [2 ** 46], [2 ** 44] * 4, [2 ** 62] * 4 + [9]])
+def test_lists_of_impossible_length(numels):
+    """Their chunks overflow 64 bits, to a workspace of a few bytes."""
+    words = (ctypes.c_uint64 * (3 * len(numels)))(*[v for n in numels for v in (0x1000, n, 0)])
+    size = ctypes.c_size_t()
+    unsupported = capi.MUON_ERR_UNSUPPORTED
+    assert capi.lib.muon_clip_workspace_bytes(words, len(numels), ctypes.byref(size)) == unsupported
+    assert "elements" in capi.muon_last_error()
+    assert capi.lib.muon_grad_norm(words, len(numels), 1.0, 0x9000, None, 0, None) == unsupported
+    assert "elements" in capi.muon_last_error()
+    assert capi.lib.muon_clip_grads(words, words, len(numels), 1.0, 0x9000, None, 0, None) == unsupported
+    assert "elements" in capi.muon_last_error()
