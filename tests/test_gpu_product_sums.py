@@ -97,3 +97,116 @@ def test_fp32_products_are_as_exact_as_plain_fp32(capi, plain_products, rows, k,
     capi.muon_check()
     want = x.double() @ w[0].double()
     assert _frobenius(y, want) <= _frobenius(x.float() @ w[0].float(), want) + 2.0 ** -24
+
+
+def _integers(gen, *shape, dtype="bf16"):
+    return torch.randint(-8, 9, shape, generator=gen, device="cuda").to(DT[dtype])
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("sizes,m,n", [
+    ([20000, 3], 72, 136),                                # one tile: shares of a cluster
+    ([19969, 0, 19983, 19984, 19985], 32, 216),           # off and on the 16-row steps
+    ([8191, 8192, 8193, 4095, 4097, 1], 130, 40),         # off and on the shares' edges
+    ([511, 512, 513, 1023, 1025, 15, 16, 17, 1], 776, 520),
+    ([2000, 1999, 65, 63, 64, 1], 264, 1416),
+])
+def test_weight_gradients_of_integers_are_exact(capi, sizes, m, n, accumulate):
+    """Sums of products of integers up to 8 stay below 2^24: every row has to be in, exactly once."""
+    gen = _gen(sum(sizes))
+    a, b = _integers(gen, sum(sizes), m), _integers(gen, sum(sizes), n)
+    dw = _integers(gen, len(sizes), m, n, dtype="fp32")
+    want = torch.stack([x.double().T @ y.double() for x, y in zip(a.split(sizes), b.split(sizes))])
+    if accumulate:
+        want += dw
+    capi.muon_grouped_wgrad(a, b, _offsets(sizes), dw, accumulate=accumulate)
+    capi.muon_check()
+    assert torch.equal(dw.double(), want)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("sizes,k,n", [
+    ([33], 2047, 130), ([1], 2049, 264), ([3, 0, 2], 4097, 77), ([64], 1023, 520), ([7, 9], 8255, 136),
+    ([700, 300, 0, 900], 1609, 2312), ([64, 1, 40], 777, 1416),
+])
+def test_products_of_integers_are_exact(capi, sizes, k, n, trans):
+    gen = _gen(k + n)
+    x = _integers(gen, sum(sizes), k, dtype="fp16")
+    w = _integers(gen, *((len(sizes), n, k) if trans else (len(sizes), k, n)), dtype="fp16")
+    y = torch.empty(sum(sizes), n, device="cuda")
+    capi.muon_grouped_mm(x, w, _offsets(sizes), y, trans_w=trans)
+    capi.muon_check()
+    want = torch.cat([a.double() @ (b.double().T if trans else b.double())
+                      for a, b in zip(x.split(sizes), w)])
+    assert torch.equal(y.double(), want)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("sizes,k,n", [([1], 2048, 256), ([0, 3, 2, 0], 1600, 264), ([33], 1090, 130),
+                                       ([2, 7], 4099, 77)])
+def test_special_values_in_split_products(capi, sizes, k, n, trans):
+    """k split over a cluster: a NaN or infinity of any part reaches its row (or, in the weight, its
+    column of its expert's rows), and nothing else."""
+    gen = _gen(k)
+    rows = sum(sizes)
+    x = (0.5 + torch.rand(rows, k, generator=gen, device="cuda")).bfloat16()
+    w = (0.5 + torch.rand(len(sizes), k, n, generator=gen, device="cuda")).bfloat16()
+    off = _offsets(sizes)
+    edge = off.tolist()
+
+    def product():
+        y = torch.empty(rows, n, device="cuda")
+        capi.muon_grouped_mm(x, w.mT.contiguous() if trans else w, off, y, trans_w=trans)
+        capi.muon_check()
+        return y
+
+    y0 = product()
+    assert torch.isfinite(y0).all()
+    for at in (0, k // 8 - 1, k // 2, k - 1):        # some part's k, the last one's among them
+        for value in (float("nan"), float("inf"), float("-inf")):
+            old = x[rows - 1, at].clone()
+            x[rows - 1, at] = value
+            y = product()
+            x[rows - 1, at] = old
+            assert torch.equal(y[:-1], y0[:-1])
+            assert torch.isnan(y[-1]).all() if value != value else (y[-1] == value).all()
+            e = max(i for i, s in enumerate(sizes) if s)
+            old = w[e, at, n - 1].clone()
+            w[e, at, n - 1] = value
+            y = product()
+            w[e, at, n - 1] = old
+            hit = y[edge[e]:edge[e + 1], n - 1]
+            assert torch.isnan(hit).all() if value != value else (hit == value).all()
+            y[edge[e]:edge[e + 1], n - 1] = y0[edge[e]:edge[e + 1], n - 1]
+            assert torch.equal(y, y0)
+
+
+@pytest.mark.parametrize("sizes,m,n", [([5000], 32, 216), ([2300, 0, 4097, 1], 72, 136), ([9, 1500], 256, 65)])
+def test_special_values_in_split_weight_gradients(capi, sizes, m, n):
+    """Rows split over a cluster: the same for a NaN or infinity in any share's rows."""
+    gen = _gen(m)
+    a = (0.5 + torch.rand(sum(sizes), m, generator=gen, device="cuda")).bfloat16()
+    b = (0.5 + torch.rand(sum(sizes), n, generator=gen, device="cuda")).bfloat16()
+    off = _offsets(sizes)
+    edge = off.tolist()
+
+    def gradient():
+        dw = torch.empty(len(sizes), m, n, device="cuda")
+        capi.muon_grouped_wgrad(a, b, off, dw)
+        capi.muon_check()
+        return dw
+
+    d0 = gradient()
+    assert torch.isfinite(d0).all()
+    for e, size in enumerate(sizes):
+        for row in {0, size // 3, size // 2, size - 1} if size else ():
+            for value in (float("nan"), float("inf")):
+                at = edge[e] + row
+                old = a[at, m - 1].clone()
+                a[at, m - 1] = value
+                dw = gradient()
+                a[at, m - 1] = old
+                hit = dw[e, m - 1]
+                assert torch.isnan(hit).all() if value != value else (hit == value).all()
+                dw[e, m - 1] = d0[e, m - 1]
+                assert torch.equal(dw, d0)
