@@ -12,7 +12,6 @@ namespace muon {
 
 constexpr int kErrTimeout = 4;      // matches MUON_ERR_TIMEOUT
 constexpr int kErrDeviceCheck = 7;  // matches MUON_ERR_DEVICE_CHECK
-constexpr int kErrRowOffsets = 8;   // matches MUON_ERR_ROW_OFFSETS
 
 // Kernel arguments: up to 128 shard base pointers, passed by value.
 struct ShardPtrs {

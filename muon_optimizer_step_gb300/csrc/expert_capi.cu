@@ -14,7 +14,7 @@ using namespace muon;
 namespace {
 
 static_assert(kF32 == MUON_DTYPE_F32 && kBf16 == MUON_DTYPE_BF16 && kF16 == MUON_DTYPE_F16, "");
-static_assert(kMaxExperts == MUON_MAX_EXPERTS, "");
+static_assert(kMaxExperts == MUON_MAX_EXPERTS && kErrRowOffsets == MUON_ERR_ROW_OFFSETS, "");
 static_assert(sizeof(TensorSpec) == sizeof(muon_tensor), "muon_tensor and TensorSpec must agree");
 
 muon_status fail(muon_status s, const char* fmt, ...) {

@@ -95,6 +95,7 @@ cudaError_t launch_selftest_timeout(int* err, long long budget, cudaStream_t st)
 // ---- expert layer (expert_capi.cu)
 constexpr int kF32 = 0, kBf16 = 1, kF16 = 2;  // muon_dtype values
 constexpr int kMaxExperts = 1024;             // MUON_MAX_EXPERTS
+constexpr int kErrRowOffsets = 8;             // MUON_ERR_ROW_OFFSETS
 
 struct GroupedMm {            // y = x W_e per expert (see muon_grouped_mm)
   const void* x;
