@@ -914,6 +914,7 @@ template <typename V>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
   using S = Shape<V>;
+  static_assert(V::kSub == 1, "a stage is a k-block");
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -950,24 +951,20 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
       const int part = x.n / S::kCtas, boxes = (part + 63) / 64;  // columns of b this CTA brings
       const int i = x.i0 + kBM * (int)rank, j = x.j0 + part * (int)rank;
-      for (int left = x.rows; left > 0; left -= kBK * V::kSub, ++fills) {
+      for (int left = x.rows; left > 0; left -= kBK, ++fills) {
         ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
         if (!ok) break;
         const uint32_t a = dst0 + ring.stage * S::kStage;
-        const int y = x.row + (x.rows - left), blocks = min(V::kSub, row_blocks(left));
+        const int y = x.row + (x.rows - left);
         // A last stage with rows to zero lands on each CTA's own barrier.
-        const bool own = V::kPair && left < kBK * V::kSub && left % 16 != 0;
+        const bool own = V::kPair && left < kBK && left % 16 != 0;
         if (own) {
           const uint32_t bar = (rank == 0 ? full0 : tail0) + 8 * ring.stage;
           if (elect_one()) {
-            expect(bar, blocks * (2 + boxes) * kBox);
-            for (int q = 0; q < blocks; ++q) {
-              const uint32_t aq = a + q * S::kBlock;
-              for (int b = 0; b < 2; ++b)
-                load_2d<false>(aq + b * kBox, &p.a, i + 64 * b, y + q * kBK, bar);
-              for (int b = 0; b < boxes; ++b)
-                load_2d<false>(aq + kABytes + b * kBox, &p.b, j + 64 * b, y + q * kBK, bar);
-            }
+            expect(bar, (2 + boxes) * kBox);
+            for (int b = 0; b < 2; ++b) load_2d<false>(a + b * kBox, &p.a, i + 64 * b, y, bar);
+            for (int b = 0; b < boxes; ++b)
+              load_2d<false>(a + kABytes + b * kBox, &p.b, j + 64 * b, y, bar);
           }
           if (rank != 0) {
             tails ^= 1u << ring.stage;
@@ -975,18 +972,12 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
           }
         } else if (elect_one()) {
           const uint32_t sig = sig0 + 8 * ring.stage;
-          if (rank == 0) expect(full0 + 8 * ring.stage, S::kCtas * blocks * (2 + boxes) * kBox);
+          if (rank == 0) expect(full0 + 8 * ring.stage, S::kCtas * (2 + boxes) * kBox);
+          load_2d<V::kPair>(a, &p.a, i, y, sig);
+          load_2d<V::kPair>(a + kBox, &p.a, i + 64, y, sig);
 #pragma unroll
-          for (int q = 0; q < V::kSub; ++q) {
-            if (q >= blocks) break;
-            const uint32_t aq = a + q * S::kBlock;
-            load_2d<V::kPair>(aq, &p.a, i, y + q * kBK, sig);
-            load_2d<V::kPair>(aq + kBox, &p.a, i + 64, y + q * kBK, sig);
-#pragma unroll
-            for (int b = 0; b < V::kMaxN / S::kCtas / 64; ++b)
-              if (b < boxes)
-                load_2d<V::kPair>(aq + kABytes + b * kBox, &p.b, j + 64 * b, y + q * kBK, sig);
-          }
+          for (int b = 0; b < V::kMaxN / S::kCtas / 64; ++b)
+            if (b < boxes) load_2d<V::kPair>(a + kABytes + b * kBox, &p.b, j + 64 * b, y, sig);
         }
         __syncwarp();
         ring.next();
@@ -1008,20 +999,19 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
       const uint32_t idesc = idesc_16(g.dtype == kBf16, S::kM, x.n, 1, 1);
-      const int seg = segment_blocks(row_blocks(x.rows), V::kSegment32, V::kSub);
+      const int seg = segment_blocks(row_blocks(x.rows), V::kSegment32, 1);
       for (int left = x.rows; left > 0;) {
         ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (use & 1) * kAccCols;
         uint32_t add = 0;
-        for (int in = 0; in < seg && left > 0; in += V::kSub, left -= kBK * V::kSub) {
+        for (int in = 0; in < seg && left > 0; ++in, left -= kBK) {
           ok = wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
           if (!ok) break;
-          if (left < kBK * V::kSub && left % 16 != 0) {
+          if (left < kBK && left % 16 != 0) {
             // The rows behind the expert's last are the next expert's.
-            zero_rows(smem + ring.stage * S::kStage + left / kBK * S::kBlock, left % kBK,
-                      2 + (x.n / S::kCtas + 63) / 64, lane);
+            zero_rows(smem + ring.stage * S::kStage, left, 2 + (x.n / S::kCtas + 63) / 64, lane);
             if (V::kPair) {
               ok = __all_sync(0xffffffffu, wait_peer(&c.fixed[ring.stage], fixes >> ring.stage & 1,
                                                      g.err, &c.abort));
@@ -1032,13 +1022,9 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
           const uint32_t a = a0 + ring.stage * (S::kStage / 16), b = b0 + ring.stage * (S::kStage / 16);
           if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < V::kSub; ++j) {
-              const uint32_t aj = a + j * (S::kBlock / 16), bj = b + j * (S::kBlock / 16);
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                if (left > j * kBK + s * 16)
-                  mma<V::kPair>(d, aj + s * kStep, bj + s * kStep, idesc, (j | s) == 0 ? add : 1);
-            }
+            for (int s = 0; s < 4; ++s)
+              if (left > s * 16)
+                mma<V::kPair>(d, a + s * kStep, b + s * kStep, idesc, s == 0 ? add : 1);
             commit<V::kPair>(&c.empty[ring.stage]);
           }
           __syncwarp();
@@ -1064,16 +1050,15 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
     uint32_t tails = 0;  // per stage: parity of the next use of its `tail` barrier
     for (uint32_t t = unit; t < tiles; t += units) {
       const WgradTile x = wgrad_tile<V>(g, w, t, bad, split);
-      fills += (row_blocks(x.rows) + V::kSub - 1) / V::kSub;
-      const int left = x.rows % (kBK * V::kSub);
+      fills += row_blocks(x.rows);
+      const int left = x.rows % kBK;
       if (left % 16 == 0) continue;
       const int stage = (int)((fills - 1) % V::kStages);
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c.tail[stage], tails >> stage & 1, kWaitBudget,
                                                      g.err, &c.abort)))
         break;
       tails ^= 1u << stage;
-      zero_rows(smem + stage * S::kStage + left / kBK * S::kBlock, left % kBK,
-                2 + (x.n / S::kCtas + 63) / 64, lane);
+      zero_rows(smem + stage * S::kStage, left, 2 + (x.n / S::kCtas + 63) / 64, lane);
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&c.fixed[stage]), 0));
     }
   } else if (warp >= 4) {
@@ -1105,7 +1090,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
         for (int i = 0; i < S::kBlocks; ++i)
           wgrad_load(dw + lane * g.lddw + (2 * i + half) * 32,
                      old && row + lane < g.m ? x.cols - (2 * i + half) * 32 : 0, sum[i]);
-      const int blocks = row_blocks(x.rows), seg = segment_blocks(blocks, V::kSegment32, V::kSub);
+      const int blocks = row_blocks(x.rows), seg = segment_blocks(blocks, V::kSegment32, 1);
       for (int b = 0; b < blocks; b += seg, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
