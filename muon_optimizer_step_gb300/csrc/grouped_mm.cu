@@ -82,10 +82,11 @@ constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 // the loads or MMAs of one narrow k-block (one token 12.5 -> 9.2 us).  Where the MMAs take 500
 // cycles a k-block, the finer stages are ahead (Pair: 328 against 335 us on 98304 x 1408 -> 2048).
 // kSegment16, kSegment32: most k-blocks per segment of a sum that is stored in 16 or 32 bits.  The
-// MMAs wait where a segment ends before the last tile's stores have left the epilogue free:
-// wide tiles pay for short segments (24570 rows, 2048 -> 1408, 16-bit: 111 us with 11, 118 with 8;
-// weight gradient of 98304 rows, 64 x 2048 x 1408: 403 us with 12, 422 with 8, 452 with 6, 523
-// with 4), the others do not.  kSegment32 is the longest whose error is a plain product's.
+// MMAs wait where a segment ends before the last tile's stores have left the epilogue free: pairs,
+// which multiply fastest, pay for short segments (24570 rows, 2048 -> 1408, 16-bit: 111 us with
+// 11, 118 with 8; weight gradient of 98304 rows, 64 x 2048 x 1408: 403 us with 12, 422 with 8, 452
+// with 6, 523 with 4), the others little (weight gradient of 24576 rows: 188 us with 12, 192 with
+// 4).  kSegment32 gives no more error than a plain fp32 product has.
 struct Pair {
   static constexpr bool kPair = true, kSplit = false;
   static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1;
@@ -94,7 +95,7 @@ struct Pair {
 struct Wide {
   static constexpr bool kPair = false, kSplit = false;
   static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
-  static constexpr int kSegment16 = 8, kSegment32 = 6;
+  static constexpr int kSegment16 = 8, kSegment32 = 4;
 };
 struct Narrow {
   static constexpr bool kPair = false, kSplit = false;

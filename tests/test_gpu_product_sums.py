@@ -71,7 +71,8 @@ def plain_products():
 
 
 @pytest.mark.parametrize("experts,rows,m,n", [(1, 1536, 520, 1416), (1, 1536, 72, 136), (1, 20000, 72, 136),
-                                              (1, 20000, 776, 1416), (8, 1536, 2048, 1408)])
+                                              (1, 20000, 776, 1416), (8, 1536, 2048, 1408), (13, 320, 130, 520),
+                                              (64, 384, 256, 1408)])
 def test_weight_gradients_are_as_exact_as_plain_fp32(capi, plain_products, experts, rows, m, n):
     """At most one rounding (2^-24) more than torch's fp32 product of the same values."""
     gen = _gen(rows + m)
