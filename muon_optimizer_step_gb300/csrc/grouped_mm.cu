@@ -1385,23 +1385,27 @@ cudaError_t launch_grouped_mm(const GroupedMm& g, void* workspace, int sms, cuda
   //  - A k-split where every cluster gets an SM for each of its CTAs, and one tile (6 rows,
   //    2048 -> 1408: 13.8 without, 9.2 with; 1 row: 13.5 and 5.9).
   //  - Few rows per expert, up to a narrow tile's: streaming the weights is the whole cost
-  //    (64 experts, 2048 -> 1408, average rows 32: narrow 58.7, pairs 66.5; 64: 65.0 and 69.1;
-  //    80: 72.5 and 70.1).  Few tiles: the more SMs work (1 expert, 512 rows, 2048 -> 2048:
-  //    narrow 11.0, wide 14.5).
-  //  - Pairs from two tiles for each pair of SMs on (8 experts, 2048 rows: 96 tiles, pairs
-  //    16.8, wide 15.0; 64 experts, 24570 rows: pairs 109, wide 125).
+  //    (64 experts, 2048 -> 1408, average rows 32: narrow 59.8, pairs 66.9; 64: 65.1 and 69.4;
+  //    80: 76.2 and 70.9).  Few tiles: the more SMs work (1 expert, 512 rows, 2048 -> 2048:
+  //    narrow 11.2, wide 14.8).
+  //  - Pairs for 16-bit results, from two tiles for each pair of SMs on (8 experts, 2048 -> 2048,
+  //    2048 rows: 128 tiles, pairs 25.6, wide 25.9; 4096 rows: 36.2 and 39.4; 64 experts, 2048 ->
+  //    1408, 24570 rows: 117 and 129).  The shorter segments of fp32 results hold pairs up (the last
+  //    two: 53.0 and 45.4, 147 and 142; 98304 rows, 1408 -> 2048: 425 and 437).
   int parts = 1;
   while (parts < kMostParts && mm_tiles<Split>(g) * parts * 2 <= sms && g.k >= 4 * kBK * parts * 2)
     parts *= 2;
   const bool narrow = g.rows <= Narrow::kMaxN * (int64_t)g.n_experts || mm_tiles<Narrow>(g) <= sms;
-  const bool pair = !narrow && g.n > kBM && mm_tiles<Pair>(g) >= sms;
+  const bool pair = !narrow && g.out_dtype != kF32 && g.n > kBM && mm_tiles<Pair>(g) >= sms;
   if (e == cudaSuccess)
     e = encode(&p.x, x, g.dtype, false, parts > 1 || narrow ? Narrow::kBoxRows : Wide::kBoxRows);
   if (e == cudaSuccess) e = encode(&p.w, w, g.dtype, true, g.trans ? kBM : 64);
   if (e != cudaSuccess) return e;
   return parts > 1 ? launch_mm_as<Split>(p, parts, sms, st)
          : narrow  ? launch_mm_as<Narrow>(p, 1, sms, st)
-         : pair    ? launch_mm_as<Pair>(p, 1, sms, st) : launch_mm_as<Wide>(p, 1, sms, st);
+         : !pair   ? launch_mm_as<Wide>(p, 1, sms, st)
+         : g.out_dtype == kBf16 ? launch_mm<Pair, __nv_bfloat16>(p, 1, sms, st)
+                                : launch_mm<Pair, __half>(p, 1, sms, st);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms, cudaStream_t st) {
@@ -1422,8 +1426,8 @@ cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms
     e = encode(&p.dw, {g.dw, g.m, g.n, g.lddw, g.n_experts, g.dw_stride}, kF32, true, 32);
   if (e != cudaSuccess) return e;
   p.max_n = 256;
-  // Pairs for many rows (64 experts of 2048 x 1408, average rows 768: pairs 252, wide 277 us;
-  // 384: 192 and 187).
+  // Pairs for many rows (64 experts of 2048 x 1408, average rows 768: pairs 279, wide 286 us, adding
+  // 421 and 449; 384: 195 and 190, adding 333 and 313).
   if (g.m > kBM && wgrad_grid<Pair>(g, 256).tiles >= sms / 2 && g.rows >= 512 * (int64_t)g.n_experts)
     return launch_wgrad<Pair>(p, 1, sms, st);
   // Few tiles: with many rows several CTAs for each (32 x 216 from 7855 rows 33.6 -> 12.6 us),
