@@ -304,11 +304,12 @@ muon_status muon_orthogonalize_full_noalloc(const muon_layout* layout, const flo
  * Sizes.  1 <= n_experts <= MUON_MAX_EXPERTS, 0 <= rows < 2^31, 1 <= k, n, m < 2^31.  ld* are
  * row pitches in elements (at least the row length); *_stride is the distance in elements
  * between two experts' matrices, so they may lie in a flat buffer among others.
- * Pointers need their element's alignment only.  Outputs must not overlap inputs.
+ * Pointers need their element's alignment only, and are of the current device, where the calls
+ * launch.  Outputs must not overlap inputs.
  * The first of these calls on a device allocates its error word: make it before any CUDA-graph
  * capture.  The calls keep nothing between them and may be used from several threads.
- * Arithmetic.  Products of the 16-bit inputs are summed in fp32 and rounded once, at the
- * store. */
+ * Arithmetic.  Products of the 16-bit inputs are summed in fp32, in short segments on the tensor
+ * cores, and rounded once, at the store. */
 typedef enum muon_dtype {
   MUON_DTYPE_F32 = 0,
   MUON_DTYPE_BF16 = 1,
@@ -378,7 +379,8 @@ typedef struct muon_tensor {
  * muon_clip_grads: the same, and outs[i] = norm[1] * grads[i].  outs[i] has grads[i]'s length
  * and either its type or MUON_DTYPE_F32; it may be grads[i] itself (then a coefficient of 1
  * moves nothing) but must not overlap any tensor otherwise.
- * max_norm: finite, >= 0.  workspace: muon_clip_workspace_bytes bytes, 8-byte aligned. */
+ * max_norm: finite, >= 0.  At most 2^45 elements in all.  workspace: muon_clip_workspace_bytes
+ * bytes, 8-byte aligned. */
 muon_status muon_grad_norm(const muon_tensor* grads, int32_t n, float max_norm, float* norm,
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 muon_status muon_clip_grads(const muon_tensor* grads, const muon_tensor* outs, int32_t n,

@@ -10,9 +10,9 @@
 // from offsets[n_experts] on) get zeros.
 //
 // mm computes tiles of y^T: the MMA's M = 128 is 128 columns of y (the weight is operand A) and
-// its N is up to kMaxN rows of one expert (x is operand B).  N goes in steps of 16 where M is
-// fixed, so the ragged side wastes at most 15 rows per tile instead of up to 127, and a single
-// token costs an MMA of N = 16.  An expert's rows are dealt evenly to its tiles.  Both weight
+// its N is up to kMaxN rows of one expert (x is operand B).  N goes in steps of 16 (32 on pairs)
+// where M is fixed, so the ragged side wastes at most 15 (31) rows per tile instead of up to 127,
+// and a single token costs an MMA of N = 16.  An expert's rows are dealt evenly to its tiles.  Both weight
 // layouts are operand majors of the MMA (K-major or MN-major boxes), nothing is transposed.
 // Rows that a tile's box reads past its expert are the next expert's; they reach accumulator
 // columns that are not stored.
@@ -24,20 +24,23 @@
 //
 // Large products run on CTA pairs (a 2-CTA cluster, cta_group::2): each CTA holds 128 of the
 // MMA's 256 rows and half of its N columns of operand B, so a k-block brings 32 KB instead of
-// 48 KB into each SM for the same work (98304 rows, 1408 -> 2048, 64 experts: pairs 332 us,
-// single CTAs 383).  The other tiles, and when they run, stand at the variants and launches below.
+// 48 KB into each SM for the same work (98304 rows, 1408 -> 2048, 64 experts: pairs 344 us,
+// single CTAs 387).  The other tiles, and when they run, stand at the variants and launches below.
 //
 // The tensor core truncates when it adds to its accumulator, always towards zero, so the error
 // of a sum grows with its number of steps (1.8e-6 of the result after 1536 rows).  Results are
 // therefore summed in short segments, which the epilogue adds up in registers with rounding to
 // nearest: 3.3e-7 whatever the length (3.6e-7 for a plain fp32 product of 1536 rows).  16-bit
-// results in longer ones: of whole sums of 4096 terms one in 430 is stored in bf16 other than the exact sum would be, of 16384
-// terms one in 110; in segments one in 2000 whatever the length (98304 rows, 1408 -> 2048: 336
-// us in segments, 333 whole; 24570 rows, 2048 -> 1408: 111 and 109).
+// results in longer ones: of whole sums of 4096 terms one in 430 is stored in bf16 other than the
+// exact sum would be, of 16384 terms one in 110; in segments one in 2000 whatever the length
+// (98304 rows, 1408 -> 2048: 336 us in segments, 333 whole; 24570 rows, 2048 -> 1408: 111 and
+// 109).
 //
 // CTA roles (384 threads): warp 0 issues the TMA loads, warp 1 the MMAs (on the first CTA of a
 // pair), warp 2 owns TMEM, warps 4-11 drain the accumulators (two, in TMEM's 512 columns, so a
-// tile's stores overlap the next one's MMAs).  Every wait is bounded.
+// tile's stores overlap the next one's MMAs).  Every wait on an mbarrier is bounded.  Those for the
+// other CTAs of the cluster at the start and end, for TMEM and for a CTA's own stores are not: they
+// end once the bounded ones have.
 //
 // The issuing warps walk their loops whole and elect a lane for each k-block: with one lane in
 // a divergent loop, descriptors and barrier addresses went through vector registers and issue
@@ -46,13 +49,14 @@
 //
 // Measured, per pass (the loads fill the 64 bytes a cycle that an SM takes from L2 to about
 // 90 %; in runs of more than a few ms the 1.4 kW limit lowers the clock to 1.35-1.5 GHz):
-//   98304 rows, 1408 -> 2048, 64 experts  332 us  1.71 PFLOP/s, tensor pipe 82 % busy
-//   4096 rows, 4096 -> 14336, 8 experts   296 us  1.62 PFLOP/s, 85 %
-//   24570 rows, 2048 -> 1408, 64 experts  108 us  1.31 PFLOP/s and 5.0 TB/s
-//   192 rows, 1408 -> 2048, 64 experts     53 us  6.6 TB/s (HBM)
+//   98304 rows, 1408 -> 2048, 64 experts  342 us  1.66 PFLOP/s, tensor pipe 82 % busy
+//   4096 rows, 4096 -> 14336, 8 experts   306 us  1.57 PFLOP/s, 84 %
+//   24570 rows, 2048 -> 1408, 64 experts  112 us  1.26 PFLOP/s and 4.8 TB/s
+//   192 rows, 1408 -> 2048, 64 experts     54 us  6.5 TB/s (HBM)
 //   6 rows, 2048 -> 1408, 64 experts      9.2 us  (4.5 us are launch, offsets and first load)
-//   weight gradient of the first          405 us  1.40 PFLOP/s and 3.5 TB/s, 62 %: loads alone
-//                                                 take 343, stores alone 288, MMAs alone 279
+//   weight gradient of the first          452 us  1.25 PFLOP/s and 3.1 TB/s, 55 % (403 us with
+//                                                 segments of 12: loads alone took 343, stores
+//                                                 alone 288, MMAs alone 279)
 #include <atomic>
 
 #include <cudaTypedefs.h>
@@ -86,7 +90,7 @@ constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 // which multiply fastest, pay for short segments (24570 rows, 2048 -> 1408, 16-bit: 111 us with
 // 11, 118 with 8; weight gradient of 98304 rows, 64 x 2048 x 1408: 403 us with 12, 422 with 8, 452
 // with 6, 523 with 4), the others little (weight gradient of 24576 rows: 188 us with 12, 192 with
-// 4).  kSegment32 gives no more error than a plain fp32 product has.
+// 4).  With kSegment32 the error is a plain fp32 product's or at most a rounding (2^-24) more.
 struct Pair {
   static constexpr bool kPair = true, kSplit = false;
   static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1;
@@ -1077,7 +1081,7 @@ grouped_wgrad_kernel(const __grid_constant__ WgradParams p) {
       const bool old = g.accumulate && !V::kSplit;
       if (old && p.bulk && t + units < tiles && lane < S::kBlocks) {
         // The next tile's come to L2, a block per lane (64 x 2048 x 1408 from 24570 rows: 354
-        // without, 317 us with).
+        // us without, 311 with).
         const WgradTile y = wgrad_tile<V>(g, w, t + units, bad, split);
         const int r = y.i0 + kBM * (int)rank + 32 * q, col = (2 * lane + half) * 32;
         if (r < g.m && col < y.cols)

@@ -172,8 +172,9 @@ cudaError_t launch_type(const SwigluArgs& s, const float* p, float* dp, int64_t 
                         int sms, cudaStream_t st) {
   constexpr int v = 16 / sizeof(T);
   // A warp per row where that gives every SM 32 warps, unless a row is long enough to give each
-  // thread of a block four accesses (gradient in bf16, us by warps and by blocks: 2048 x 1408 7.6
-  // and 6.6, 4864 x 1408 11.5 and 15.3, 19456 x 64 7.0 and 24.8, 9728 x 14336 226 and 213).
+  // thread of a block four accesses (gradient in bf16, us by warps and by blocks: 2048 x 1408 6.9
+  // and 7.3, forward 5.9 and 3.9; 4864 x 1408 12.3 and 17.4, 19456 x 64 8.7 and 25.7, 9728 x 14336
+  // 225 and 221).
   const bool many = rows >= (int64_t)sms * 32 && cols < 4 * kThreads * (vectors<T>(s, cols) ? v : 1);
   if (vectors<T>(s, cols))
     return many ? launch_as<T, v, 32>(s, p, dp, rows, cols, sms, st)
