@@ -388,6 +388,31 @@ muon_status muon_clip_grads(const muon_tensor* grads, const muon_tensor* outs, i
                             cudaStream_t stream);
 muon_status muon_clip_workspace_bytes(const muon_tensor* grads, int32_t n, size_t* bytes);
 
+/* ---------------------------------------------------------------- feed-forward operators
+ * What stands around and inside a layer's products in training and serving.  The pages have no
+ * counterpart.  Conventions as for the expert layers; rows are independent of each other, so a NaN
+ * stays in its row (and in the sums over rows).
+ *
+ * muon_layer_norm: y = (x - mean) * rstd * weight + bias row by row, with mean the row's mean and
+ * rstd = 1 / sqrt(its variance + eps); the variance is the mean square of the deviations from the
+ * mean.  x, y: rows x cols of type dtype (any muon_dtype); weight, bias: cols fp32 values, e.g. in
+ * the flat parameter buffer (NULL: 1 and 0).  mean, rstd: NULL, or receive rows fp32 values for
+ * the gradient.  Sums in fp32, one rounding at the store. */
+muon_status muon_layer_norm(const void* x, int64_t ldx, const float* weight, const float* bias, void* y,
+                            int64_t ldy, float* mean, float* rstd, int64_t rows, int32_t cols, float eps,
+                            int32_t dtype, cudaStream_t stream);
+/* Its gradient, from dy and the forward pass's x, mean and rstd: writes dx (rows x cols), and dweight
+ * and dbias (cols fp32 values, e.g. in the flat gradient buffer; NULL: not wanted), or (accumulate
+ * != 0) adds to those two.  The sums over the rows have a fixed order: equal inputs give equal bits.
+ * workspace: muon_layer_norm_grad_workspace_bytes bytes, 16-byte aligned; not used where dweight and
+ * dbias are both NULL. */
+muon_status muon_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                 const float* weight, const float* mean, const float* rstd, void* dx,
+                                 int64_t lddx, float* dweight, float* dbias, int64_t rows, int32_t cols,
+                                 int32_t accumulate, int32_t dtype, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+muon_status muon_layer_norm_grad_workspace_bytes(int64_t rows, int32_t cols, size_t* bytes);
+
 /* ---------------------------------------------------------------- status
  * Synchronises `stream`, then reports a device-side wait timeout recorded since the last
  * check (MUON_ERR_TIMEOUT, and clears it), a failed range check of a debug build

@@ -106,6 +106,10 @@ SIGNATURES = [
     ("muon_grad_norm", _I32, [_P, _I32, _F, _P, _P, _SZ, _P]),
     ("muon_clip_grads", _I32, [_P, _P, _I32, _F, _P, _P, _SZ, _P]),
     ("muon_clip_workspace_bytes", _I32, [_P, _I32, ctypes.POINTER(_SZ)]),
+    ("muon_layer_norm", _I32, [_P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _I32, _F, _I32, _P]),
+    ("muon_layer_norm_grad", _I32, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _I64, _I32,
+                                    _I32, _I32, _P, _SZ, _P]),
+    ("muon_layer_norm_grad_workspace_bytes", _I32, [_I64, _I32, ctypes.POINTER(_SZ)]),
 ]
 
 
@@ -668,6 +672,58 @@ def layout_grads(layout, flat_grads):
         flat_grads = [flat_grads]
     return [g[:max(0, min(layout.shard_len, layout.numel - s * layout.shard_len))]
             for s, g in enumerate(flat_grads)]
+
+
+# ------------------------------------------------------------------ feed-forward operators
+def muon_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None):
+    """y = (x - mean) * rstd * weight + bias, row by row; x and y (rows, cols) of one type.
+
+    weight and bias: cols float32 values (None: 1 and 0); mean and rstd: None, or rows float32
+    values that the gradient will take."""
+    device = _device_of(x, "x")
+    xp, ldx, dtype = _matrix(x, "x", device)
+    rows, cols = x.shape
+    yp, ldy, ykind = _matrix(y, "y", device, x.shape)
+    if ykind != dtype:
+        raise ValueError("x and y must have the same type")
+    st = lib.muon_layer_norm(xp, ldx, _row_floats(weight, cols, "weight", device),
+                             _row_floats(bias, cols, "bias", device), yp, ldy,
+                             _row_floats(mean, rows, "mean", device),
+                             _row_floats(rstd, rows, "rstd", device), rows, cols, eps, dtype,
+                             _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_layer_norm")
+
+
+def muon_layer_norm_grad(dy, x, weight, mean, rstd, dx, dweight, dbias, accumulate=False,
+                         workspace=None, stream=None):
+    """The gradient of muon_layer_norm: writes dx, and dweight and dbias (float32, None: not wanted),
+    or with accumulate adds to those two."""
+    device = _device_of(x, "x")
+    xp, ldx, dtype = _matrix(x, "x", device)
+    rows, cols = x.shape
+    dyp, lddy, dykind = _matrix(dy, "dy", device, x.shape)
+    dxp, lddx, dxkind = _matrix(dx, "dx", device, x.shape)
+    if not dtype == dykind == dxkind:
+        raise ValueError("dy, x and dx must have the same type")
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd: the forward pass's are needed")
+    nbytes = 0
+    if workspace is None and (dweight is not None or dbias is not None):
+        need = _SZ()
+        _check(lib.muon_layer_norm_grad_workspace_bytes(rows, cols, ctypes.byref(need)),
+               "muon_layer_norm_grad_workspace_bytes")
+        nbytes = need.value
+    ws, nbytes, owner = _workspace(workspace, nbytes, 16, x, stream)
+    st = lib.muon_layer_norm_grad(dyp, lddy, xp, ldx, _row_floats(weight, cols, "weight", device),
+                                  _row_floats(mean, rows, "mean", device),
+                                  _row_floats(rstd, rows, "rstd", device), dxp, lddx,
+                                  _row_floats(dweight, cols, "dweight", device),
+                                  _row_floats(dbias, cols, "dbias", device), rows, cols,
+                                  1 if accumulate else 0, dtype, ws, nbytes,
+                                  _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_layer_norm_grad")
 
 
 def muon_check(stream=None):

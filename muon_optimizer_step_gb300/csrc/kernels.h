@@ -134,6 +134,22 @@ struct SwigluArgs {
 cudaError_t launch_swiglu(const SwigluArgs& s, int dtype, const float* p, float* dp, int64_t rows,
                           int32_t cols, int sms, cudaStream_t st);
 
+// Layer norm (out = y) and its gradient (out = dx); see muon_layer_norm.  Null weights count as 1,
+// null biases as 0; null results are not wanted.
+struct NormArgs {
+  const void *x, *dy;
+  void* out;
+  const float *w, *b, *mean_in, *rstd_in;
+  float *mean, *rstd, *dw, *db;
+  float* part;                // the gradient's workspace
+  int64_t ldx, lddy, ldo, rows;
+  int32_t cols, accumulate;
+  float eps;
+};
+cudaError_t launch_layer_norm(const NormArgs& a, int dtype, int sms, cudaStream_t st);
+size_t norm_grad_workspace(int64_t rows, int32_t cols);
+cudaError_t launch_layer_norm_grad(const NormArgs& a, int dtype, int sms, cudaStream_t st);
+
 struct TensorSpec {           // same layout as muon_tensor
   void* data;
   int64_t numel;
