@@ -413,6 +413,59 @@ muon_status muon_layer_norm_grad(const void* dy, int64_t lddy, const void* x, in
                                  size_t workspace_bytes, cudaStream_t stream);
 muon_status muon_layer_norm_grad_workspace_bytes(int64_t rows, int32_t cols, size_t* bytes);
 
+/* A gated feed-forward block: out = row weight * silu(x Wg) * (x Wu), and what its backward pass needs
+ * beside muon_grouped_wgrad.  Products per expert over ragged rows, as muon_grouped_mm, or
+ * (row_offsets NULL, n_experts 1) one dense product of all rows.  Weights are stored k x n, or
+ * (trans_w != 0) n x k.  dtype: MUON_DTYPE_BF16 or _F16 of every matrix.  Sums and activations in
+ * fp32, one rounding at each store.  Rows of no expert get zeros in every result.  workspace: what
+ * the call's *_workspace_bytes says (copies of operands whose rows do not start on 16 bytes), 1024-byte
+ * aligned; NULL is accepted for 0 bytes.
+ *
+ * muon_gated_mm: both projections, the activation and their product in one kernel.  x: rows x k, out:
+ * rows x n; row_weight: rows fp32 values (NULL: 1); gate, up: NULL, or receive x Wg and x Wu
+ * (rows x n) for the backward pass. */
+muon_status muon_gated_mm(const void* x, int64_t ldx, const void* w_gate, int64_t ldw_gate,
+                          int64_t w_gate_stride, const void* w_up, int64_t ldw_up, int64_t w_up_stride,
+                          const int64_t* row_offsets, const float* row_weight, void* out, int64_t ld_out,
+                          void* gate, int64_t ld_gate, void* up, int64_t ld_up, int64_t rows,
+                          int32_t n_experts, int32_t k, int32_t n, int32_t trans_w, int32_t dtype,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+muon_status muon_gated_mm_workspace_bytes(const void* x, int64_t ldx, const void* w_gate, int64_t ldw_gate,
+                                          int64_t w_gate_stride, const void* w_up, int64_t ldw_up,
+                                          int64_t w_up_stride, int64_t rows, int32_t n_experts, int32_t k,
+                                          int32_t n, int32_t trans_w, size_t* bytes);
+/* muon_gated_mm_grad: the gradient through the block's second product and its activation in one
+ * kernel.  With dh = dy W per expert (W the down projection: stored inner x hidden it is n x k here, so
+ * trans_w != 0; dy: rows x k, dh: rows x n, never stored) and the gate and up that the forward
+ * pass kept: dup = dh p silu(gate), dgate = dh p up silu'(gate), out = p silu(gate) up (NULL: not
+ * wanted; the down projection's weight gradient takes it) and d_row_weight[r] = sum over the row of
+ * dh silu(gate) up (fp32; NULL: not wanted; row_weight_grad != 0 in the workspace query). */
+muon_status muon_gated_mm_grad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t w_stride,
+                               const int64_t* row_offsets, const void* gate, int64_t ld_gate,
+                               const void* up, int64_t ld_up, const float* row_weight, void* dgate,
+                               int64_t ld_dgate, void* dup, int64_t ld_dup, void* out, int64_t ld_out,
+                               float* d_row_weight, int64_t rows, int32_t n_experts, int32_t k, int32_t n,
+                               int32_t trans_w, int32_t dtype, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+muon_status muon_gated_mm_grad_workspace_bytes(const void* dy, int64_t lddy, const void* w, int64_t ldw,
+                                               int64_t w_stride, int64_t rows, int32_t n_experts,
+                                               int32_t k, int32_t n, int32_t trans_w,
+                                               int32_t row_weight_grad, size_t* bytes);
+/* muon_grouped_mm_sum: y = x1 W1 + x2 W2 per expert, summed before the one rounding: with dgate and dup
+ * and the two projections (the other trans_w) the gradient with respect to the block's input.  Both
+ * products have the same k; out_dtype: dtype or MUON_DTYPE_F32. */
+muon_status muon_grouped_mm_sum(const void* x1, int64_t ldx1, const void* w1, int64_t ldw1,
+                                int64_t w1_stride, const void* x2, int64_t ldx2, const void* w2,
+                                int64_t ldw2, int64_t w2_stride, const int64_t* row_offsets, void* y,
+                                int64_t ldy, int64_t rows, int32_t n_experts, int32_t k, int32_t n,
+                                int32_t trans_w, int32_t dtype, int32_t out_dtype, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+muon_status muon_grouped_mm_sum_workspace_bytes(const void* x1, int64_t ldx1, const void* w1, int64_t ldw1,
+                                                int64_t w1_stride, const void* x2, int64_t ldx2,
+                                                const void* w2, int64_t ldw2, int64_t w2_stride,
+                                                int64_t rows, int32_t n_experts, int32_t k, int32_t n,
+                                                int32_t trans_w, size_t* bytes);
+
 /* ---------------------------------------------------------------- status
  * Synchronises `stream`, then reports a device-side wait timeout recorded since the last
  * check (MUON_ERR_TIMEOUT, and clears it), a failed range check of a debug build

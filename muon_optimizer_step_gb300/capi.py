@@ -110,6 +110,20 @@ SIGNATURES = [
     ("muon_layer_norm_grad", _I32, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _I64, _I32,
                                     _I32, _I32, _P, _SZ, _P]),
     ("muon_layer_norm_grad_workspace_bytes", _I32, [_I64, _I32, ctypes.POINTER(_SZ)]),
+    ("muon_gated_mm", _I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _I64,
+                             _P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P]),
+    ("muon_gated_mm_workspace_bytes", _I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32,
+                                             _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("muon_gated_mm_grad", _I32, [_P, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _P, _I64, _P,
+                                  _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _SZ,
+                                  _P]),
+    ("muon_gated_mm_grad_workspace_bytes", _I32, [_P, _I64, _P, _I64, _I64, _I64, _I32, _I32, _I32,
+                                                  _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("muon_grouped_mm_sum", _I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I64,
+                                   _I64, _I32, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P]),
+    ("muon_grouped_mm_sum_workspace_bytes", _I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64,
+                                                   _I64, _I64, _I32, _I32, _I32, _I32,
+                                                   ctypes.POINTER(_SZ)]),
 ]
 
 
@@ -724,6 +738,141 @@ def muon_layer_norm_grad(dy, x, weight, mean, rstd, dx, dweight, dbias, accumula
                                   _stream_of(stream, device))
     if st != MUON_OK:
         raise MuonError(st, "muon_layer_norm_grad")
+
+
+def _product_offsets(offsets, n_experts, device):
+    """The row offsets' pointer; None: one expert owns every row."""
+    if offsets is None:
+        if n_experts != 1:
+            raise ValueError(f"offsets: needed for {n_experts} experts")
+        return None
+    return _offsets(offsets, n_experts, device)
+
+
+def _same_shape(w, other, name):
+    if other.shape != w.shape:
+        raise ValueError(f"{name}: shape {tuple(other.shape)}, expected {tuple(w.shape)}")
+
+
+def _optional_matrix(t, name, device, shape, dtype):
+    """(pointer, pitch) of a matrix of the call's type, or of None."""
+    if t is None:
+        return None, 0
+    p, ld, kind = _matrix(t, name, device, shape)
+    if kind != dtype:
+        raise ValueError(f"{name}: must have the type of the call's other matrices")
+    return p, ld
+
+
+def _need(call, *args):
+    """The bytes of workspace that a query reports."""
+    need = _SZ()
+    _check(getattr(lib, call)(*args, ctypes.byref(need)), call)
+    return need.value
+
+
+def muon_gated_mm(x, w_gate, w_up, offsets, out, gate=None, up=None, row_weight=None, trans_w=False,
+                  workspace=None, stream=None):
+    """out[r] = row_weight[r] * silu(x[r] @ w_gate[e]) * (x[r] @ w_up[e]) in one kernel (trans_w:
+    w.T) for the rows offsets[e]..offsets[e+1]-1 of every expert e; rows of no expert get zeros.
+
+    x (rows, k), both weights (experts, k, n) (trans_w: (experts, n, k)) and out (rows, n) are all
+    bfloat16 or all float16.  offsets: experts + 1 int64 values on the GPU, or None for one expert
+    that owns every row.  gate and up: None, or receive the two products for muon_gated_mm_grad."""
+    device = _device_of(w_gate, "w_gate")
+    wp, ldw, apart, dtype = _matrices(w_gate, "w_gate", device)
+    _same_shape(w_gate, w_up, "w_up")
+    up_p, ldw_up, up_apart, up_kind = _matrices(w_up, "w_up", device)
+    e, k, n = w_gate.shape
+    if trans_w:
+        k, n = n, k
+    rows = x.shape[0]
+    xp, ldx, xkind = _matrix(x, "x", device, (rows, k))
+    op, ldo, okind = _matrix(out, "out", device, (rows, n))
+    if not dtype == up_kind == xkind == okind or dtype == MUON_DTYPE_F32:
+        raise ValueError("x, w_gate, w_up and out must all be bfloat16 or all float16")
+    gp, ldg = _optional_matrix(gate, "gate", device, (rows, n), dtype)
+    upp, ldu = _optional_matrix(up, "up", device, (rows, n), dtype)
+    trans = 1 if trans_w else 0
+    nbytes = 0
+    if (xp | wp | up_p) & 15 or (ldx | ldw | apart | ldw_up | up_apart) & 7:
+        nbytes = _need("muon_gated_mm_workspace_bytes", xp, ldx, wp, ldw, apart, up_p, ldw_up, up_apart,
+                       rows, e, k, n, trans)
+    ws, nbytes, owner = _workspace(workspace, nbytes, WORKSPACE_ALIGN, x, stream)
+    st = lib.muon_gated_mm(xp, ldx, wp, ldw, apart, up_p, ldw_up, up_apart,
+                           _product_offsets(offsets, e, device),
+                           _row_floats(row_weight, rows, "row_weight", device), op, ldo, gp, ldg, upp,
+                           ldu, rows, e, k, n, trans, dtype, ws, nbytes, _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_gated_mm")
+
+
+def muon_gated_mm_grad(dy, w, offsets, gate, up, dgate, dup, out=None, row_weight=None,
+                       d_row_weight=None, trans_w=False, workspace=None, stream=None):
+    """Backward through a gated block's second product and its activation in one kernel: from dh =
+    dy @ w[e] (trans_w: w[e].T, which a down projection stored (inner, hidden) takes), which is never
+    stored, and the forward pass's gate and up, writes dgate and dup and, where given, out (the
+    activation, for the second product's weight gradient) and d_row_weight.
+
+    dy (rows, k), gate, up, dgate, dup and out (rows, n) and w are all bfloat16 or all float16."""
+    device = _device_of(w, "w")
+    wp, ldw, apart, dtype = _matrices(w, "w", device)
+    e, k, n = w.shape
+    if trans_w:
+        k, n = n, k
+    rows = dy.shape[0]
+    yp, ldy, ykind = _matrix(dy, "dy", device, (rows, k))
+    g, ldg, gkind = _matrix(gate, "gate", device, (rows, n))
+    u, ldu, ukind = _matrix(up, "up", device, (rows, n))
+    dg, lddg, dgkind = _matrix(dgate, "dgate", device, (rows, n))
+    du, lddu, dukind = _matrix(dup, "dup", device, (rows, n))
+    if not dtype == ykind == gkind == ukind == dgkind == dukind or dtype == MUON_DTYPE_F32:
+        raise ValueError("dy, w, gate, up, dgate and dup must all be bfloat16 or all float16")
+    op, ldo = _optional_matrix(out, "out", device, (rows, n), dtype)
+    trans = 1 if trans_w else 0
+    nbytes = 0
+    if d_row_weight is not None or (yp | wp) & 15 or (ldy | ldw | apart) & 7:
+        nbytes = _need("muon_gated_mm_grad_workspace_bytes", yp, ldy, wp, ldw, apart, rows, e, k, n,
+                       trans, 0 if d_row_weight is None else 1)
+    ws, nbytes, owner = _workspace(workspace, nbytes, WORKSPACE_ALIGN, dy, stream)
+    st = lib.muon_gated_mm_grad(yp, ldy, wp, ldw, apart, _product_offsets(offsets, e, device), g, ldg, u,
+                                ldu, _row_floats(row_weight, rows, "row_weight", device), dg, lddg, du,
+                                lddu, op, ldo, _row_floats(d_row_weight, rows, "d_row_weight", device),
+                                rows, e, k, n, trans, dtype, ws, nbytes, _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_gated_mm_grad")
+
+
+def muon_grouped_mm_sum(x1, w1, x2, w2, offsets, y, trans_w=False, workspace=None, stream=None):
+    """y[r] = x1[r] @ w1[e] + x2[r] @ w2[e] (trans_w: w.T), summed before the one rounding, for the
+    rows offsets[e]..offsets[e+1]-1 of every expert e (offsets None: one expert owns every row).
+
+    x1 and x2 (rows, k), w1 and w2 (experts, k, n) (trans_w: (experts, n, k)) are all bfloat16 or
+    all float16, y (rows, n) is of their type or float32."""
+    device = _device_of(w1, "w1")
+    p1, ldw1, apart1, dtype = _matrices(w1, "w1", device)
+    _same_shape(w1, w2, "w2")
+    p2, ldw2, apart2, kind2 = _matrices(w2, "w2", device)
+    e, k, n = w1.shape
+    if trans_w:
+        k, n = n, k
+    rows = x1.shape[0]
+    a, lda, akind = _matrix(x1, "x1", device, (rows, k))
+    b, ldb, bkind = _matrix(x2, "x2", device, (rows, k))
+    yp, ldy, out = _matrix(y, "y", device, (rows, n))
+    if not dtype == kind2 == akind == bkind or dtype == MUON_DTYPE_F32 or out not in (dtype, MUON_DTYPE_F32):
+        raise ValueError("x1, w1, x2 and w2 must all be bfloat16 or all float16, y of their type or float32")
+    trans = 1 if trans_w else 0
+    nbytes = 0
+    if (a | b | p1 | p2) & 15 or (lda | ldb | ldw1 | apart1 | ldw2 | apart2) & 7:
+        nbytes = _need("muon_grouped_mm_sum_workspace_bytes", a, lda, p1, ldw1, apart1, b, ldb, p2, ldw2,
+                       apart2, rows, e, k, n, trans)
+    ws, nbytes, owner = _workspace(workspace, nbytes, WORKSPACE_ALIGN, x1, stream)
+    st = lib.muon_grouped_mm_sum(a, lda, p1, ldw1, apart1, b, ldb, p2, ldw2, apart2,
+                                 _product_offsets(offsets, e, device), yp, ldy, rows, e, k, n, trans,
+                                 dtype, out, ws, nbytes, _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_grouped_mm_sum")
 
 
 def muon_check(stream=None):

@@ -125,6 +125,37 @@ bool grouped_wgrad_fits(const GroupedWgrad& g);
 size_t grouped_wgrad_workspace(const GroupedWgrad& g);
 cudaError_t launch_grouped_wgrad(const GroupedWgrad& g, void* workspace, int sms, cudaStream_t st);
 
+// Gated projections (see muon_gated_mm): x, w (the gate's), k and n of the products, y the result.
+struct GatedMm : GroupedMm {
+  const void* w2;             // the up projection's
+  int64_t ldw2, w2_stride;
+  void *gate, *up;            // may be null
+  int64_t ld_gate, ld_up;
+  const float* p;             // row weights, may be null
+};
+// What feeds the gated activation's gradient (see muon_gated_mm_grad): x = dy, w = w_down, y the
+// activation (may be null).
+struct GatedGrad : GroupedMm {
+  const void *gate, *up;
+  int64_t ld_gate, ld_up;
+  void *dgate, *dup;
+  int64_t ld_dgate, ld_dup;
+  const float* p;             // may be null
+  float *dp, *part;           // dp may be null; part: its sums over 32 columns
+};
+// y = x W_e + x2 W2_e.
+struct MmSum : GroupedMm {
+  const void *x2, *w2;
+  int64_t ldx2, ldw2, w2_stride;
+};
+bool gated_mm_fits(const GroupedMm& g);
+size_t gated_mm_workspace(const GatedMm& g);
+cudaError_t launch_gated_mm(const GatedMm& g, void* workspace, int sms, cudaStream_t st);
+size_t gated_grad_workspace(const GatedGrad& g);
+cudaError_t launch_gated_grad(const GatedGrad& g, void* workspace, int sms, cudaStream_t st);
+size_t mm_sum_workspace(const MmSum& g);
+cudaError_t launch_mm_sum(const MmSum& g, void* workspace, int sms, cudaStream_t st);
+
 // n = 3: g, u, a (forward); n = 5: da, g, u, dg, du (gradient).
 struct SwigluArgs {
   int n;

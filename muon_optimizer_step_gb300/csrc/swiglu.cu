@@ -16,6 +16,7 @@
 // kTpr threads share a row: a warp where there are many rows (dp then needs shuffles only), a
 // block where there are few, so that a small batch still fills the machine with loads
 // (192 x 1408: 1.9 us).
+#include "activation.cuh"
 #include "element.cuh"
 #include "kernels.h"
 
@@ -51,16 +52,6 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& r) {
     memcpy(&q, r.v, 16);
     *reinterpret_cast<uint4*>(p) = q;
   }
-}
-
-// With e = exp(-|x|), 1 / (1 + e) for x >= 0 and e / (1 + e) below: no power overflows and no
-// reciprocal is flushed to 0, as that of 1 + exp(-x) would be from x = -87.3 down.
-// kFast: what follows from it is rounded to 16 bits.
-template <typename T, bool kFast>
-__device__ __forceinline__ float sigmoid(float x) {
-  const float e = kFast ? __expf(-fabsf(x)) : expf(-fabsf(x));
-  const float r = sizeof(T) == 4 ? 1.f / (1.f + e) : __fdividef(1.f, 1.f + e);
-  return x < 0.f ? e * r : r;
 }
 
 template <typename T, int V, int kTpr>
