@@ -466,6 +466,35 @@ muon_status muon_grouped_mm_sum_workspace_bytes(const void* x1, int64_t ldx1, co
                                                 int64_t rows, int32_t n_experts, int32_t k, int32_t n,
                                                 int32_t trans_w, size_t* bytes);
 
+/* Products in 8-bit floating point (e4m3: 4 exponent and 3 fraction bits, largest value 448, no
+ * infinities) with a scale for each block of 128.  A block's scale is the smallest power of two s with
+ * max|x| / s <= 448 over its finite elements (1 where all are zero; never below 2^-126), and its values
+ * are x / s, an exact quotient, rounded to nearest.  NaN and infinite elements become NaN.
+ *
+ * muon_quantize_rows: x (rows x cols, any muon_dtype) to q (rows x cols bytes) with blocks of 128
+ * columns of a row; scale[b * ld_scale + r] (fp32) is that of columns 128 b .. of row r. */
+muon_status muon_quantize_rows(const void* x, int64_t ldx, void* q, int64_t ldq, float* scale,
+                               int64_t ld_scale, int64_t rows, int32_t cols, int32_t dtype,
+                               cudaStream_t stream);
+/* muon_quantize_weights: n (1..MUON_MAX_EXPERTS) matrices w of rows x cols to q with blocks of 128 x
+ * 128, in the same order or (transpose != 0) transposed, cols x rows.  scale: for each matrix, for each
+ * 128 rows of q's order, for each 128 columns of it, one behind the other.  q's matrices must not
+ * overlap. */
+muon_status muon_quantize_weights(const void* w, int64_t ldw, int64_t w_stride, void* q, int64_t ldq,
+                                  int64_t q_stride, float* scale, int32_t n, int32_t rows, int32_t cols,
+                                  int32_t transpose, int32_t dtype, cudaStream_t stream);
+/* muon_grouped_mm_fp8: y[r, :] = x[r, :] W_e^T for the rows r of every expert e (row_offsets NULL:
+ * n_experts is 1 and owns every row), x (rows x k) and w (n x k for each expert) in e4m3 with the scales
+ * of the two calls above (any finite values will do).  Each block's sum over 128 of k comes from the
+ * tensor cores in fp32 and is added, times both scales, in fp32; one rounding to out_dtype (any
+ * muon_dtype) at the store.  Rows of no expert get zeros.  x, w and all their rows must start on 16
+ * bytes (MUON_ERR_ALIGNMENT otherwise): pitches and w_stride are multiples of 16, whatever k is. */
+muon_status muon_grouped_mm_fp8(const void* x, int64_t ldx, const float* x_scale, int64_t ld_x_scale,
+                                const void* w, int64_t ldw, int64_t w_stride, const float* w_scale,
+                                const int64_t* row_offsets, void* y, int64_t ldy, int64_t rows,
+                                int32_t n_experts, int32_t k, int32_t n, int32_t out_dtype,
+                                cudaStream_t stream);
+
 /* ---------------------------------------------------------------- status
  * Synchronises `stream`, then reports a device-side wait timeout recorded since the last
  * check (MUON_ERR_TIMEOUT, and clears it), a failed range check of a debug build

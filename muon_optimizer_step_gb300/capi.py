@@ -124,6 +124,11 @@ SIGNATURES = [
     ("muon_grouped_mm_sum_workspace_bytes", _I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64,
                                                    _I64, _I64, _I32, _I32, _I32, _I32,
                                                    ctypes.POINTER(_SZ)]),
+    ("muon_quantize_rows", _I32, [_P, _I64, _P, _I64, _P, _I64, _I64, _I32, _I32, _P]),
+    ("muon_quantize_weights", _I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _I32, _I32, _I32, _I32, _I32,
+                                     _P]),
+    ("muon_grouped_mm_fp8", _I32, [_P, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _I32,
+                                   _I32, _I32, _I32, _P]),
 ]
 
 
@@ -873,6 +878,95 @@ def muon_grouped_mm_sum(x1, w1, x2, w2, offsets, y, trans_w=False, workspace=Non
                                  dtype, out, ws, nbytes, _stream_of(stream, device))
     if st != MUON_OK:
         raise MuonError(st, "muon_grouped_mm_sum")
+
+
+FP8_BLOCK = 128   # elements (of a row), or rows and columns (of a weight), that share a scale
+
+
+def _fp8_blocks(n):
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _fp8(t, name, device, dims):
+    """(pointer, strides) of an e4m3 tensor with contiguous rows; a single row's (or matrix's) stride
+    means nothing and counts as the least that works."""
+    _on(t, name, device)
+    size, step = t.shape, t.stride()
+    if t.dtype != _torch.float8_e4m3fn or len(size) != dims:
+        raise ValueError(f"{name}: must be a float8_e4m3fn tensor of {dims} dimensions")
+    if step[-1] != 1 and size[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    pitch = step[-2] if size[-2] > 1 else max(size[-1], 1)
+    if dims == 2:
+        return t.data_ptr(), pitch
+    return t.data_ptr(), pitch, step[0] if size[0] > 1 else max(size[1], 1) * pitch
+
+
+def muon_quantize_rows(x, q, scale, stream=None):
+    """x (rows, cols; any type) to q (rows, cols) in float8_e4m3fn, with scale (blocks of 128 columns,
+    rows) in float32: q * scale is x but for the rounding to e4m3."""
+    device = _device_of(x, "x")
+    xp, ldx, dtype = _matrix(x, "x", device)
+    rows, cols = x.shape
+    qp, ldq = _fp8(q, "q", device, 2)
+    if q.shape != x.shape:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected {tuple(x.shape)}")
+    sp, ld_scale, kind = _matrix(scale, "scale", device, (_fp8_blocks(cols), rows))
+    if kind != MUON_DTYPE_F32:
+        raise ValueError("scale: must be float32")
+    st = lib.muon_quantize_rows(xp, ldx, qp, ldq, sp, ld_scale, rows, cols, dtype,
+                                _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_quantize_rows")
+
+
+def muon_quantize_weights(w, q, scale, transpose=False, stream=None):
+    """w (n, rows, cols; any type) to q in float8_e4m3fn, (n, rows, cols) or with transpose (n, cols,
+    rows), with a float32 scale for each 128 x 128 block in q's order (n, blocks, blocks; contiguous)."""
+    device = _device_of(w, "w")
+    wp, ldw, apart, dtype = _matrices(w, "w", device)
+    n, rows, cols = w.shape
+    want = (n, cols, rows) if transpose else (n, rows, cols)
+    qp, ldq, q_apart = _fp8(q, "q", device, 3)
+    if q.shape != want:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected {want}")
+    _on(scale, "scale", device)
+    blocks = (n, _fp8_blocks(want[1]), _fp8_blocks(want[2]))
+    if scale.shape != blocks or not scale.is_contiguous() or _kind(scale, "scale") != MUON_DTYPE_F32:
+        raise ValueError(f"scale: must be {blocks} contiguous float32 values")
+    st = lib.muon_quantize_weights(wp, ldw, apart, qp, ldq, q_apart, scale.data_ptr(), n, rows, cols,
+                                   1 if transpose else 0, dtype, _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_quantize_weights")
+
+
+def muon_grouped_mm_fp8(x, x_scale, w, w_scale, offsets, y, stream=None):
+    """y[r] = x[r] @ w[e].T for the rows offsets[e]..offsets[e+1]-1 of every expert e (offsets None: one
+    expert owns every row), from e4m3 values and the scales of muon_quantize_rows and
+    muon_quantize_weights.
+
+    x (rows, k) and w (experts, n, k) are float8_e4m3fn with rows that start on 16 bytes, y (rows, n) is
+    bfloat16, float16 or float32."""
+    device = _device_of(w, "w")
+    wp, ldw, apart = _fp8(w, "w", device, 3)
+    e, n, k = w.shape
+    rows = x.shape[0]
+    xp, ldx = _fp8(x, "x", device, 2)
+    if x.shape[1] != k:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected {(rows, k)}")
+    blocks = _fp8_blocks(k)
+    xs, ld_xs, xs_kind = _matrix(x_scale, "x_scale", device, (blocks, rows))
+    _on(w_scale, "w_scale", device)
+    if xs_kind != MUON_DTYPE_F32 or _kind(w_scale, "w_scale") != MUON_DTYPE_F32 \
+            or w_scale.shape != (e, _fp8_blocks(n), blocks) or not w_scale.is_contiguous():
+        raise ValueError(f"x_scale and w_scale: must be {(blocks, rows)} and contiguous "
+                         f"{(e, _fp8_blocks(n), blocks)} float32 values")
+    yp, ldy, out = _matrix(y, "y", device, (rows, n))
+    st = lib.muon_grouped_mm_fp8(xp, ldx, xs, ld_xs, wp, ldw, apart, w_scale.data_ptr(),
+                                 _product_offsets(offsets, e, device), yp, ldy, rows, e, k, n, out,
+                                 _stream_of(stream, device))
+    if st != MUON_OK:
+        raise MuonError(st, "muon_grouped_mm_fp8")
 
 
 def muon_check(stream=None):

@@ -28,7 +28,8 @@ LIB_PATH_DEBUG = os.path.join(PKG, "libmuon_debug.so")
 
 SOURCES = ["layout.cpp", "capi.cu", "stream_kernels.cu", "gemm_f32.cu", "gemm_ns.cu",
            "noalloc.cu", "expert_capi.cu", "grouped_mm.cu", "swiglu.cu", "grad_norm.cu",
-           "feed_forward_capi.cu", "layer_norm.cu", "gated_mm.cu"]
+           "feed_forward_capi.cu", "layer_norm.cu", "gated_mm.cu",
+           "quantize.cu", "fp8_mm.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -330,4 +330,87 @@ muon_status muon_grouped_mm_sum(const void* x1, int64_t ldx1, const void* w1, in
   return done(launch_mm_sum(g, workspace, d.sms, stream), "sum of two grouped products");
 }
 
+muon_status muon_quantize_rows(const void* x, int64_t ldx, void* q, int64_t ldq, float* scale,
+                               int64_t ld_scale, int64_t rows, int32_t cols, int32_t dtype,
+                               cudaStream_t stream) {
+  EXPERT_TRY(check_dtype(dtype, "dtype"));
+  EXPERT_TRY(check_rows(rows));
+  EXPERT_TRY(check_dim(cols, "cols"));
+  EXPERT_TRY(check_matrix(x, ldx, rows, cols, dtype, false, "x"));
+  EXPERT_TRY(check_pitch(ldq, cols, "ldq"));
+  EXPERT_TRY(check_pitch(ld_scale, rows, "ld_scale"));
+  if (rows > 0) {
+    EXPERT_TRY(check_ptr(q, 1, "q"));
+    EXPERT_TRY(check_ptr(scale, sizeof(float), "scale"));
+  }
+  Device d;
+  EXPERT_TRY(current_device(&d));
+  if (rows == 0) return done(cudaSuccess, "");
+  const QuantizeRows a{x, static_cast<uint8_t*>(q), scale, ldx, ldq, ld_scale, rows, cols};
+  return done(launch_quantize_rows(a, dtype, d.sms, stream), "quantization of rows");
+}
+
+muon_status muon_quantize_weights(const void* w, int64_t ldw, int64_t w_stride, void* q, int64_t ldq,
+                                  int64_t q_stride, float* scale, int32_t n, int32_t rows, int32_t cols,
+                                  int32_t transpose, int32_t dtype, cudaStream_t stream) {
+  EXPERT_TRY(check_dtype(dtype, "dtype"));
+  EXPERT_TRY(check_groups(0, n));
+  EXPERT_TRY(check_dim(rows, "rows"));
+  EXPERT_TRY(check_dim(cols, "cols"));
+  EXPERT_TRY(check_matrix(w, ldw, rows, cols, dtype, false, "w"));
+  const int64_t q_rows = transpose ? cols : rows, q_cols = transpose ? rows : cols;
+  EXPERT_TRY(check_pitch(ldq, q_cols, "ldq"));
+  if (n > 1) {
+    EXPERT_TRY(check_pitch(w_stride, 1, "w_stride"));
+    if (q_stride < q_cols || (q_stride - q_cols) / ldq < q_rows - 1 || q_stride >= (int64_t)1 << 52)
+      return fail(MUON_ERR_INVALID_ARG, "q_stride=%lld: matrices of q overlap or lie too far apart",
+                  (long long)q_stride);
+  }
+  EXPERT_TRY(check_ptr(q, 1, "q"));
+  EXPERT_TRY(check_ptr(scale, sizeof(float), "scale"));
+  Device d;
+  EXPERT_TRY(current_device(&d));
+  const QuantizeWeights a{w,        static_cast<uint8_t*>(q), scale, ldw,  w_stride, ldq,
+                          q_stride, n,                        rows,  cols, transpose ? 1 : 0, false};
+  return done(launch_quantize_weights(a, dtype, d.sms, stream), "quantization of weights");
+}
+
+muon_status muon_grouped_mm_fp8(const void* x, int64_t ldx, const float* x_scale, int64_t ld_x_scale,
+                                const void* w, int64_t ldw, int64_t w_stride, const float* w_scale,
+                                const int64_t* row_offsets, void* y, int64_t ldy, int64_t rows,
+                                int32_t n_experts, int32_t k, int32_t n, int32_t out_dtype,
+                                cudaStream_t stream) {
+  Fp8Mm g{};
+  set_product(&g, x, ldx, w, ldw, w_stride, rows, n_experts, k, n, 1, MUON_DTYPE_BF16);
+  g.offsets = row_offsets;
+  g.x_scale = x_scale;
+  g.ld_x_scale = ld_x_scale;
+  g.w_scale = w_scale;
+  g.y = y;
+  g.ldy = ldy;
+  g.out_dtype = out_dtype;
+  EXPERT_TRY(check_product(g));
+  EXPERT_TRY(check_offsets(g));
+  EXPERT_TRY(check_dtype(out_dtype, "out_dtype"));
+  EXPERT_TRY(check_pitch(ldx, k, "ldx"));
+  EXPERT_TRY(check_pitch(ldw, k, "ldw"));
+  if (n_experts > 1) EXPERT_TRY(check_pitch(w_stride, 1, "w_stride"));
+  EXPERT_TRY(check_pitch(ld_x_scale, rows, "ld_x_scale"));
+  if ((rows > 1 && ldx % 16 != 0) || (n > 1 && ldw % 16 != 0) || (n_experts > 1 && w_stride % 16 != 0))
+    return fail(MUON_ERR_ALIGNMENT, "ldx=%lld, ldw=%lld, w_stride=%lld: rows must start on 16 bytes",
+                (long long)ldx, (long long)ldw, (long long)w_stride);
+  EXPERT_TRY(check_matrix(y, ldy, rows, n, out_dtype, false, "y"));
+  if (rows > 0) {
+    EXPERT_TRY(check_ptr(x, 16, "x"));
+    EXPERT_TRY(check_ptr(w, 16, "w"));
+    EXPERT_TRY(check_ptr(x_scale, sizeof(float), "x_scale"));
+    EXPERT_TRY(check_ptr(w_scale, sizeof(float), "w_scale"));
+  }
+  Device d;
+  EXPERT_TRY(current_device(&d));
+  if (rows == 0) return done(cudaSuccess, "");
+  g.err = d.err;
+  return done(launch_fp8_mm(g, d.sms, stream), "8-bit grouped product");
+}
+
 }  // extern "C"

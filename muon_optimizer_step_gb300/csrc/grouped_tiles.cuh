@@ -131,24 +131,23 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
   return (saddr & 0x3FFFF) >> 4 | (lbo >> 4) << 16;
 }
 
-template <bool kPair>
+// kind::f16 products of 16-bit operands; kFp8: kind::f8f6f4 of 8-bit ones.
+#define MUON_MMA(group, kind)                                                                      \
+  asm volatile(                                                                                    \
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"                                                 \
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"                \
+      "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], a, b, %3, p;\n\t}" ::"r"(d),          \
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)                                     \
+      : "memory")
+template <bool kPair, bool kFp8 = false>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                     uint32_t add) {
-  if constexpr (kPair)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
-        : "memory");
+  if constexpr (kPair && kFp8) MUON_MMA("2", "f8f6f4");
+  else if constexpr (kPair) MUON_MMA("2", "f16");
+  else if constexpr (kFp8) MUON_MMA("1", "f8f6f4");
+  else MUON_MMA("1", "f16");
 }
+#undef MUON_MMA
 
 // One lane of the (whole) warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -575,13 +574,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 inline cudaError_t encode(CUtensorMap* map, const Operand& o, int32_t dtype, bool batched, uint32_t box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
   if (fn == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t size = dtype == kF32 ? 4 : 2;
+  const cuuint64_t size = dtype == kF32 ? 4 : dtype == kE4m3 ? 1 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.batch};
   // (The stride of a dimension of length 1 means nothing, but has to be a valid one.)
   const cuuint64_t strides[2] = {(cuuint64_t)o.ld * size,
                                  (cuuint64_t)(o.batch == 1 ? o.ld : o.stride) * size};
   const cuuint32_t box[3] = {(cuuint32_t)(128 / size), box_rows, 1}, unit[3] = {1, 1, 1};
   const CUresult r = fn(map, dtype == kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                             : dtype == kE4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                              : dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         batched ? 3 : 2, const_cast<void*>(o.ptr), dims, strides, box, unit,

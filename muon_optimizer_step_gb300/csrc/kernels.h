@@ -156,6 +156,33 @@ cudaError_t launch_gated_grad(const GatedGrad& g, void* workspace, int sms, cuda
 size_t mm_sum_workspace(const MmSum& g);
 cudaError_t launch_mm_sum(const MmSum& g, void* workspace, int sms, cudaStream_t st);
 
+// Quantization to e4m3 with a scale per block of 128 (see muon_quantize_rows, muon_quantize_weights).
+struct QuantizeRows {
+  const void* x;
+  uint8_t* q;
+  float* scale;
+  int64_t ldx, ldq, ld_scale, rows;
+  int32_t cols;
+};
+struct QuantizeWeights {
+  const void* w;
+  uint8_t* q;
+  float* scale;
+  int64_t ldw, w_stride, ldq, q_stride;
+  int32_t n, rows, cols, transpose;
+  bool wide_q;                // set by the launch: q's rows start on 8 bytes
+};
+cudaError_t launch_quantize_rows(const QuantizeRows& a, int dtype, int sms, cudaStream_t st);
+cudaError_t launch_quantize_weights(const QuantizeWeights& a, int dtype, int sms, cudaStream_t st);
+
+// The product of 8-bit operands (see muon_grouped_mm_fp8): x and w with their scales.
+constexpr int kE4m3 = 3;      // an operand type of tensor maps, beside the muon_dtype values
+struct Fp8Mm : GroupedMm {
+  const float *x_scale, *w_scale;
+  int64_t ld_x_scale;
+};
+cudaError_t launch_fp8_mm(const Fp8Mm& g, int sms, cudaStream_t st);
+
 // n = 3: g, u, a (forward); n = 5: da, g, u, dg, du (gradient).
 struct SwigluArgs {
   int n;
