@@ -22,13 +22,24 @@ namespace {
 constexpr int kBK8 = 128;   // elements of a k-block: 128 bytes
 constexpr int kSlots = 8;   // of scales
 constexpr int kAhead = 6;   // k-blocks that scales are asked for ahead
+constexpr int kWarps8 = 16;              // of the epilogue
+constexpr int kThreads8 = 128 + 32 * kWarps8;
+constexpr int kStaging8 = 1024;          // bytes of each epilogue warp: 8 rows of its 32 columns
 
 struct Fp8Params {
   CUtensorMap x, w;  // (k, rows): boxes of 128 x kBoxRows; (k, columns of y, expert): 128 x 128
   Fp8Mm g;
 };
 
-// Pair and Wide as for 16-bit operands; narrow tiles with a k-block per stage.
+// Tile variants as for 16-bit operands (see grouped_tiles.cuh), with a k-block per stage.
+struct Pair8 {
+  static constexpr bool kPair = true, kSplit = false;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 5, kSub = 1;
+};
+struct Wide8 {
+  static constexpr bool kPair = false, kSplit = false;
+  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
+};
 struct Narrow8 {
   static constexpr bool kPair = false, kSplit = false;
   static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 6, kSub = 1;
@@ -48,8 +59,28 @@ __device__ __forceinline__ void copy_4(void* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
+// v times the scales s, two at a time, added to the sums.
+__device__ __forceinline__ void add_scaled(uint64_t& sum, uint32_t v0, uint32_t v1, uint64_t s) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+      : "+l"(sum)
+      : "r"(v0), "r"(v1), "l"(s));
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// sum += 16 accumulator columns in v, times their scales from s on (16-byte aligned).
+__device__ __forceinline__ void add_block(uint64_t (&sum)[16], int at, const uint32_t (&v)[16], const float* s) {
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    uint64_t x, y;
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(smem_u32(s + k)));
+    add_scaled(sum[at + k / 2], v[k], v[k + 1], x);
+    add_scaled(sum[at + k / 2 + 1], v[k + 2], v[k + 3], y);
+  }
+}
+
 template <typename V, typename O>
-__global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_constant__ Fp8Params p) {
+__global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_constant__ Fp8Params p) {
   using S = Shape<V>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
@@ -67,9 +98,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
   if (threadIdx.x == 0)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sc.full[s], 1);
-      mbar_init(&sc.empty[s], kEpiWarps);
+      mbar_init(&sc.empty[s], kWarps8);
     }
-  setup<V::kPair>(c, warp);
+  setup<V::kPair, kWarps8>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kMaxN, lane, first);
   __syncthreads();
@@ -190,39 +221,34 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     if (ok)
       for (int64_t u = use < kAhead ? 0 : use - kAhead; u < use; ++u) ready(u);
   } else if (warp >= 4) {
-    const int q = warp & 3, half = (warp - 4) >> 2;  // a quarter of the lanes, every second block
+    // A quarter of the lanes, and every fourth block of 32 columns.
+    const int q = warp & 3, group = (warp - 4) >> 2;
+    constexpr int kBlocks8 = (V::kMaxN + 127) / 128;
     int use = 0;
     bool ok = true;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kBM>(t, f_tiles, g.n_experts, off, first);
       const int f = m.f0 + kBM * (int)rank + 32 * q;
-      float sum[S::kBlocks][32];
+      uint64_t sum[kBlocks8][16];  // pairs
 #pragma unroll
-      for (int i = 0; i < S::kBlocks; ++i)
+      for (int i = 0; i < kBlocks8; ++i)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) sum[i][k] = 0.f;
+        for (int k = 0; k < 16; ++k) sum[i][k] = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++use) {
         const int s = use % kSlots;
         ok = wait_warp(&sc.full[s], (uint32_t)(use / kSlots) & 1u, g.err, &c.abort) && wait_acc(c, use, g.err);
         if (!ok) break;
+        const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)((use & 1) * kAccCols + 32 * group);
+        const float* scales = &sc.slot[s][32 * group];
 #pragma unroll
-        for (int i = 0; i < S::kBlocks; ++i) {
-          const int col = (2 * i + half) * 32;
-          if (col >= m.n) continue;
-          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)((use & 1) * kAccCols + col);
+        for (int i = 0; i < kBlocks8; ++i) {
+          if ((4 * i + group) * 32 >= m.n) continue;
 #pragma unroll
           for (int h = 0; h < 32; h += 16) {
             uint32_t v[16];
-            tmem_ld_32x32b_x16(at + h, v);
+            tmem_ld_32x32b_x16(at + 128 * i + h, v);
             tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(&sc.slot[s][col + h + k]);
-              sum[i][h + k] = fmaf(__uint_as_float(v[k]), x.x, sum[i][h + k]);
-              sum[i][h + k + 1] = fmaf(__uint_as_float(v[k + 1]), x.y, sum[i][h + k + 1]);
-              sum[i][h + k + 2] = fmaf(__uint_as_float(v[k + 2]), x.z, sum[i][h + k + 2]);
-              sum[i][h + k + 3] = fmaf(__uint_as_float(v[k + 3]), x.w, sum[i][h + k + 3]);
-            }
+            add_block(sum[i], h / 2, v, scales + 128 * i + h);
           }
         }
         release_acc<V::kPair>(c, use & 1, rank, lane);
@@ -231,26 +257,30 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
       if (!ok) break;
       if constexpr (V::kSplit) {
         // The operand stages are free: this tile's MMAs were the last.
-        if (half * 32 < m.n)
+        if (group * 32 < m.n)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            reinterpret_cast<float*>(smem)[(q * V::kMaxN + half * 32 + k) * 32 + lane] = sum[0][k];
+            reinterpret_cast<float*>(smem)[(q * V::kMaxN + group * 32 + k) * 32 + lane] =
+                k & 1 ? high(sum[0][k / 2]) : low(sum[0][k / 2]);
       } else {
-#pragma unroll
-        for (int i = 0; i < S::kBlocks; ++i)
-          if ((2 * i + half) * 32 < m.n) mm_store<O>(g, m, 2 * i + half, f, lane, sum[i]);
+        const int col = f + lane % 4 * 8, inside = g.n - col;
+        O* y = static_cast<O*>(g.y) + (int64_t)m.row * g.ldy + col;
+        by_rows<kBlocks8, 8, 4>(
+            reinterpret_cast<float*>(smem + V::kStages * S::kStage + (warp - 4) * kStaging8), lane, m.rows, group,
+            [&](int i, int k) { return k & 1 ? high(sum[i][k / 2]) : low(sum[i][k / 2]); },
+            [&](int r, const float (&v)[8]) { store_8(y + r * g.ldy, inside, v); });
       }
     }
     // Rows of no expert.
     const int64_t head = off[0], none = head + g.rows - off[g.n_experts];
     for (int64_t z = blockIdx.x; z < none; z += gridDim.x)
-      Store<O>::zero_row(p, z < head ? z : off[g.n_experts] + z - head, (int)threadIdx.x - 128);
+      Store<O>::template zero_row<kWarps8>(p, z < head ? z : off[g.n_experts] + z - head, (int)threadIdx.x - 128);
   }
   if constexpr (V::kSplit) {
     __syncwarp();
     cluster_sync();
     if (warp >= 4 && unit < tiles)
-      Store<O>::template join<V>(p, mm_tile<V, kBM>(unit, f_tiles, g.n_experts, off, first), part_k, smem);
+      Store<O>::template join<V, kWarps8>(p, mm_tile<V, kBM>(unit, f_tiles, g.n_experts, off, first), part_k, smem);
     __syncwarp();
   }
   teardown<V>(c, warp);
@@ -260,14 +290,15 @@ template <typename V, typename O>
 cudaError_t launch_as(const Fp8Params& p, int parts, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   return launch(fp8_mm_kernel<V, O>, p, mm_tiles<V>(p.g), Shape<V>::kCtas * parts, sms,
-                V::kStages * Shape<V>::kStage + 1024, &ready, st);
+                V::kStages * Shape<V>::kStage + (V::kSplit ? 0 : kWarps8 * kStaging8) + 1024, &ready, st,
+                kThreads8);
 }
 
 template <typename O>
 cudaError_t launch_type(const Fp8Params& p, const MmChoice& c, int sms, cudaStream_t st) {
   return c.parts > 1 ? launch_as<Split8, O>(p, c.parts, sms, st)
          : c.narrow  ? launch_as<Narrow8, O>(p, 1, sms, st)
-         : c.pair    ? launch_as<Pair, O>(p, 1, sms, st) : launch_as<Wide, O>(p, 1, sms, st);
+         : c.pair    ? launch_as<Pair8, O>(p, 1, sms, st) : launch_as<Wide8, O>(p, 1, sms, st);
 }
 
 }  // namespace
@@ -283,7 +314,7 @@ cudaError_t launch_fp8_mm(const Fp8Mm& g, int sms, cudaStream_t st) {
   while (c.parts < kMostParts && mm_tiles<Split8>(g) * c.parts * 2 <= sms && g.k >= 4 * kBK8 * c.parts * 2)
     c.parts *= 2;
   c.narrow = g.rows <= Narrow8::kMaxN * (int64_t)g.n_experts || mm_tiles<Narrow8>(g) <= sms;
-  c.pair = !c.narrow && g.n > kBM && mm_tiles<Pair>(g) >= sms;
+  c.pair = !c.narrow && g.n > kBM && mm_tiles<Pair8>(g) >= sms;
   cudaError_t e = encode(&p.x, x, kE4m3, false, c.box_rows());
   if (e == cudaSuccess) e = encode(&p.w, w, kE4m3, true, kBM);
   if (e != cudaSuccess) return e;

@@ -9,8 +9,8 @@
 //
 // gated: a tile's 128 accumulator lanes are 64 columns of g and the same 64 columns of u, so a k-block
 // brings as many bytes into an SM as a plain product's of the same work.  The epilogue warp that holds 32
-// columns of g and the one that holds them of u exchange halves of their rows through shared memory;
-// each then has g and u of 16 of 32 rows.  g and u go to memory only where the caller keeps them.
+// columns of g and the one that holds them of u put 16 rows at a time into shared memory; each then takes
+// g and u of 8 of them.  g and u go to memory only where the caller keeps them.
 //
 // grad: dh stays in the accumulators.  The epilogue reads g and u of its tile (asked into L2 when the
 // tile begins) and writes three results.  dp_r is summed over 32 columns in a warp; a second kernel adds
@@ -25,7 +25,7 @@ namespace muon {
 namespace {
 
 // The two warps that hold the same 32 columns of g and of u.
-__device__ __forceinline__ int gate_pair(int q, int half) { return (q & 1) + 2 * half; }
+__device__ __forceinline__ int gate_pair(int q, int group) { return (q & 1) + 2 * group; }
 __device__ __forceinline__ void sync_pair(int pair) {
   asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
 }
@@ -39,9 +39,10 @@ template <typename T>
 struct Gated {
   using Params = GatedParams;
   static constexpr bool kGated = true;
-  static constexpr int kCols = 64, kPasses = 1;
+  static constexpr int kCols = 64, kPasses = 1, kWarps = 16;
+  static constexpr bool kFromTmem = true;
   static constexpr int kSlot = 16 * 32;                  // floats: 16 rows of a warp's 32 columns
-  static constexpr int kStaging = 4 * 2 * kSlot * 4;     // two slots for each pair of warps
+  static constexpr int kStaging = kWarps * kSlot * 4;
   static __device__ __forceinline__ const CUtensorMap* x_map(const Params& p, bool) { return &p.x; }
   static __device__ __forceinline__ const CUtensorMap* w_map(const Params& p, bool second) {
     return second ? &p.w2 : &p.w;
@@ -51,13 +52,13 @@ struct Gated {
   static __device__ __forceinline__ void ahead(const Params&, const MmTile&, int, int, int, int) {}
 
   // Both warps of a pair give up, or neither: one that finished alone would wait for ever.
-  static __device__ __forceinline__ bool agree(int q, int half, bool ok) {
+  static __device__ __forceinline__ bool agree(int q, int group, bool ok) {
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
         "barrier.cta.red.and.pred b, %2, 64, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
         : "=r"(all)
-        : "r"((uint32_t)ok), "r"(gate_pair(q, half) + 1)
+        : "r"((uint32_t)ok), "r"(gate_pair(q, group) + 1)
         : "memory");
     return all != 0;
   }
@@ -66,38 +67,31 @@ struct Gated {
     return g * sigmoid<T, true>(g) * u * w;
   }
 
-  template <typename V>
-  static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int half,
-                                                int lane, const float (&sum)[Shape<V>::kBlocks][32],
-                                                uint8_t* staging) {
+  template <typename V, int kBlocks>
+  static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int group,
+                                                int lane, uint32_t tmem, uint8_t* staging) {
     const GatedMm& o = p.g;
-    const int pair = gate_pair(q, half), col = f + 32 * (q & 1) + lane;
-    const bool up = q >= 2;  // has u, and finishes rows 16 .. 31 of each 32
-    float* slot = reinterpret_cast<float*>(staging) + pair * 2 * kSlot + lane;
-#pragma unroll
-    for (int i = 0; i < Shape<V>::kBlocks; ++i) {
-      if ((2 * i + half) * 32 >= m.n) continue;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) slot[(up ? 0 : kSlot) + 32 * k] = sum[i][up ? k : 16 + k];
+    const int pair = gate_pair(q, group), mine = q >> 1;  // 0: has g; 1: has u
+    float* slots = reinterpret_cast<float*>(staging) + pair * 2 * kSlot;
+    const int col = f + 32 * (q & 1) + lane % 4 * 8, line = 8 * mine + lane / 4;
+#pragma unroll 1
+    for (int c = 0; c < kBlocks * 2; ++c) {
+      const int r0 = chunk_row<16, kWarps / 4>(c, group);
+      if (r0 >= m.rows) break;
+      put_tmem(slots + mine * kSlot, lane, tmem + r0);
       sync_pair(pair);
-      const int r0 = (2 * i + half) * 32 + (up ? 16 : 0), left = m.rows - r0;
-      const float weight = o.p != nullptr && lane < left && lane < 16 ? o.p[m.row + r0 + lane] : 1.f;
-      const int64_t row = (int64_t)m.row + r0;
-      T* out = static_cast<T*>(o.y) + row * o.ldy + col;
-      T* gate = static_cast<T*>(o.gate) + row * o.ld_gate + col;
-      T* upper = static_cast<T*>(o.up) + row * o.ld_up + col;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float other = slot[(up ? kSlot : 0) + 32 * k];
-        const float g = up ? other : sum[i][k], u = up ? sum[i][16 + k] : other;
-        const float w = __shfl_sync(0xffffffffu, weight, k);
-        if (k < left && col < o.n) {
-          put(out + k * o.ldy, value(g, u, w));
-          if (o.gate != nullptr) put(gate + k * o.ld_gate, g);
-          if (o.up != nullptr) put(upper + k * o.ld_up, u);
-        }
-      }
+      float g[8], u[8], v[8];
+      get_line(slots, lane, line, g);
+      get_line(slots + kSlot, lane, line, u);
       sync_pair(pair);  // the slots are read
+      if (r0 + line >= m.rows) continue;
+      const int64_t row = (int64_t)m.row + r0 + line;
+      const float w = o.p != nullptr ? o.p[row] : 1.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = value(g[k], u[k], w);
+      store_8(static_cast<T*>(o.y) + row * o.ldy + col, o.n - col, v);
+      if (o.gate != nullptr) store_8(static_cast<T*>(o.gate) + row * o.ld_gate + col, o.n - col, g);
+      if (o.up != nullptr) store_8(static_cast<T*>(o.up) + row * o.ld_up + col, o.n - col, u);
     }
   }
 
@@ -105,8 +99,8 @@ struct Gated {
   static __device__ __forceinline__ void join(const Params& p, const MmTile& m, const Part& part,
                                               uint8_t* smem) {
     const GatedMm& o = p.g;
-    for (int i = threadIdx.x - 128 + part.index * kEpiWarps * 32; i < m.rows * 8;
-         i += part.parts * kEpiWarps * 32) {
+    for (int i = threadIdx.x - 128 + part.index * kWarps * 32; i < m.rows * 8;
+         i += part.parts * kWarps * 32) {
       const int r = i / 8, col = i % 8 * 8, f = m.f0 + col;
       float g[8], u[8], v[8];
       join_parts<V>(smem, part.parts, r, col, g);
@@ -123,7 +117,7 @@ struct Gated {
 
   static __device__ __forceinline__ void zero_row(const Params& p, int64_t row, int thread) {
     const GatedMm& o = p.g;
-    for (int64_t f = thread; f < o.n; f += kEpiWarps * 32) {
+    for (int64_t f = thread; f < o.n; f += kWarps * 32) {
       put(static_cast<T*>(o.y) + row * o.ldy + f, 0.f);
       if (o.gate != nullptr) put(static_cast<T*>(o.gate) + row * o.ld_gate + f, 0.f);
       if (o.up != nullptr) put(static_cast<T*>(o.up) + row * o.ld_up + f, 0.f);
@@ -134,13 +128,17 @@ struct Gated {
 struct GradParams {
   CUtensorMap x, w;  // as MmParams
   GatedGrad g;
+  bool wide;         // every row of gate and up starts on 16 bytes
 };
 
 template <typename T>
 struct Grad {
   using Params = GradParams;
   static constexpr bool kGated = false;
-  static constexpr int kCols = kBM, kPasses = 1, kStaging = 0;
+  static constexpr int kCols = kBM, kPasses = 1, kWarps = 16;
+  static constexpr bool kFromTmem = true;
+  static constexpr int kSlot = 16 * 32;                 // floats: 16 rows of a warp's 32 columns
+  static constexpr int kStaging = kWarps * kSlot * 4;
   static __device__ __forceinline__ const CUtensorMap* x_map(const Params& p, bool) { return &p.x; }
   static __device__ __forceinline__ const CUtensorMap* w_map(const Params& p, bool) { return &p.w; }
   // dp, an fp32 result, is made of whole sums.
@@ -149,11 +147,11 @@ struct Grad {
 
   // Asks for the tile's g and u: a row per lane, the lines of its columns.
   template <typename V>
-  static __device__ __forceinline__ void ahead(const Params& p, const MmTile& m, int f, int q, int half,
+  static __device__ __forceinline__ void ahead(const Params& p, const MmTile& m, int f, int q, int group,
                                                int lane) {
     const GatedGrad& o = p.g;
-    const int r = 32 * (q + 4 * half) + lane, cols = min(kBM, o.n - f);
-    if (r >= m.rows || cols <= 0) return;
+    const int r = 16 * (q + 4 * group) + lane % 16, cols = min(kBM, o.n - f);
+    if (r >= m.rows || cols <= 0 || lane >= 16) return;
     const int64_t row = (int64_t)m.row + r;
     const char* g = reinterpret_cast<const char*>(static_cast<const T*>(o.gate) + row * o.ld_gate + f);
     const char* u = reinterpret_cast<const char*>(static_cast<const T*>(o.up) + row * o.ld_up + f);
@@ -165,75 +163,77 @@ struct Grad {
     }
   }
 
-  // From dh, g, u and the row's weight: dgate, dup and the activation; returns dp's term.
-  static __device__ __forceinline__ float values(float dh, float g, float u, float w, bool exact,
-                                                 float* dgate, float* dup, float* out) {
-    const float s = exact ? sigmoid<T, false>(g) : sigmoid<T, true>(g), silu = g * s;
-    *dup = dh * w * silu;
-    *dgate = dh * w * u * (s * (1.f + g * (1.f - s)));
-    *out = silu * u * w;
-    return dh * silu * u;
+  // From dh, g, u and the row's weight: dgate, dup and the activation; returns dp's term.  silu'(g) = s +
+  // silu(g) (1 - s), with s and 1 - s both from exp(-|g|): neither overflows nor cancels.
+  static __device__ __forceinline__ float values(float dh, float g, float u, float w, float* dgate,
+                                                 float* dup, float* out) {
+    const float e = __expf(-fabsf(g)), r = __fdividef(1.f, 1.f + e), er = e * r;
+    const float s = g < 0.f ? er : r, silu = g * s, slope = fmaf(silu, g < 0.f ? r : er, s);
+    const float d = dh * w, t = silu * u;
+    *dup = d * silu;
+    *dgate = d * (u * slope);
+    *out = t * w;
+    return dh * t;
   }
 
-  template <typename V>
-  static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int half,
-                                                int lane, const float (&sum)[Shape<V>::kBlocks][32],
-                                                uint8_t*) {
+  // Eight values of a row from base + at on, `left` of them inside it, as they are stored; wide: on 16
+  // bytes.  (Both ways end in the same words: nothing waits for the load here.)
+  static __device__ __forceinline__ uint4 load_row(const void* base, int64_t at, int left, bool wide) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if (wide && left >= 8) return *reinterpret_cast<const uint4*>(p);
+    uint32_t e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = k < left ? p[k] : 0;
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
+
+  template <typename V, int kBlocks>
+  static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int group,
+                                                int lane, uint32_t tmem, uint8_t* staging) {
     const GatedGrad& o = p.g;
-    const int col = f + 32 * q + lane;
     if (f + 32 * q >= o.n) return;
-    const bool in = col < o.n;
+    float* stage = reinterpret_cast<float*>(staging) + (q + 4 * group) * kSlot;
+    const int col = f + 32 * q + lane % 4 * 8, inside = o.n - col;
+#pragma unroll 1
+    for (int c = 0; c < kBlocks * 2; ++c) {
+      const int r0 = chunk_row<16, kWarps / 4>(c, group);
+      if (r0 >= m.rows) break;
+      uint4 g[2], u[2];
+      float w[2];
 #pragma unroll
-    for (int i = 0; i < Shape<V>::kBlocks; ++i) {
-      if ((2 * i + half) * 32 >= m.n) continue;
+      for (int j = 0; j < 2; ++j) {
+        const int r = r0 + 8 * j + lane / 4, left = r < m.rows ? inside : 0;
+        const int64_t row = (int64_t)m.row + r;
+        g[j] = load_row(o.gate, row * o.ld_gate + col, left, p.wide);
+        u[j] = load_row(o.up, row * o.ld_up + col, left, p.wide);
+        w[j] = o.p != nullptr && left > 0 ? o.p[row] : 1.f;
+      }
+      __syncwarp();
+      put_tmem(stage, lane, tmem + r0);
+      __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 32; h += 16) {
-        const int r0 = (2 * i + half) * 32 + h, left = m.rows - r0;
-        if (left <= 0) continue;
-        const int64_t row = (int64_t)m.row + r0;
-        const float weight = o.p != nullptr && lane < left && lane < 16 ? o.p[row + lane] : 1.f;
-        const T* gate = static_cast<const T*>(o.gate) + row * o.ld_gate + col;
-        const T* up = static_cast<const T*>(o.up) + row * o.ld_up + col;
-        T g[16], u[16];
+      for (int j = 0; j < 2; ++j) {
+        const int line = 8 * j + lane / 4, r = r0 + line, left = r < m.rows ? inside : 0;
+        const int64_t row = (int64_t)m.row + r;
+        const uint32_t gw[4] = {g[j].x, g[j].y, g[j].z, g[j].w}, uw[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+        float dh[8], dg[8], du[8], out[8], term = 0.f;
+        get_line(stage, lane, line, dh);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          put(&g[k], 0.f);
-          put(&u[k], 0.f);
-          if (k < left && in) {
-            g[k] = gate[k * o.ld_gate];
-            u[k] = up[k * o.ld_up];
-          }
+        for (int k = 0; k < 8; k += 2) {
+          const float2 a = unpack_2<T>(gw[k / 2]), b = unpack_2<T>(uw[k / 2]);
+          const float t0 = values(dh[k], a.x, b.x, w[j], &dg[k], &du[k], &out[k]);
+          const float t1 = values(dh[k + 1], a.y, b.y, w[j], &dg[k + 1], &du[k + 1], &out[k + 1]);
+          if (k < left) term += t0;
+          if (k + 1 < left) term += t1;
         }
-        T* dgate = static_cast<T*>(o.dgate) + row * o.ld_dgate + col;
-        T* dup = static_cast<T*>(o.dup) + row * o.ld_dup + col;
-        T* out = static_cast<T*>(o.y) + row * o.ldy + col;
-        float term[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float w = __shfl_sync(0xffffffffu, weight, k);
-          float dg, du, a;
-          term[k] = values(sum[i][h + k], cvt(g[k]), cvt(u[k]), w, o.dp != nullptr, &dg, &du, &a);
-          if (k < left && in) {
-            put(dgate + k * o.ld_dgate, dg);
-            put(dup + k * o.ld_dup, du);
-            if (o.y != nullptr) put(out + k * o.ldy, a);
-          } else {
-            term[k] = 0.f;
-          }
-        }
+        store_8(static_cast<T*>(o.dgate) + row * o.ld_dgate + col, left, dg);
+        store_8(static_cast<T*>(o.dup) + row * o.ld_dup + col, left, du);
+        if (o.y != nullptr) store_8(static_cast<T*>(o.y) + row * o.ldy + col, left, out);
         if (o.dp != nullptr) {
-          // 16 sums over the warp at once: each step halves the rows a lane still holds.
-#pragma unroll
-          for (int step = 16, n = 8; n > 0; step >>= 1, n >>= 1)
-#pragma unroll
-            for (int k = 0; k < n; ++k) {
-              const bool hi = (lane & step) != 0;
-              const float send = hi ? term[k] : term[k + n], keep = hi ? term[k + n] : term[k];
-              term[k] = keep + __shfl_xor_sync(0xffffffffu, send, step);
-            }
-          term[0] += __shfl_xor_sync(0xffffffffu, term[0], 1);
-          if ((lane & 1) == 0 && lane / 2 < left)
-            o.part[(int64_t)((f + 32 * q) / 32) * o.rows + row + lane / 2] = term[0];
+          // Four neighbouring lanes have the row's 32 columns.
+          term += __shfl_xor_sync(0xffffffffu, term, 1);
+          term += __shfl_xor_sync(0xffffffffu, term, 2);
+          if (lane % 4 == 0 && left > 0) o.part[(int64_t)((f + 32 * q) / 32) * o.rows + row] = term;
         }
       }
     }
@@ -243,8 +243,8 @@ struct Grad {
   static __device__ __forceinline__ void join(const Params& p, const MmTile& m, const Part& part,
                                               uint8_t* smem) {
     const GatedGrad& o = p.g;
-    for (int i = threadIdx.x - 128 + part.index * kEpiWarps * 32; i < m.rows * 16;
-         i += part.parts * kEpiWarps * 32) {
+    for (int i = threadIdx.x - 128 + part.index * kWarps * 32; i < m.rows * 16;
+         i += part.parts * kWarps * 32) {
       const int r = i / 16, col = i % 16 * 8, f = m.f0 + col, left = o.n - f;
       float dh[8], dg[8], du[8], out[8], term = 0.f;
       join_parts<V>(smem, part.parts, r, col, dh);
@@ -255,7 +255,7 @@ struct Grad {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float g = k < left ? cvt(gate[k]) : 0.f, u = k < left ? cvt(up[k]) : 0.f;
-        const float t = values(dh[k], g, u, w, o.dp != nullptr, &dg[k], &du[k], &out[k]);
+        const float t = values(dh[k], g, u, w, &dg[k], &du[k], &out[k]);
         if (k < left) term += t;
       }
       store_8(static_cast<T*>(o.dgate) + row * o.ld_dgate + f, left, dg);
@@ -273,7 +273,7 @@ struct Grad {
 
   static __device__ __forceinline__ void zero_row(const Params& p, int64_t row, int thread) {
     const GatedGrad& o = p.g;
-    for (int64_t f = thread; f < o.n; f += kEpiWarps * 32) {
+    for (int64_t f = thread; f < o.n; f += kWarps * 32) {
       put(static_cast<T*>(o.dgate) + row * o.ld_dgate + f, 0.f);
       put(static_cast<T*>(o.dup) + row * o.ld_dup + f, 0.f);
       if (o.y != nullptr) put(static_cast<T*>(o.y) + row * o.ldy + f, 0.f);
@@ -307,6 +307,18 @@ struct Sum : Store<O> {
   }
   static __device__ __forceinline__ const CUtensorMap* w_map(const Params& p, bool second) {
     return second ? &p.w2 : &p.w;
+  }
+  static constexpr int kSlot = 16 * 32, kStaging = kEpiWarps * kSlot * 4;
+  template <typename V>
+  static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int half,
+                                                int lane, const float (&sum)[Shape<V>::kBlocks][32],
+                                                uint8_t* staging) {
+    const int col = f + 32 * q + lane % 4 * 8, inside = p.g.n - col;
+    O* y = static_cast<O*>(p.g.y) + (int64_t)m.row * p.g.ldy + col;
+    by_rows<Shape<V>::kBlocks, 16, 2>(
+        reinterpret_cast<float*>(staging) + (q + 4 * half) * kSlot, lane, m.rows, half,
+        [&](int i, int k) { return sum[i][k]; },
+        [&](int r, const float (&v)[8]) { store_8(y + r * p.g.ldy, inside, v); });
   }
 };
 
@@ -364,6 +376,8 @@ cudaError_t launch_gated_grad(const GatedGrad& g, void* workspace, int sms, cuda
   uint8_t* at = static_cast<uint8_t*>(workspace);
   cudaError_t e = align_operands(&x, &w, g.offsets, &at, sms, st);
   p.g.part = reinterpret_cast<float*>(at);
+  p.wide = reinterpret_cast<uintptr_t>(g.gate) % 16 == 0 && reinterpret_cast<uintptr_t>(g.up) % 16 == 0 &&
+           g.ld_gate % 8 == 0 && g.ld_up % 8 == 0;
   const MmChoice c = choose_tiles<Grad<__half>>(g, false, sms);
   if (e == cudaSuccess) e = encode(&p.x, x, g.dtype, false, c.box_rows());
   if (e == cudaSuccess) e = encode(&p.w, w, g.dtype, true, g.trans ? kBM : 64);

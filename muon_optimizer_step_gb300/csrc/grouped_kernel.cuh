@@ -2,16 +2,42 @@
 // an Op says which tensor maps the loads take (Params, x_map, w_map; kPasses: products whose sums are
 // added; kGated: two weights, 64 columns of each in a tile's 128 lanes), how many columns of the result a
 // CTA's tile is wide (kCols), whether sums are kept in short segments (fine), and what becomes of the
-// accumulators (ahead: before a tile's first, agree: whether warps that finish a tile together all
-// have it, finish, join for tiles that a cluster shares, zero_row).
+// accumulators (kWarps of the epilogue; ahead: before a tile's first, agree: whether warps that finish a tile
+// together all have it, finish, join for tiles that a cluster shares, zero_row).
+//
+// kFromTmem: a tile's sums go back into TMEM, over its last segment, and finish takes them from there 16 columns
+// at a time.  An epilogue that reads and computes a lot beside the sums has the registers to itself then:
+// with the sums in them it spilled, and what spills has no L1 to go to beside the stages (backward of
+// 98304 x 2048 -> 1408: 1706 us).
 #pragma once
 
 #include "grouped_tiles.cuh"
 
 namespace muon {
 
+// The variant with as many stages as the shared memory beside an Op's staging holds (what is left
+// of 227 KB are the barriers and the experts' offsets).
+template <typename V, int kStaging>
+struct Fit : V {
+  static constexpr int kRoom = (217 * 1024 - kStaging) / Shape<V>::kStage;
+  static constexpr int kStages = kRoom < V::kStages ? kRoom : V::kStages;
+};
+
+// Writes 16 accumulator columns of this warp's lanes.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 template <typename V, typename Op>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(128 + 32 * Op::kWarps, 1)
 grouped_mm_kernel(const __grid_constant__ typename Op::Params p) {
   using S = Shape<V>;
   constexpr int kCols = Op::kCols;
@@ -27,7 +53,7 @@ grouped_mm_kernel(const __grid_constant__ typename Op::Params p) {
     prefetch_tmap(&p.w);
     prefetch_tmap(&p.x);
   }
-  setup<V::kPair>(c, warp);
+  setup<V::kPair, Op::kWarps>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kMaxN, lane, first);
   __syncthreads();
@@ -154,32 +180,51 @@ grouped_mm_kernel(const __grid_constant__ typename Op::Params p) {
     }
     __syncwarp();
   } else if (warp >= 4) {
-    const int q = warp & 3, half = (warp - 4) >> 2;  // a quarter of the lanes, every second block
+    // A quarter of the lanes, every kGroups-th block of 32 columns.
+    constexpr int kGroups = Op::kWarps / 4, kBlocks = (V::kMaxN / 32 + kGroups - 1) / kGroups;
+    const int q = warp & 3, group = (warp - 4) >> 2;
     int use = 0;
     bool ok = true;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kCols>(t, f_tiles, g.n_experts, off, first);
-      Op::template ahead<V>(p, m, m.f0 + kCols * (int)rank, q, half, lane);
-      float sum[S::kBlocks][32];
+      Op::template ahead<V>(p, m, m.f0 + kCols * (int)rank, q, group, lane);
+      float sum[kBlocks][32];
       for (int kb = kb0; kb < kb1; kb += seg, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
+        // Where the epilogue takes the sums out of TMEM, one segment's are there already.
+        const bool last = Op::kFromTmem && !V::kSplit && kb + seg >= kb1;
+        if (last && kb == kb0) continue;
 #pragma unroll
-        for (int i = 0; i < S::kBlocks; ++i)
-          if ((2 * i + half) * 32 < m.n)
-            add_acc(tmem, use & 1, q, (2 * i + half) * 32, kb == kb0, sum[i]);
-        release_acc<V::kPair>(c, use & 1, rank, lane);
+        for (int i = 0; i < kBlocks; ++i) {
+          const int col = (kGroups * i + group) * 32;
+          if (col >= m.n) continue;
+          add_acc<kGroups == 2>(tmem, use & 1, q, col, kb == kb0, sum[i]);
+          if (last) {
+            const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)((use & 1) * kAccCols + col);
+            tmem_st_32x32b_x16(at, sum[i]);
+            tmem_st_32x32b_x16(at + 16, sum[i] + 16);
+          }
+        }
+        if (last) tmem_st_wait();
+        else release_acc<V::kPair>(c, use & 1, rank, lane);
       }
-      ok = Op::agree(q, half, ok);
+      ok = Op::agree(q, group, ok);
       if (!ok) break;
       if constexpr (V::kSplit) {
         // The operand stages are free: this tile's MMAs were the last.
-        if (half * 32 < m.n)
+        if (group * 32 < m.n)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            reinterpret_cast<float*>(smem)[(q * V::kMaxN + half * 32 + k) * 32 + lane] = sum[0][k];
+            reinterpret_cast<float*>(smem)[(q * V::kMaxN + group * 32 + k) * 32 + lane] = sum[0][k];
+      } else if constexpr (Op::kFromTmem) {
+        const int ab = (use - 1) & 1;
+        Op::template finish<V, kBlocks>(p, m, m.f0 + kCols * (int)rank, q, group, lane,
+                                        tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kAccCols),
+                                        smem + V::kStages * S::kStage);
+        release_acc<V::kPair>(c, ab, rank, lane);
       } else {
-        Op::template finish<V>(p, m, m.f0 + kCols * (int)rank, q, half, lane, sum,
+        Op::template finish<V>(p, m, m.f0 + kCols * (int)rank, q, group, lane, sum,
                                smem + V::kStages * S::kStage);
       }
     }
@@ -226,12 +271,13 @@ __device__ __forceinline__ void join_parts(uint8_t* smem, int parts, int r, int 
 template <typename O>
 __device__ __forceinline__ void store_8(O* dst, int left, const float (&v)[8]) {
   if (left >= 8 && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
-    __align__(16) O o[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) put(&o[k], v[k]);
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(O) / 2; ++k)
-      reinterpret_cast<uint4*>(dst)[k] = reinterpret_cast<const uint4*>(o)[k];
+    if constexpr (sizeof(O) == 4) {
+      reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_2<O>(v[0], v[1]), pack_2<O>(v[2], v[3]),
+                                                  pack_2<O>(v[4], v[5]), pack_2<O>(v[6], v[7]));
+    }
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -257,11 +303,68 @@ __device__ __forceinline__ void mm_store(const GroupedMm& g, const MmTile& m, in
   }
 }
 
+// A warp's accumulators turned around, kLines (8 or 16) rows of its 32 columns at a time: in the
+// accumulators a lane has one column, behind `stage` (kLines x 32 floats) eight columns of a row, so that
+// results and what is read beside them move in 16-byte units.  16-byte chunk c of line r stands in slot
+// c ^ (r & 7), free of bank conflicts both ways.  The loop over the chunks is not unrolled, only the
+// choice of the registers to store.
+__device__ __forceinline__ void put_line(float* stage, int lane, int k, float v) {
+  stage[32 * k + ((lane >> 2 ^ (k & 7)) << 2 | (lane & 3))] = v;
+}
+// Columns 8 (lane % 4) .. + 7 of a line.
+__device__ __forceinline__ void get_line(const float* stage, int lane, int line, float (&v)[8]) {
+  const float4* at = reinterpret_cast<const float4*>(stage + 32 * line);
+  const float4 a = at[(lane % 4 * 2) ^ (line & 7)], b = at[(lane % 4 * 2 + 1) ^ (line & 7)];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+// Stores chunk `c` of the accumulators (value(i, k): row k of block i) to the stage.
+template <int kBlocks, int kLines, typename F>
+__device__ __forceinline__ void put_chunk(float* stage, int lane, int c, const F& value) {
+#pragma unroll
+  for (int cc = 0; cc < kBlocks * 32 / kLines; ++cc)
+    if (cc == c)
+#pragma unroll
+      for (int k = 0; k < kLines; ++k) put_line(stage, lane, k, value(cc * kLines / 32, cc * kLines % 32 + k));
+}
+// The same of 16 accumulator columns in TMEM.
+__device__ __forceinline__ void put_tmem(float* stage, int lane, uint32_t taddr) {
+  uint32_t v[16];
+  tmem_ld_32x32b_x16(taddr, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) put_line(stage, lane, k, __uint_as_float(v[k]));
+}
+// First row of chunk c of a warp that has every kGroups-th block of 32 rows.
+template <int kLines, int kGroups>
+__device__ __forceinline__ int chunk_row(int c, int group) {
+  return (kGroups * (c * kLines / 32) + group) * 32 + c * kLines % 32;
+}
+// f(row, eight values) for the lane's part of each of the tile's rows.
+template <int kBlocks, int kLines, int kGroups, typename G, typename F>
+__device__ __forceinline__ void by_rows(float* stage, int lane, int rows, int group, const G& value, const F& f) {
+#pragma unroll 1
+  for (int c = 0; c < kBlocks * 32 / kLines; ++c) {
+    const int r0 = chunk_row<kLines, kGroups>(c, group);
+    if (r0 >= rows) break;
+    __syncwarp();
+    put_chunk<kBlocks, kLines>(stage, lane, c, value);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kLines; j += 8) {
+      const int line = j + lane / 4;
+      float v[8];
+      get_line(stage, lane, line, v);
+      if (r0 + line < rows) f(r0 + line, v);
+    }
+  }
+}
+
 // What products do whose result is stored as it is, in type O.
 template <typename O>
 struct Store {
   static constexpr bool kGated = false;
-  static constexpr int kCols = kBM, kStaging = 0;
+  static constexpr int kCols = kBM, kStaging = 0, kWarps = kEpiWarps;
+  static constexpr bool kFromTmem = false;
   static __device__ __forceinline__ bool agree(int, int, bool ok) { return ok; }
   template <typename P>
   static __device__ __forceinline__ bool fine(const P&) { return sizeof(O) == 4; }
@@ -277,12 +380,12 @@ struct Store {
       if ((2 * i + half) * 32 < m.n) mm_store<O>(p.g, m, 2 * i + half, f + 32 * q, lane, sum[i]);
   }
 
-  template <typename V, typename P>
+  template <typename V, int kWarps = kEpiWarps, typename P>
   static __device__ __forceinline__ void join(const P& p, const MmTile& m, const Part& part,
                                               uint8_t* smem) {
     const int cols = p.g.n - m.f0;
-    for (int i = threadIdx.x - 128 + part.index * kEpiWarps * 32; i < m.rows * 16;
-         i += part.parts * kEpiWarps * 32) {
+    for (int i = threadIdx.x - 128 + part.index * kWarps * 32; i < m.rows * 16;
+         i += part.parts * kWarps * 32) {
       const int r = i / 16, col = i % 16 * 8;
       float sum[8];
       join_parts<V>(smem, part.parts, r, col, sum);
@@ -290,10 +393,10 @@ struct Store {
     }
   }
 
-  template <typename P>
+  template <int kWarps = kEpiWarps, typename P>
   static __device__ __forceinline__ void zero_row(const P& p, int64_t row, int thread) {
     O* at = static_cast<O*>(p.g.y) + row * p.g.ldy;
-    for (int64_t f = thread; f < p.g.n; f += kEpiWarps * 32) put(&at[f], 0.f);
+    for (int64_t f = thread; f < p.g.n; f += kWarps * 32) put(&at[f], 0.f);
   }
 };
 
@@ -340,11 +443,13 @@ MmChoice choose_tiles(const GroupedMm& g, bool fine, int sms) {
   return c;
 }
 
-template <typename V, typename Op>
+template <typename W, typename Op>
 cudaError_t launch_op(const typename Op::Params& p, int parts, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
+  constexpr int kStaging = W::kSplit ? 0 : Op::kStaging;
+  using V = Fit<W, kStaging>;
   return launch(grouped_mm_kernel<V, Op>, p, mm_tiles<V>(p.g, Op::kCols), Shape<V>::kCtas * parts, sms,
-                V::kStages * Shape<V>::kStage + (V::kSplit ? 0 : Op::kStaging) + 1024, &ready, st);
+                V::kStages * Shape<V>::kStage + kStaging + 1024, &ready, st, 128 + 32 * Op::kWarps);
 }
 
 // kPairs: whether results of this type ever run on pairs.
