@@ -78,7 +78,7 @@ struct Gated {
     for (int c = 0; c < kBlocks * 2; ++c) {
       const int r0 = chunk_row<16, kWarps / 4>(c, group);
       if (r0 >= m.rows) break;
-      put_tmem(slots + mine * kSlot, lane, tmem + r0);
+      put_tmem_16(slots + mine * kSlot, lane, tmem + r0);
       sync_pair(pair);
       float g[8], u[8], v[8];
       get_line(slots, lane, line, g);
@@ -137,7 +137,7 @@ struct Grad {
   static constexpr bool kGated = false;
   static constexpr int kCols = kBM, kPasses = 1, kWarps = 16;
   static constexpr bool kFromTmem = true;
-  static constexpr int kSlot = 16 * 32;                 // floats: 16 rows of a warp's 32 columns
+  static constexpr int kSlot = 8 * 32;                  // floats: 8 rows of a warp's 32 columns
   static constexpr int kStaging = kWarps * kSlot * 4;
   static __device__ __forceinline__ const CUtensorMap* x_map(const Params& p, bool) { return &p.x; }
   static __device__ __forceinline__ const CUtensorMap* w_map(const Params& p, bool) { return &p.w; }
@@ -193,48 +193,47 @@ struct Grad {
     const GatedGrad& o = p.g;
     if (f + 32 * q >= o.n) return;
     float* stage = reinterpret_cast<float*>(staging) + (q + 4 * group) * kSlot;
-    const int col = f + 32 * q + lane % 4 * 8, inside = o.n - col;
+    const int col = f + 32 * q + lane % 4 * 8;
+    // g, u and the row's weight of the next chunk arrive while this one is computed.
+    uint4 g, u;
+    float w = 1.f;
+    const auto load = [&](int c) {
+      const int r = chunk_row<8, kWarps / 4>(c, group) + lane / 4, left = r < m.rows ? o.n - col : 0;
+      const int64_t row = (int64_t)m.row + r;
+      g = load_row(o.gate, row * o.ld_gate + col, left, p.wide);
+      u = load_row(o.up, row * o.ld_up + col, left, p.wide);
+      if (o.p != nullptr && left > 0) w = o.p[row];
+    };
+    load(0);
 #pragma unroll 1
-    for (int c = 0; c < kBlocks * 2; ++c) {
-      const int r0 = chunk_row<16, kWarps / 4>(c, group);
+    for (int c = 0; c < kBlocks * 4; ++c) {
+      const int r0 = chunk_row<8, kWarps / 4>(c, group), r = r0 + lane / 4, left = r < m.rows ? o.n - col : 0;
       if (r0 >= m.rows) break;
-      uint4 g[2], u[2];
-      float w[2];
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+      const float weight = w;
+      if (c + 1 < kBlocks * 4) load(c + 1);
+      __syncwarp();
+      put_tmem_8(stage, lane, tmem + r0);
+      __syncwarp();
+      float dh[8], dg[8], du[8], out[8], term = 0.f;
+      get_line(stage, lane, lane / 4, dh);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = r0 + 8 * j + lane / 4, left = r < m.rows ? inside : 0;
-        const int64_t row = (int64_t)m.row + r;
-        g[j] = load_row(o.gate, row * o.ld_gate + col, left, p.wide);
-        u[j] = load_row(o.up, row * o.ld_up + col, left, p.wide);
-        w[j] = o.p != nullptr && left > 0 ? o.p[row] : 1.f;
+      for (int k = 0; k < 8; k += 2) {
+        const float2 a = unpack_2<T>(gw[k / 2]), b = unpack_2<T>(uw[k / 2]);
+        const float t0 = values(dh[k], a.x, b.x, weight, &dg[k], &du[k], &out[k]);
+        const float t1 = values(dh[k + 1], a.y, b.y, weight, &dg[k + 1], &du[k + 1], &out[k + 1]);
+        if (k < left) term += t0;
+        if (k + 1 < left) term += t1;
       }
-      __syncwarp();
-      put_tmem(stage, lane, tmem + r0);
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int line = 8 * j + lane / 4, r = r0 + line, left = r < m.rows ? inside : 0;
-        const int64_t row = (int64_t)m.row + r;
-        const uint32_t gw[4] = {g[j].x, g[j].y, g[j].z, g[j].w}, uw[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-        float dh[8], dg[8], du[8], out[8], term = 0.f;
-        get_line(stage, lane, line, dh);
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          const float2 a = unpack_2<T>(gw[k / 2]), b = unpack_2<T>(uw[k / 2]);
-          const float t0 = values(dh[k], a.x, b.x, w[j], &dg[k], &du[k], &out[k]);
-          const float t1 = values(dh[k + 1], a.y, b.y, w[j], &dg[k + 1], &du[k + 1], &out[k + 1]);
-          if (k < left) term += t0;
-          if (k + 1 < left) term += t1;
-        }
-        store_8(static_cast<T*>(o.dgate) + row * o.ld_dgate + col, left, dg);
-        store_8(static_cast<T*>(o.dup) + row * o.ld_dup + col, left, du);
-        if (o.y != nullptr) store_8(static_cast<T*>(o.y) + row * o.ldy + col, left, out);
-        if (o.dp != nullptr) {
-          // Four neighbouring lanes have the row's 32 columns.
-          term += __shfl_xor_sync(0xffffffffu, term, 1);
-          term += __shfl_xor_sync(0xffffffffu, term, 2);
-          if (lane % 4 == 0 && left > 0) o.part[(int64_t)((f + 32 * q) / 32) * o.rows + row] = term;
-        }
+      const int64_t row = (int64_t)m.row + r;
+      store_8(static_cast<T*>(o.dgate) + row * o.ld_dgate + col, left, dg);
+      store_8(static_cast<T*>(o.dup) + row * o.ld_dup + col, left, du);
+      if (o.y != nullptr) store_8(static_cast<T*>(o.y) + row * o.ldy + col, left, out);
+      if (o.dp != nullptr) {
+        // Four neighbouring lanes have the row's 32 columns.
+        term += __shfl_xor_sync(0xffffffffu, term, 1);
+        term += __shfl_xor_sync(0xffffffffu, term, 2);
+        if (lane % 4 == 0 && left > 0) o.part[(int64_t)((f + 32 * q) / 32) * o.rows + row] = term;
       }
     }
   }

@@ -189,6 +189,12 @@ grouped_mm_kernel(const __grid_constant__ typename Op::Params p) {
       const MmTile m = mm_tile<V, kCols>(t, f_tiles, g.n_experts, off, first);
       Op::template ahead<V>(p, m, m.f0 + kCols * (int)rank, q, group, lane);
       float sum[kBlocks][32];
+      if constexpr (Op::kFromTmem) {  // (or the last tile's would be kept through its epilogue)
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sum[i][k] = 0.f;
+      }
       for (int kb = kb0; kb < kb1; kb += seg, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
@@ -326,13 +332,24 @@ __device__ __forceinline__ void put_chunk(float* stage, int lane, int c, const F
 #pragma unroll
       for (int k = 0; k < kLines; ++k) put_line(stage, lane, k, value(cc * kLines / 32, cc * kLines % 32 + k));
 }
-// The same of 16 accumulator columns in TMEM.
-__device__ __forceinline__ void put_tmem(float* stage, int lane, uint32_t taddr) {
+// The same of 16, or 8, accumulator columns in TMEM.
+__device__ __forceinline__ void put_tmem_16(float* stage, int lane, uint32_t taddr) {
   uint32_t v[16];
   tmem_ld_32x32b_x16(taddr, v);
   tmem_ld_wait();
 #pragma unroll
   for (int k = 0; k < 16; ++k) put_line(stage, lane, k, __uint_as_float(v[k]));
+}
+__device__ __forceinline__ void put_tmem_8(float* stage, int lane, uint32_t taddr) {
+  uint32_t v[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr)
+      : "memory");
+  tmem_ld_wait();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) put_line(stage, lane, k, __uint_as_float(v[k]));
 }
 // First row of chunk c of a warp that has every kGroups-th block of 32 rows.
 template <int kLines, int kGroups>
