@@ -1,7 +1,9 @@
-// The sigmoid of the gated activation.
+// The sigmoid of the gated activation, one by one and two at a time.
 #pragma once
 
 #include <cuda_runtime.h>
+
+#include "element.cuh"
 
 namespace muon {
 
@@ -13,6 +15,23 @@ __device__ __forceinline__ float sigmoid(float x) {
   const float e = kFast ? __expf(-fabsf(x)) : expf(-fabsf(x));
   const float r = sizeof(T) == 4 ? 1.f / (1.f + e) : __fdividef(1.f, 1.f + e);
   return x < 0.f ? e * r : r;
+}
+
+// The same of two values, for results that are rounded to 16 bits.  exp(-|x|) is the square of 2^(-|x| log2(e)
+// / 2), which stays normal wherever exp(-|x|) is not zero in fp32, so that the fast power, which flushes
+// subnormals, does for all x; 1 + e lies in 1 .. 2, where the fast reciprocal is within an ulp.
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
+  const float2 v = parts(x);
+  float2 h, r;
+  const float half_log2e = 0.72134752f;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h.x) : "f"(-fabsf(v.x) * half_log2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h.y) : "f"(-fabsf(v.y) * half_log2e));
+  const f32x2 hh = pair(h.x, h.y), e = mul2(hh, hh);
+  const float2 one = parts(add2(e, pair(1.f, 1.f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(one.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(one.y));
+  const float2 er = parts(mul2(e, pair(r.x, r.y)));
+  return pair(v.x < 0.f ? er.x : r.x, v.y < 0.f ? er.y : r.y);
 }
 
 }  // namespace muon

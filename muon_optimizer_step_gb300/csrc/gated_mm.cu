@@ -12,8 +12,7 @@
 // columns of g and the one that holds them of u put 16 rows at a time into shared memory; each then takes
 // g and u of 8 of them.  g and u go to memory only where the caller keeps them.
 //
-// grad: dh stays in the accumulators.  The epilogue reads g and u of its tile (asked into L2 when the
-// tile begins) and writes three results.  dp_r is summed over 32 columns in a warp; a second kernel adds
+// grad: dh stays in the accumulators.  The epilogue reads g and u of its tile and writes three results.  dp_r is summed over 32 columns in a warp; a second kernel adds
 // those sums in order, so equal inputs give equal bits.
 //
 // sum: the k-blocks of the second product follow those of the first.
@@ -40,7 +39,7 @@ struct Gated {
   using Params = GatedParams;
   static constexpr bool kGated = true;
   static constexpr int kCols = 64, kPasses = 1, kWarps = 16;
-  static constexpr bool kFromTmem = true;
+  static constexpr bool kFromTmem = true, kKeep = true;
   static constexpr int kSlot = 16 * 32;                  // floats: 16 rows of a warp's 32 columns
   static constexpr int kStaging = kWarps * kSlot * 4;
   static __device__ __forceinline__ const CUtensorMap* x_map(const Params& p, bool) { return &p.x; }
@@ -63,13 +62,21 @@ struct Gated {
     return all != 0;
   }
 
-  static __device__ __forceinline__ float value(float g, float u, float w) {
-    return g * sigmoid<T, true>(g) * u * w;
+  static __device__ __forceinline__ void values(const float (&g)[8], const float (&u)[8], float w,
+                                                float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const f32x2 x = pair(g[k], g[k + 1]);
+      const float2 a = parts(mul2(mul2(mul2(x, sigmoid2(x)), pair(u[k], u[k + 1])), pair(w, w)));
+      v[k] = a.x, v[k + 1] = a.y;
+    }
   }
 
-  template <typename V, int kBlocks>
+  template <typename V, int kBlocks, typename F>
   static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int group,
-                                                int lane, uint32_t tmem, uint8_t* staging) {
+                                                int lane, uint32_t tmem, const float (&kept)[32],
+                                                const F& release, uint8_t* staging) {
+    constexpr int kInTmem = kBlocks == 1 || !kKeep ? kBlocks * 2 : (kBlocks - 1) * 2;  // chunks
     const GatedMm& o = p.g;
     const int pair = gate_pair(q, group), mine = q >> 1;  // 0: has g; 1: has u
     float* slots = reinterpret_cast<float*>(staging) + pair * 2 * kSlot;
@@ -78,7 +85,9 @@ struct Gated {
     for (int c = 0; c < kBlocks * 2; ++c) {
       const int r0 = chunk_row<16, kWarps / 4>(c, group);
       if (r0 >= m.rows) break;
-      put_tmem_16(slots + mine * kSlot, lane, tmem + r0);
+      if (c < kInTmem) put_tmem_16(slots + mine * kSlot, lane, tmem + r0);
+      else put_chunk<1, 16>(slots + mine * kSlot, lane, c - kInTmem, [&](int, int k) { return kept[k]; });
+      if (c == kInTmem - 1) release();
       sync_pair(pair);
       float g[8], u[8], v[8];
       get_line(slots, lane, line, g);
@@ -87,8 +96,7 @@ struct Gated {
       if (r0 + line >= m.rows) continue;
       const int64_t row = (int64_t)m.row + r0 + line;
       const float w = o.p != nullptr ? o.p[row] : 1.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = value(g[k], u[k], w);
+      values(g, u, w, v);
       store_8(static_cast<T*>(o.y) + row * o.ldy + col, o.n - col, v);
       if (o.gate != nullptr) store_8(static_cast<T*>(o.gate) + row * o.ld_gate + col, o.n - col, g);
       if (o.up != nullptr) store_8(static_cast<T*>(o.up) + row * o.ld_up + col, o.n - col, u);
@@ -107,8 +115,7 @@ struct Gated {
       join_parts<V>(smem, part.parts, r, 64 + col, u);
       const int64_t row = (int64_t)m.row + r;
       const float w = o.p != nullptr ? o.p[row] : 1.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = value(g[k], u[k], w);
+      values(g, u, w, v);
       store_8(static_cast<T*>(o.y) + row * o.ldy + f, o.n - f, v);
       if (o.gate != nullptr) store_8(static_cast<T*>(o.gate) + row * o.ld_gate + f, o.n - f, g);
       if (o.up != nullptr) store_8(static_cast<T*>(o.up) + row * o.ld_up + f, o.n - f, u);
@@ -128,7 +135,7 @@ struct Gated {
 struct GradParams {
   CUtensorMap x, w;  // as MmParams
   GatedGrad g;
-  bool wide;         // every row of gate and up starts on 16 bytes
+  bool wide;         // every row of gate, up and the results starts on 16 bytes
 };
 
 template <typename T>
@@ -136,7 +143,7 @@ struct Grad {
   using Params = GradParams;
   static constexpr bool kGated = false;
   static constexpr int kCols = kBM, kPasses = 1, kWarps = 16;
-  static constexpr bool kFromTmem = true;
+  static constexpr bool kFromTmem = true, kKeep = false;
   static constexpr int kSlot = 8 * 32;                  // floats: 8 rows of a warp's 32 columns
   static constexpr int kStaging = kWarps * kSlot * 4;
   static __device__ __forceinline__ const CUtensorMap* x_map(const Params& p, bool) { return &p.x; }
@@ -145,95 +152,102 @@ struct Grad {
   static __device__ __forceinline__ bool fine(const Params& p) { return p.g.dp != nullptr; }
   static __device__ __forceinline__ bool agree(int, int, bool ok) { return ok; }
 
-  // Asks for the tile's g and u: a row per lane, the lines of its columns.
   template <typename V>
-  static __device__ __forceinline__ void ahead(const Params& p, const MmTile& m, int f, int q, int group,
-                                               int lane) {
-    const GatedGrad& o = p.g;
-    const int r = 16 * (q + 4 * group) + lane % 16, cols = min(kBM, o.n - f);
-    if (r >= m.rows || cols <= 0 || lane >= 16) return;
-    const int64_t row = (int64_t)m.row + r;
-    const char* g = reinterpret_cast<const char*>(static_cast<const T*>(o.gate) + row * o.ld_gate + f);
-    const char* u = reinterpret_cast<const char*>(static_cast<const T*>(o.up) + row * o.ld_up + f);
-    const int last = 2 * cols - 2;
-#pragma unroll
-    for (int b = 0; b <= 256; b += 128) {
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(g + min(b, last)));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(u + min(b, last)));
-    }
+  static __device__ __forceinline__ void ahead(const Params&, const MmTile&, int, int, int, int) {}
+
+  // From dh, g, u and the row's weight (twice), two at a time: dgate, dup and the activation; adds dp's terms.
+  // silu'(g) = s + silu(g) (1 - s).
+  static __device__ __forceinline__ void values(f32x2 dh, f32x2 g, f32x2 u, f32x2 w, float* dgate, float* dup,
+                                                float* out, f32x2& dp) {
+    const f32x2 s = sigmoid2(g), silu = mul2(g, s);
+    const f32x2 slope = fma2(silu, fma2(s, pair(-1.f, -1.f), pair(1.f, 1.f)), s);
+    const f32x2 d = mul2(dh, w), t = mul2(silu, u);
+    const float2 a = parts(mul2(d, mul2(u, slope))), b = parts(mul2(d, silu)), c = parts(mul2(t, w));
+    dgate[0] = a.x, dgate[1] = a.y, dup[0] = b.x, dup[1] = b.y, out[0] = c.x, out[1] = c.y;
+    dp = fma2(dh, t, dp);
   }
 
-  // From dh, g, u and the row's weight: dgate, dup and the activation; returns dp's term.  silu'(g) = s +
-  // silu(g) (1 - s), with s and 1 - s both from exp(-|g|): neither overflows nor cancels.
-  static __device__ __forceinline__ float values(float dh, float g, float u, float w, float* dgate,
-                                                 float* dup, float* out) {
-    const float e = __expf(-fabsf(g)), r = __fdividef(1.f, 1.f + e), er = e * r;
-    const float s = g < 0.f ? er : r, silu = g * s, slope = fmaf(silu, g < 0.f ? r : er, s);
-    const float d = dh * w, t = silu * u;
-    *dup = d * silu;
-    *dgate = d * (u * slope);
-    *out = t * w;
-    return dh * t;
-  }
-
-  // Eight values of a row from base + at on, `left` of them inside it, as they are stored; wide: on 16
-  // bytes.  (Both ways end in the same words: nothing waits for the load here.)
-  static __device__ __forceinline__ uint4 load_row(const void* base, int64_t at, int left, bool wide) {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    if (wide && left >= 8) return *reinterpret_cast<const uint4*>(p);
+  // Eight values of a row, `left` of them inside it, as they are stored.  (Both ways end in the same words:
+  // nothing waits for the load here.)
+  static __device__ __forceinline__ uint4 load_row(const T* at, int left, bool wide) {
+    if (wide && left >= 8) return *reinterpret_cast<const uint4*>(at);
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(at);
     uint32_t e[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) e[k] = k < left ? p[k] : 0;
     return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
   }
+  static __device__ __forceinline__ void store_row(T* at, int left, bool wide, const float (&v)[8]) {
+    if (wide && left >= 8) {
+      *reinterpret_cast<uint4*>(at) = make_uint4(pack_2<T>(v[0], v[1]), pack_2<T>(v[2], v[3]),
+                                                 pack_2<T>(v[4], v[5]), pack_2<T>(v[6], v[7]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < left) put(&at[k], v[k]);
+    }
+  }
 
-  template <typename V, int kBlocks>
+  // 8 rows of the warp's 32 columns at a time: dh goes through shared memory (see put_line), so that a lane
+  // then has eight columns of a row, the width of its loads and stores.
+  template <typename V, int kBlocks, typename F>
   static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int group,
-                                                int lane, uint32_t tmem, uint8_t* staging) {
+                                                int lane, uint32_t tmem, const float (&kept)[32],
+                                                const F& release, uint8_t* staging) {
+    constexpr int kInTmem = kBlocks == 1 || !kKeep ? kBlocks * 4 : (kBlocks - 1) * 4;  // chunks
     const GatedGrad& o = p.g;
     if (f + 32 * q >= o.n) return;
     float* stage = reinterpret_cast<float*>(staging) + (q + 4 * group) * kSlot;
-    const int col = f + 32 * q + lane % 4 * 8;
+    const int col = f + 32 * q + lane % 4 * 8, inside = o.n - col;
+    const bool wide = p.wide;
     // g, u and the row's weight of the next chunk arrive while this one is computed.
+    const T* gate = static_cast<const T*>(o.gate) + (int64_t)m.row * o.ld_gate + col;
+    const T* up = static_cast<const T*>(o.up) + (int64_t)m.row * o.ld_up + col;
+    T* dgate = static_cast<T*>(o.dgate) + (int64_t)m.row * o.ld_dgate + col;
+    T* dup = static_cast<T*>(o.dup) + (int64_t)m.row * o.ld_dup + col;
+    T* act = static_cast<T*>(o.y) + (int64_t)m.row * o.ldy + col;
     uint4 g, u;
     float w = 1.f;
     const auto load = [&](int c) {
-      const int r = chunk_row<8, kWarps / 4>(c, group) + lane / 4, left = r < m.rows ? o.n - col : 0;
-      const int64_t row = (int64_t)m.row + r;
-      g = load_row(o.gate, row * o.ld_gate + col, left, p.wide);
-      u = load_row(o.up, row * o.ld_up + col, left, p.wide);
-      if (o.p != nullptr && left > 0) w = o.p[row];
+      const int r = chunk_row<8, kWarps / 4>(c, group) + lane / 4, left = r < m.rows ? inside : 0;
+      g = load_row(gate + r * o.ld_gate, left, wide);
+      u = load_row(up + r * o.ld_up, left, wide);
+      if (o.p != nullptr && left > 0) w = o.p[m.row + r];
     };
     load(0);
 #pragma unroll 1
     for (int c = 0; c < kBlocks * 4; ++c) {
-      const int r0 = chunk_row<8, kWarps / 4>(c, group), r = r0 + lane / 4, left = r < m.rows ? o.n - col : 0;
+      const int r0 = chunk_row<8, kWarps / 4>(c, group), r = r0 + lane / 4, left = r < m.rows ? inside : 0;
       if (r0 >= m.rows) break;
       const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
       const float weight = w;
       if (c + 1 < kBlocks * 4) load(c + 1);
       __syncwarp();
-      put_tmem_8(stage, lane, tmem + r0);
+      if (c < kInTmem) put_tmem_8(stage, lane, tmem + r0);
+      else put_chunk<1, 8>(stage, lane, c - kInTmem, [&](int, int k) { return kept[k]; });
+      if (c == kInTmem - 1) release();
       __syncwarp();
-      float dh[8], dg[8], du[8], out[8], term = 0.f;
+      float dh[8], dg[8], du[8], out[8];
+      f32x2 terms = 0;
       get_line(stage, lane, lane / 4, dh);
+      if (left < 8)  // columns outside: nothing that dp adds
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dh[k] = k < left ? dh[k] : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; k += 2) {
         const float2 a = unpack_2<T>(gw[k / 2]), b = unpack_2<T>(uw[k / 2]);
-        const float t0 = values(dh[k], a.x, b.x, weight, &dg[k], &du[k], &out[k]);
-        const float t1 = values(dh[k + 1], a.y, b.y, weight, &dg[k + 1], &du[k + 1], &out[k + 1]);
-        if (k < left) term += t0;
-        if (k + 1 < left) term += t1;
+        values(pair(dh[k], dh[k + 1]), pair(a.x, a.y), pair(b.x, b.y), pair(weight, weight), &dg[k], &du[k],
+               &out[k], terms);
       }
-      const int64_t row = (int64_t)m.row + r;
-      store_8(static_cast<T*>(o.dgate) + row * o.ld_dgate + col, left, dg);
-      store_8(static_cast<T*>(o.dup) + row * o.ld_dup + col, left, du);
-      if (o.y != nullptr) store_8(static_cast<T*>(o.y) + row * o.ldy + col, left, out);
+      store_row(dgate + r * o.ld_dgate, left, wide, dg);
+      store_row(dup + r * o.ld_dup, left, wide, du);
+      if (o.y != nullptr) store_row(act + r * o.ldy, left, wide, out);
       if (o.dp != nullptr) {
         // Four neighbouring lanes have the row's 32 columns.
+        float term = parts(terms).x + parts(terms).y;
         term += __shfl_xor_sync(0xffffffffu, term, 1);
         term += __shfl_xor_sync(0xffffffffu, term, 2);
-        if (lane % 4 == 0 && left > 0) o.part[(int64_t)((f + 32 * q) / 32) * o.rows + row] = term;
+        if (lane % 4 == 0 && left > 0) o.part[(int64_t)((f + 32 * q) / 32) * o.rows + m.row + r] = term;
       }
     }
   }
@@ -245,7 +259,8 @@ struct Grad {
     for (int i = threadIdx.x - 128 + part.index * kWarps * 32; i < m.rows * 16;
          i += part.parts * kWarps * 32) {
       const int r = i / 16, col = i % 16 * 8, f = m.f0 + col, left = o.n - f;
-      float dh[8], dg[8], du[8], out[8], term = 0.f;
+      float dh[8], g[8], u[8], dg[8], du[8], out[8];
+      f32x2 terms = 0;
       join_parts<V>(smem, part.parts, r, col, dh);
       const int64_t row = (int64_t)m.row + r;
       const float w = o.p != nullptr ? o.p[row] : 1.f;
@@ -253,15 +268,20 @@ struct Grad {
       const T* up = static_cast<const T*>(o.up) + row * o.ld_up + f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float g = k < left ? cvt(gate[k]) : 0.f, u = k < left ? cvt(up[k]) : 0.f;
-        const float t = values(dh[k], g, u, w, &dg[k], &du[k], &out[k]);
-        if (k < left) term += t;
+        dh[k] = k < left ? dh[k] : 0.f;
+        g[k] = k < left ? cvt(gate[k]) : 0.f;
+        u[k] = k < left ? cvt(up[k]) : 0.f;
       }
+#pragma unroll
+      for (int k = 0; k < 8; k += 2)
+        values(pair(dh[k], dh[k + 1]), pair(g[k], g[k + 1]), pair(u[k], u[k + 1]), pair(w, w), &dg[k], &du[k],
+               &out[k], terms);
       store_8(static_cast<T*>(o.dgate) + row * o.ld_dgate + f, left, dg);
       store_8(static_cast<T*>(o.dup) + row * o.ld_dup + f, left, du);
       if (o.y != nullptr) store_8(static_cast<T*>(o.y) + row * o.ldy + f, left, out);
       if (o.dp != nullptr) {
         // Four neighbouring threads have 32 columns (a row's 16 are all here).
+        float term = parts(terms).x + parts(terms).y;
         const uint32_t four = 0xfu << (threadIdx.x & 28);
         term += __shfl_xor_sync(four, term, 1);
         term += __shfl_xor_sync(four, term, 2);
@@ -375,8 +395,11 @@ cudaError_t launch_gated_grad(const GatedGrad& g, void* workspace, int sms, cuda
   uint8_t* at = static_cast<uint8_t*>(workspace);
   cudaError_t e = align_operands(&x, &w, g.offsets, &at, sms, st);
   p.g.part = reinterpret_cast<float*>(at);
-  p.wide = reinterpret_cast<uintptr_t>(g.gate) % 16 == 0 && reinterpret_cast<uintptr_t>(g.up) % 16 == 0 &&
-           g.ld_gate % 8 == 0 && g.ld_up % 8 == 0;
+  p.wide = true;
+  const void* const matrices[] = {g.gate, g.up, g.dgate, g.dup, g.y};
+  const int64_t pitches[] = {g.ld_gate, g.ld_up, g.ld_dgate, g.ld_dup, g.y != nullptr ? g.ldy : 0};
+  for (int i = 0; i < 5; ++i)
+    p.wide = p.wide && reinterpret_cast<uintptr_t>(matrices[i]) % 16 == 0 && pitches[i] % 8 == 0;
   const MmChoice c = choose_tiles<Grad<__half>>(g, false, sms);
   if (e == cudaSuccess) e = encode(&p.x, x, g.dtype, false, c.box_rows());
   if (e == cudaSuccess) e = encode(&p.w, w, g.dtype, true, g.trans ? kBM : 64);

@@ -5,10 +5,11 @@
 // accumulators (kWarps of the epilogue; ahead: before a tile's first, agree: whether warps that finish a tile
 // together all have it, finish, join for tiles that a cluster shares, zero_row).
 //
-// kFromTmem: a tile's sums go back into TMEM, over its last segment, and finish takes them from there 16 columns
-// at a time.  An epilogue that reads and computes a lot beside the sums has the registers to itself then:
-// with the sums in them it spilled, and what spills has no L1 to go to beside the stages (backward of
-// 98304 x 2048 -> 1408: 1706 us).
+// kFromTmem: all but the last of a warp's blocks of sums go back into TMEM, over the tile's last segment, and
+// finish takes them from there a few columns at a time; once it has, it hands the accumulator back and takes
+// the last block from registers.  With all sums in registers an epilogue that reads and computes a lot beside
+// them spilled, and what spills has no L1 to go to beside the stages (backward of 98304 x 2048 -> 1408:
+// 1706 us); with all of them in TMEM the MMAs waited for the accumulator (636 us).
 #pragma once
 
 #include "grouped_tiles.cuh"
@@ -198,15 +199,15 @@ grouped_mm_kernel(const __grid_constant__ typename Op::Params p) {
       for (int kb = kb0; kb < kb1; kb += seg, ++use) {
         ok = wait_acc(c, use, g.err);
         if (!ok) break;
-        // Where the epilogue takes the sums out of TMEM, one segment's are there already.
         const bool last = Op::kFromTmem && !V::kSplit && kb + seg >= kb1;
-        if (last && kb == kb0) continue;
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
           const int col = (kGroups * i + group) * 32;
-          if (col >= m.n) continue;
+          const bool back = last && (kBlocks == 1 || !Op::kKeep || i < kBlocks - 1);
+          // (One segment's sums are in TMEM already.)
+          if (col >= m.n || (back && kb == kb0)) continue;
           add_acc<kGroups == 2>(tmem, use & 1, q, col, kb == kb0, sum[i]);
-          if (last) {
+          if (back) {
             const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)((use & 1) * kAccCols + col);
             tmem_st_32x32b_x16(at, sum[i]);
             tmem_st_32x32b_x16(at + 16, sum[i] + 16);
@@ -225,10 +226,16 @@ grouped_mm_kernel(const __grid_constant__ typename Op::Params p) {
             reinterpret_cast<float*>(smem)[(q * V::kMaxN + group * 32 + k) * 32 + lane] = sum[0][k];
       } else if constexpr (Op::kFromTmem) {
         const int ab = (use - 1) & 1;
-        Op::template finish<V, kBlocks>(p, m, m.f0 + kCols * (int)rank, q, group, lane,
-                                        tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kAccCols),
-                                        smem + V::kStages * S::kStage);
-        release_acc<V::kPair>(c, ab, rank, lane);
+        bool held = true;
+        Op::template finish<V, kBlocks>(
+            p, m, m.f0 + kCols * (int)rank, q, group, lane,
+            tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kAccCols), sum[kBlocks - 1],
+            [&] {
+              release_acc<V::kPair>(c, ab, rank, lane);
+              held = false;
+            },
+            smem + V::kStages * S::kStage);
+        if (held) release_acc<V::kPair>(c, ab, rank, lane);
       } else {
         Op::template finish<V>(p, m, m.f0 + kCols * (int)rank, q, group, lane, sum,
                                smem + V::kStages * S::kStage);
@@ -315,7 +322,7 @@ __device__ __forceinline__ void mm_store(const GroupedMm& g, const MmTile& m, in
 // c ^ (r & 7), free of bank conflicts both ways.  The loop over the chunks is not unrolled, only the
 // choice of the registers to store.
 __device__ __forceinline__ void put_line(float* stage, int lane, int k, float v) {
-  stage[32 * k + ((lane >> 2 ^ (k & 7)) << 2 | (lane & 3))] = v;
+  stage[32 * k + (lane ^ (k & 7) << 2)] = v;  // chunk lane / 4, element lane % 4
 }
 // Columns 8 (lane % 4) .. + 7 of a line.
 __device__ __forceinline__ void get_line(const float* stage, int lane, int line, float (&v)[8]) {
@@ -381,7 +388,7 @@ template <typename O>
 struct Store {
   static constexpr bool kGated = false;
   static constexpr int kCols = kBM, kStaging = 0, kWarps = kEpiWarps;
-  static constexpr bool kFromTmem = false;
+  static constexpr bool kFromTmem = false, kKeep = false;
   static __device__ __forceinline__ bool agree(int, int, bool ok) { return ok; }
   template <typename P>
   static __device__ __forceinline__ bool fine(const P&) { return sizeof(O) == 4; }
