@@ -22,8 +22,7 @@ namespace {
 constexpr int kBK8 = 128;   // elements of a k-block: 128 bytes
 constexpr int kSlots = 8;   // of scales
 constexpr int kAhead = 6;   // k-blocks that scales are asked for ahead
-constexpr int kWarps8 = 16;              // of the epilogue
-constexpr int kThreads8 = 128 + 32 * kWarps8;
+constexpr uint32_t kAccs = 2;
 constexpr int kStaging8 = 1024;          // bytes of each epilogue warp: 8 rows of its 32 columns
 
 struct Fp8Params {
@@ -31,15 +30,8 @@ struct Fp8Params {
   Fp8Mm g;
 };
 
-// Tile variants as for 16-bit operands (see grouped_tiles.cuh), with a k-block per stage.
-struct Pair8 {
-  static constexpr bool kPair = true, kSplit = false;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 5, kSub = 1;
-};
-struct Wide8 {
-  static constexpr bool kPair = false, kSplit = false;
-  static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 4, kSub = 1;
-};
+// Few rows per expert: the tiles of y^T, as for 16-bit operands (see grouped_tiles.cuh), with a k-block per
+// stage.
 struct Narrow8 {
   static constexpr bool kPair = false, kSplit = false;
   static constexpr int kMaxN = 64, kBoxRows = 16, kStages = 6, kSub = 1;
@@ -50,7 +42,7 @@ struct Split8 {
 };
 
 struct Scales {
-  float slot[kSlots][256];
+  float slot[kSlots][64];
   float weight[kSlots][32];  // the weight's scale, a copy for each lane of warp 3
   uint64_t full[kSlots], empty[kSlots];
 };
@@ -59,28 +51,22 @@ __device__ __forceinline__ void copy_4(void* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// v times the scales s, two at a time, added to the sums.
-__device__ __forceinline__ void add_scaled(uint64_t& sum, uint32_t v0, uint32_t v1, uint64_t s) {
-  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
-      : "+l"(sum)
-      : "r"(v0), "r"(v1), "l"(s));
-}
-__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ float low(f32x2 v) { return parts(v).x; }
+__device__ __forceinline__ float high(f32x2 v) { return parts(v).y; }
 
-// sum += 16 accumulator columns in v, times their scales from s on (16-byte aligned).
-__device__ __forceinline__ void add_block(uint64_t (&sum)[16], int at, const uint32_t (&v)[16], const float* s) {
+// sum += 32 accumulator columns in v, times their scales from s on (16-byte aligned).
+__device__ __forceinline__ void add_block(f32x2 (&sum)[16], const uint32_t (&v)[32], const float* s) {
 #pragma unroll
-  for (int k = 0; k < 16; k += 4) {
-    uint64_t x, y;
+  for (int k = 0; k < 32; k += 4) {
+    f32x2 x, y;
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(smem_u32(s + k)));
-    add_scaled(sum[at + k / 2], v[k], v[k + 1], x);
-    add_scaled(sum[at + k / 2 + 1], v[k + 2], v[k + 3], y);
+    sum[k / 2] = fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), x, sum[k / 2]);
+    sum[k / 2 + 1] = fma2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), y, sum[k / 2 + 1]);
   }
 }
 
 template <typename V, typename O>
-__global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_constant__ Fp8Params p) {
+__global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_constant__ Fp8Params p) {
   using S = Shape<V>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
@@ -98,9 +84,9 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_const
   if (threadIdx.x == 0)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sc.full[s], 1);
-      mbar_init(&sc.empty[s], kWarps8);
+      mbar_init(&sc.empty[s], kEpiWarps);
     }
-  setup<V::kPair, kWarps8>(c, warp);
+  setup<V::kPair>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kMaxN, lane, first);
   __syncthreads();
@@ -151,18 +137,18 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_const
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     Ring<V::kStages> ring;
-    int use = 0;
+    uint32_t use = 0;
     bool ok = true;
     const uint32_t a0 = desc_lo(smem_u32(smem), 16), b0 = desc_lo(smem_u32(smem) + kABytes, 16);
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kBM>(t, f_tiles, g.n_experts, off, first);
       const uint32_t idesc = idesc_16(false, S::kM, m.n, 0, 0);  // e4m3 has the same code as fp16
       for (int kb = kb0; kb < kb1; ++kb, ++use) {
-        ok = wait_warp(&c.acc_empty[use & 1], ((use >> 1) & 1) ^ 1u, g.err, &c.abort) &&
+        ok = wait_warp(&c.acc_empty[use % kAccs], (use / kAccs & 1u) ^ 1u, g.err, &c.abort) &&
              wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (use & 1) * kAccCols;
+        const uint32_t d = tmem + use % kAccs * kAccCols;
         const uint32_t a = a0 + ring.stage * (S::kStage / 16), b = b0 + ring.stage * (S::kStage / 16);
         if (elect_one()) {
           // K = 32 each; columns past k are zeros in both operands.
@@ -171,7 +157,7 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_const
           mma<V::kPair, true>(d, a + 4, b + 4, idesc, 1);
           mma<V::kPair, true>(d, a + 6, b + 6, idesc, 1);
           commit<V::kPair>(&c.empty[ring.stage]);
-          commit<V::kPair>(&c.acc_full[use & 1]);
+          commit<V::kPair>(&c.acc_full[use % kAccs]);
         }
         __syncwarp();
         ring.next();
@@ -191,7 +177,7 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_const
       const int s = (int)(u % kSlots);
       const float w = sc.weight[s][lane];
 #pragma unroll
-      for (int k = 0; k < 256; k += 32) sc.slot[s][k + lane] *= w;
+      for (int k = 0; k < 64; k += 32) sc.slot[s][k + lane] *= w;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc.full[s]);
     };
@@ -207,7 +193,7 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_const
         ok = wait_warp(&sc.empty[s], (uint32_t)((use / kSlots) & 1) ^ 1u, g.err, &c.abort);
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < 256; k += 32)
+        for (int k = 0; k < 64; k += 32)
           if (k + lane < m.rows) copy_4(&sc.slot[s][k + lane], xs + (int64_t)kb * g.ld_x_scale + k + lane);
         copy_4(&sc.weight[s][lane], ws + kb);
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -221,37 +207,26 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_const
     if (ok)
       for (int64_t u = use < kAhead ? 0 : use - kAhead; u < use; ++u) ready(u);
   } else if (warp >= 4) {
-    // A quarter of the lanes, and every fourth block of 32 columns.
+    // A quarter of the lanes, and one of two blocks of 32 columns.
     const int q = warp & 3, group = (warp - 4) >> 2;
-    constexpr int kBlocks8 = (V::kMaxN + 127) / 128;
-    int use = 0;
+    uint32_t use = 0;
     bool ok = true;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kBM>(t, f_tiles, g.n_experts, off, first);
       const int f = m.f0 + kBM * (int)rank + 32 * q;
-      uint64_t sum[kBlocks8][16];  // pairs
-#pragma unroll
-      for (int i = 0; i < kBlocks8; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) sum[i][k] = 0;
+      f32x2 sum[16] = {};  // pairs
       for (int kb = kb0; kb < kb1; ++kb, ++use) {
-        const int s = use % kSlots;
-        ok = wait_warp(&sc.full[s], (uint32_t)(use / kSlots) & 1u, g.err, &c.abort) && wait_acc(c, use, g.err);
+        const uint32_t s = use % kSlots;
+        ok = wait_warp(&sc.full[s], use / kSlots & 1u, g.err, &c.abort) &&
+             wait_acc<kAccs>(c, use, g.err);
         if (!ok) break;
-        const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)((use & 1) * kAccCols + 32 * group);
-        const float* scales = &sc.slot[s][32 * group];
-#pragma unroll
-        for (int i = 0; i < kBlocks8; ++i) {
-          if ((4 * i + group) * 32 >= m.n) continue;
-#pragma unroll
-          for (int h = 0; h < 32; h += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(at + 128 * i + h, v);
-            tmem_ld_wait();
-            add_block(sum[i], h / 2, v, scales + 128 * i + h);
-          }
+        if (32 * group < m.n) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + use % kAccs * kAccCols + 32u * group, v);
+          tmem_ld_wait();
+          add_block(sum, v, &sc.slot[s][32 * group]);
         }
-        release_acc<V::kPair>(c, use & 1, rank, lane);
+        release_acc<V::kPair>(c, use % kAccs, rank, lane);
         if (lane == 0) mbar_arrive(&sc.empty[s]);
       }
       if (!ok) break;
@@ -261,44 +236,340 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_mm_kernel(const __grid_const
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             reinterpret_cast<float*>(smem)[(q * V::kMaxN + group * 32 + k) * 32 + lane] =
-                k & 1 ? high(sum[0][k / 2]) : low(sum[0][k / 2]);
+                k & 1 ? high(sum[k / 2]) : low(sum[k / 2]);
       } else {
         const int col = f + lane % 4 * 8, inside = g.n - col;
         O* y = static_cast<O*>(g.y) + (int64_t)m.row * g.ldy + col;
-        by_rows<kBlocks8, 8, 4>(
+        by_rows<1, 8, 2>(
             reinterpret_cast<float*>(smem + V::kStages * S::kStage + (warp - 4) * kStaging8), lane, m.rows, group,
-            [&](int i, int k) { return k & 1 ? high(sum[i][k / 2]) : low(sum[i][k / 2]); },
+            [&](int, int k) { return k & 1 ? high(sum[k / 2]) : low(sum[k / 2]); },
             [&](int r, const float (&v)[8]) { store_8(y + r * g.ldy, inside, v); });
       }
     }
     // Rows of no expert.
     const int64_t head = off[0], none = head + g.rows - off[g.n_experts];
     for (int64_t z = blockIdx.x; z < none; z += gridDim.x)
-      Store<O>::template zero_row<kWarps8>(p, z < head ? z : off[g.n_experts] + z - head, (int)threadIdx.x - 128);
+      Store<O>::zero_row(p, z < head ? z : off[g.n_experts] + z - head, (int)threadIdx.x - 128);
   }
   if constexpr (V::kSplit) {
     __syncwarp();
     cluster_sync();
     if (warp >= 4 && unit < tiles)
-      Store<O>::template join<V, kWarps8>(p, mm_tile<V, kBM>(unit, f_tiles, g.n_experts, off, first), part_k, smem);
+      Store<O>::template join<V>(p, mm_tile<V, kBM>(unit, f_tiles, g.n_experts, off, first), part_k, smem);
     __syncwarp();
   }
   teardown<V>(c, warp);
 }
 
+// ---------------------------------------------------------------------------- many rows
+// Tiles of y itself: 128 rows of one expert per CTA (x, operand A) by up to 256 columns (the weight, operand
+// B), on pairs of CTAs (256 rows, half of B each) or single ones.  An accumulator lane is then a row of y
+// and its scale one value of the thread's, where tiles of y^T need one for each column out of shared memory,
+// whose bandwidth the MMAs want for their operands (98304 rows, 1408 -> 2048: 501 us).
+constexpr int kRowWarps = 16;                       // of the epilogue: 64 columns each
+constexpr int kRowThreads = 128 + 32 * kRowWarps;
+constexpr int kRowStage = 2048;                     // bytes of each epilogue warp: 64 bytes of its 32 rows
+constexpr int kGroup = 8;                           // k-blocks whose scales come together
+constexpr int kGroups = 3;
+
+template <bool kPair_>
+struct Rows8 {
+  static constexpr bool kPair = kPair_;
+  static constexpr int kCtas = kPair ? 2 : 1, kTileRows = kBM * kCtas, kTileCols = 256;
+  static constexpr int kStages = kPair ? 5 : 3;
+  static constexpr int kStage = kABytes + kTileCols / kCtas * 128;
+};
+
+struct RowScales {
+  float x[kGroups][kGroup][kBM];
+  float w[kGroups][2][kGroup];  // of the tile's two blocks of 128 columns
+  uint64_t full[kGroups], empty[kGroups];
+};
+
+// The tile's rows row .. row + rows - 1 of expert `expert` and its first column.
+struct RowTile {
+  int expert, row, rows, f0;
+};
+template <int kRows>
+__device__ __forceinline__ RowTile row_tile(uint32_t t, uint32_t f_tiles, int n_experts, const int32_t* off,
+                                            const int32_t* first) {
+  const int rt = (int)(t / f_tiles);
+  int lo = 0, hi = n_experts - 1;  // the expert with first[e] <= rt < first[e + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid + 1] > rt) hi = mid; else lo = mid + 1;
+  }
+  // Groups of 8 row tiles, in each every column tile, in each the group's row tiles (as mm_tile).
+  const uint32_t tiles = (uint32_t)(first[lo + 1] - first[lo]);
+  uint32_t rest = t - (uint32_t)first[lo] * f_tiles;
+  const uint32_t group = rest / (8 * f_tiles) * 8, size = min(8u, tiles - group);
+  rest -= group * f_tiles;
+  const uint32_t f = rest / size, r = group + rest - f * size;
+  RowTile m;
+  m.expert = lo;
+  m.row = off[lo] + (int)(r * kRows);
+  m.rows = min(kRows, off[lo + 1] - m.row);
+  m.f0 = (int)f * 256;
+  return m;
+}
+
+// 16 bytes of results: vectors of O.
+template <typename O>
+__device__ __forceinline__ uint4 pack_16(const f32x2* v) {
+  const float2 a = parts(v[0]), b = parts(v[1]);
+  if constexpr (sizeof(O) == 4) {
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  } else {
+    const float2 c = parts(v[2]), d = parts(v[3]);
+    return make_uint4(pack_2<O>(a.x, a.y), pack_2<O>(b.x, b.y), pack_2<O>(c.x, c.y), pack_2<O>(d.x, d.y));
+  }
+}
+
+template <typename V, typename O>
+__global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_constant__ Fp8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Control c;
+  __shared__ RowScales sc;
+  __shared__ int32_t off[kMaxExperts + 1], first[kMaxExperts + 1];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const Fp8Mm& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = V::kPair ? cluster_ctarank() : 0u;
+  if (threadIdx.x == 96) {
+    prefetch_tmap(&p.w);
+    prefetch_tmap(&p.x);
+  }
+  if (threadIdx.x == 0)
+    for (int s = 0; s < kGroups; ++s) {
+      mbar_init(&sc.full[s], 1);
+      mbar_init(&sc.empty[s], kRowWarps);
+    }
+  setup<V::kPair, kRowWarps>(c, warp);
+  load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
+  if (warp == 3) count_tiles(off, g.n_experts, V::kTileRows, lane, first);
+  __syncthreads();
+  sync_ctas<V::kPair>();
+  const uint32_t tmem = c.tmem;
+  const uint32_t f_tiles = (uint32_t)(g.n - 1) / 256 + 1, tiles = (uint32_t)first[g.n_experts] * f_tiles;
+  const int blocks = (g.k - 1) / kBK8 + 1;
+  const uint32_t unit = blockIdx.x / V::kCtas, units = gridDim.x / V::kCtas;
+  // The MMA's N: the tile's columns in steps of 32.
+  const auto columns = [&](const RowTile& m) { return min(256, (g.n - m.f0 + 31) / 32 * 32); };
+
+  if (warp == 0) {
+    Ring<V::kStages> ring;
+    int64_t fills = 0;
+    bool ok = true;
+    const uint32_t full0 = smem_u32(c.full), dst0 = smem_u32(smem);
+    const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
+      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
+      const int part = columns(m) / V::kCtas;  // columns this CTA brings
+      const int boxes = (part + 63) / 64;
+      const uint32_t bytes = V::kCtas * (kABytes + boxes * kBox);
+      const int f = m.f0 + part * (int)rank, row = (int)((uint32_t)m.row + kBM * rank);
+      for (int kb = 0; kb < blocks; ++kb, ++fills) {
+        ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
+        if (!ok) break;
+        const uint32_t sig = sig0 + 8 * ring.stage, a = dst0 + ring.stage * V::kStage;
+        if (elect_one()) {
+          if (rank == 0) expect(full0 + 8 * ring.stage, bytes);
+          load_2d<V::kPair>(a, &p.x, kb * kBK8, row, sig);
+#pragma unroll
+          for (int b = 0; b < V::kTileCols / V::kCtas / 64; ++b)
+            if (b < boxes) load_3d<V::kPair>(a + kABytes + b * kBox, &p.w, kb * kBK8, f + 64 * b, m.expert, sig);
+        }
+        __syncwarp();
+        ring.next();
+      }
+    }
+    if (elect_one()) drain_ring<V>(c, fills, rank, g.err);
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    Ring<V::kStages> ring;
+    uint32_t use = 0;
+    bool ok = true;
+    const uint32_t a0 = desc_lo(smem_u32(smem), 16), b0 = desc_lo(smem_u32(smem) + kABytes, 16);
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
+      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
+      const uint32_t idesc = idesc_16(false, V::kTileRows, columns(m), 0, 0);  // e4m3 has the same code as fp16
+      for (int kb = 0; kb < blocks; ++kb, ++use) {
+        ok = wait_warp(&c.acc_empty[use & 1], (use >> 1 & 1u) ^ 1u, g.err, &c.abort) &&
+             wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (use & 1) * kAccCols;
+        const uint32_t a = a0 + ring.stage * (V::kStage / 16), b = b0 + ring.stage * (V::kStage / 16);
+        if (elect_one()) {
+          mma<V::kPair, true>(d, a, b, idesc, 0);
+          mma<V::kPair, true>(d, a + 2, b + 2, idesc, 1);
+          mma<V::kPair, true>(d, a + 4, b + 4, idesc, 1);
+          mma<V::kPair, true>(d, a + 6, b + 6, idesc, 1);
+          commit<V::kPair>(&c.acc_full[use & 1]);
+          commit<V::kPair>(&c.empty[ring.stage]);
+        }
+        __syncwarp();
+        ring.next();
+      }
+    }
+    if (elect_one()) {
+      if constexpr (V::kPair) tc_commit_pair(&c.mma_done, (uint16_t)0x1);
+      else tc_commit(&c.mma_done);
+      drain(&c.mma_done, 0, g.err);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // Scales, kGroup k-blocks at a time.  A group is handed over when the next one has been asked for.
+    uint32_t use = 0;
+    bool ok = true;
+    const auto ready = [&](uint32_t u) {
+      __syncwarp();  // every lane's copies have landed
+      if (lane == 0) mbar_arrive(&sc.full[u % kGroups]);
+    };
+    const int64_t n_blocks = (g.n - 1) / 128 + 1;
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
+      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
+      const float* xs = g.x_scale + m.row + kBM * (int64_t)rank;
+      const int rows = m.rows - kBM * (int)rank;
+      for (int kb = 0; kb < blocks; kb += kGroup, ++use) {
+        const uint32_t s = use % kGroups;
+        ok = wait_warp(&sc.empty[s], (use / kGroups & 1u) ^ 1u, g.err, &c.abort);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+          if (kb + i < blocks)
+#pragma unroll
+            for (int r = 0; r < kBM; r += 32)
+              if (r + lane < rows) copy_4(&sc.x[s][i][r + lane], xs + (int64_t)(kb + i) * g.ld_x_scale + r + lane);
+        const int half = lane / kGroup, b = lane % kGroup;
+        if (half < 2 && kb + b < blocks && m.f0 / 128 + half < n_blocks)
+          copy_4(&sc.w[s][half][b], g.w_scale + ((int64_t)m.expert * n_blocks + m.f0 / 128 + half) * blocks + kb + b);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (use > 0) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          ready(use - 1);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (ok && use > 0) ready(use - 1);
+  } else if (warp >= 4) {
+    const int q = warp & 3, group = (warp - 4) >> 2;  // a quarter of the lanes, 64 columns
+    uint4* stage = reinterpret_cast<uint4*>(smem + V::kStages * V::kStage + (warp - 4) * kRowStage);
+    uint32_t use = 0, groups = 0;
+    bool ok = true;
+    for (uint32_t t = unit; t < tiles && ok; t += units) {
+      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
+      const bool on = 64 * group < columns(m);
+      f32x2 sum[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) sum[k] = 0;
+      for (int kb = 0; kb < blocks; ++kb, ++use) {
+        const int i = kb % kGroup;
+        const uint32_t s = groups % kGroups;
+        if (i == 0) ok = wait_warp(&sc.full[s], groups / kGroups & 1u, g.err, &c.abort);
+        ok = ok && wait_acc(c, use, g.err);
+        if (!ok) break;
+        if (on) {
+          const float scale = sc.x[s][i][32 * q + lane] * sc.w[s][group / 2][i];
+          const f32x2 both = pair(scale, scale);
+          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 64u * group;
+#pragma unroll
+          for (int h = 0; h < 64; h += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(at + h, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; k += 2)
+              sum[(h + k) / 2] =
+                  fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), both, sum[(h + k) / 2]);
+          }
+        }
+        release_acc<V::kPair>(c, use & 1, rank, lane);
+        if (i == kGroup - 1 || kb == blocks - 1) {
+          if (lane == 0) mbar_arrive(&sc.empty[s]);
+          ++groups;
+        }
+      }
+      if (!ok) break;
+      if (!on) continue;
+      // 64 bytes of the warp's 32 rows at a time, so that a store covers whole sectors of 8 rows: 16-byte
+      // chunk c of row r stands in slot c ^ (r / 2 % 4), free of bank conflicts.
+      constexpr int kValues = 16 / (int)sizeof(O), kPasses = 64 / (4 * kValues);
+      const int left = m.rows - kBM * (int)rank - 32 * q;
+      O* y = static_cast<O*>(g.y) + ((int64_t)m.row + kBM * (int)rank + 32 * q) * g.ldy;
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass) {
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+          stage[4 * lane + (ch ^ (lane >> 1 & 3))] = pack_16<O>(&sum[(pass * 4 + ch) * kValues / 2]);
+        __syncwarp();
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+          const int r = r0 + lane / 4, ch = lane % 4;
+          const uint4 v = stage[4 * r + (ch ^ (r >> 1 & 3))];
+          const int col = m.f0 + 64 * group + (pass * 4 + ch) * kValues, inside = g.n - col;
+          if (r >= left || inside <= 0) continue;
+          O* at = y + r * g.ldy + col;
+          if (inside >= kValues && reinterpret_cast<uintptr_t>(at) % 16 == 0) {
+            *reinterpret_cast<uint4*>(at) = v;
+          } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < kValues; ++k) {
+              if (k >= inside) break;
+              if constexpr (sizeof(O) == 4) reinterpret_cast<uint32_t*>(at)[k] = w[k];
+              else reinterpret_cast<uint16_t*>(at)[k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+            }
+          }
+        }
+      }
+    }
+    // Rows of no expert.
+    const int64_t head = off[0], none = head + g.rows - off[g.n_experts];
+    for (int64_t z = blockIdx.x; z < none; z += gridDim.x)
+      Store<O>::template zero_row<kRowWarps>(p, z < head ? z : off[g.n_experts] + z - head,
+                                             (int)threadIdx.x - 128);
+  }
+  sync_ctas<V::kPair>();
+  if (warp == 2) {
+    if constexpr (V::kPair) tmem_dealloc_pair(tmem, kTmemCols);
+    else tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// At least as many tiles as the offsets can make of the rows.
+template <typename V>
+int64_t row_tiles(const GroupedMm& g) {
+  return (g.rows / V::kTileRows + (g.rows < g.n_experts ? g.rows : g.n_experts)) *
+         (((int64_t)g.n - 1) / 256 + 1);
+}
+
+template <typename V, typename O>
+cudaError_t launch_rows(const Fp8Params& p, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  return launch(fp8_rows_kernel<V, O>, p, row_tiles<V>(p.g), V::kCtas, sms,
+                V::kStages * V::kStage + kRowWarps * kRowStage + 1024, &ready, st, kRowThreads);
+}
+
 template <typename V, typename O>
 cudaError_t launch_as(const Fp8Params& p, int parts, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  return launch(fp8_mm_kernel<V, O>, p, mm_tiles<V>(p.g), Shape<V>::kCtas * parts, sms,
-                V::kStages * Shape<V>::kStage + (V::kSplit ? 0 : kWarps8 * kStaging8) + 1024, &ready, st,
-                kThreads8);
+  return launch(fp8_mm_kernel<V, O>, p, mm_tiles<V>(p.g), parts, sms,
+                V::kStages * Shape<V>::kStage + (V::kSplit ? 0 : kEpiWarps * kStaging8) + 1024, &ready, st);
 }
 
+struct Fp8Choice {
+  int parts;
+  bool narrow, pair;
+};
+
 template <typename O>
-cudaError_t launch_type(const Fp8Params& p, const MmChoice& c, int sms, cudaStream_t st) {
+cudaError_t launch_type(const Fp8Params& p, const Fp8Choice& c, int sms, cudaStream_t st) {
   return c.parts > 1 ? launch_as<Split8, O>(p, c.parts, sms, st)
          : c.narrow  ? launch_as<Narrow8, O>(p, 1, sms, st)
-         : c.pair    ? launch_as<Pair8, O>(p, 1, sms, st) : launch_as<Wide8, O>(p, 1, sms, st);
+         : c.pair    ? launch_rows<Rows8<true>, O>(p, sms, st) : launch_rows<Rows8<false>, O>(p, sms, st);
 }
 
 }  // namespace
@@ -310,13 +581,14 @@ cudaError_t launch_fp8_mm(const Fp8Mm& g, int sms, cudaStream_t st) {
   const int64_t line = ((int64_t)g.k + 15) / 16 * 16;
   const Operand x{g.x, g.rows, g.k, g.rows == 1 ? line : g.ldx, 1, 0};
   const Operand w{g.w, g.n, g.k, g.n == 1 ? line : g.ldw, g.n_experts, g.w_stride};
-  MmChoice c{1, false, false};
+  Fp8Choice c{1, false, false};
   while (c.parts < kMostParts && mm_tiles<Split8>(g) * c.parts * 2 <= sms && g.k >= 4 * kBK8 * c.parts * 2)
     c.parts *= 2;
   c.narrow = g.rows <= Narrow8::kMaxN * (int64_t)g.n_experts || mm_tiles<Narrow8>(g) <= sms;
-  c.pair = !c.narrow && g.n > kBM && mm_tiles<Pair8>(g) >= sms;
-  cudaError_t e = encode(&p.x, x, kE4m3, false, c.box_rows());
-  if (e == cudaSuccess) e = encode(&p.w, w, kE4m3, true, kBM);
+  c.pair = !c.narrow && row_tiles<Rows8<true>>(g) * 2 >= sms;
+  const bool few = c.parts > 1 || c.narrow;
+  cudaError_t e = encode(&p.x, x, kE4m3, false, few ? Narrow8::kBoxRows : kBM);
+  if (e == cudaSuccess) e = encode(&p.w, w, kE4m3, true, few ? kBM : 64);
   if (e != cudaSuccess) return e;
   return g.out_dtype == kF32 ? launch_type<float>(p, c, sms, st)
          : g.out_dtype == kBf16 ? launch_type<__nv_bfloat16>(p, c, sms, st)

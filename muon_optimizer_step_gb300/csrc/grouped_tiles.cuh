@@ -19,7 +19,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kBM = 128;            // rows of operand A: M of the MMA
 constexpr int kABytes = kBM * 128;  // 16 KB
 constexpr int kBox = 64 * 128;      // an MN-major box: 64 k-rows of 128 bytes
-constexpr int kAccCols = 256;       // TMEM columns of one accumulator
+constexpr int kTmemCols = 512;
+constexpr int kAccCols = 256;       // TMEM columns of one accumulator, of two
+constexpr int kMostAccs = 4;
 constexpr int kMaxStages = 6;
 constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 
@@ -83,7 +85,7 @@ struct Control {
   // wgrad on pairs, last stage of a tile: the second CTA's own operands have landed, and it
   // has zeroed the rows that are not its expert's.
   uint64_t tail[kMaxStages], fixed[kMaxStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[kMostAccs], acc_empty[kMostAccs];
   uint64_t mma_done;
   uint32_t tmem;
   int abort;
@@ -248,7 +250,7 @@ __device__ __forceinline__ void setup(Control& c, int warp) {
       mbar_init(&c.tail[s], 1);
       mbar_init(&c.fixed[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kMostAccs; ++b) {
       mbar_init(&c.acc_full[b], 1);
       mbar_init(&c.acc_empty[b], (kPair ? 2 : 1) * kWarps);
     }
@@ -258,10 +260,10 @@ __device__ __forceinline__ void setup(Control& c, int warp) {
   }
   if (warp == 2) {
     if constexpr (kPair) {
-      tmem_alloc_pair(&c.tmem, 2 * kAccCols);
+      tmem_alloc_pair(&c.tmem, kTmemCols);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(&c.tmem, 2 * kAccCols);
+      tmem_alloc(&c.tmem, kTmemCols);
       tmem_relinquish();
     }
   }
@@ -280,8 +282,8 @@ template <typename V>
 __device__ __forceinline__ void teardown(Control& c, int warp) {
   sync_ctas<V::kPair || V::kSplit>();
   if (warp == 2) {
-    if constexpr (V::kPair) tmem_dealloc_pair(c.tmem, 2 * kAccCols);
-    else tmem_dealloc(c.tmem, 2 * kAccCols);
+    if constexpr (V::kPair) tmem_dealloc_pair(c.tmem, kTmemCols);
+    else tmem_dealloc(c.tmem, kTmemCols);
   }
 }
 
@@ -298,9 +300,10 @@ __device__ __forceinline__ void release_acc(Control& c, int ab, uint32_t rank, i
   }
 }
 
-// Waits for accumulator use number `use` (epilogue warp).
-__device__ __forceinline__ bool wait_acc(Control& c, int use, int* err) {
-  if (!wait_warp(&c.acc_full[use & 1], (use >> 1) & 1, err, &c.abort)) return false;
+// Waits for accumulator use number `use`, one of kAccs in turn (epilogue warp).
+template <uint32_t kAccs = 2>
+__device__ __forceinline__ bool wait_acc(Control& c, uint32_t use, int* err) {
+  if (!wait_warp(&c.acc_full[use % kAccs], use / kAccs & 1u, err, &c.abort)) return false;
   tc_fence_after();
   return true;
 }
