@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 // B), on pairs of CTAs (256 rows, half of B each) or single ones.  An accumulator lane is then a row of y
 // and its scale one value of the thread's, where tiles of y^T need one for each column out of shared memory,
 // whose bandwidth the MMAs want for their operands (98304 rows, 1408 -> 2048: 501 us).
-constexpr int kRowWarps = 16;                       // of the epilogue: 64 columns each
+constexpr int kRowWarps = 8;                        // of the epilogue: a block of 128 columns each
 constexpr int kRowThreads = 128 + 32 * kRowWarps;
 constexpr int kRowStage = 2048;                     // bytes of each epilogue warp: 64 bytes of its 32 rows
 constexpr int kGroup = 8;                           // k-blocks whose scales come together
@@ -288,29 +288,25 @@ struct RowScales {
 
 // The tile's rows row .. row + rows - 1 of expert `expert` and its first column.
 struct RowTile {
-  int expert, row, rows, f0;
+  int expert = 0, row, rows, f0;
 };
+// Tiles are asked for in ascending order: the search for the expert goes on from the last one's.
 template <int kRows>
-__device__ __forceinline__ RowTile row_tile(uint32_t t, uint32_t f_tiles, int n_experts, const int32_t* off,
-                                            const int32_t* first) {
+__device__ __forceinline__ void row_tile(RowTile& m, uint32_t t, uint32_t f_tiles, const int32_t* off,
+                                         const int32_t* first) {
   const int rt = (int)(t / f_tiles);
-  int lo = 0, hi = n_experts - 1;  // the expert with first[e] <= rt < first[e + 1]
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid + 1] > rt) hi = mid; else lo = mid + 1;
-  }
+  int lo = m.expert;  // first[lo] <= rt < first[lo + 1]
+  while (first[lo + 1] <= rt) ++lo;
   // Groups of 8 row tiles, in each every column tile, in each the group's row tiles (as mm_tile).
   const uint32_t tiles = (uint32_t)(first[lo + 1] - first[lo]);
   uint32_t rest = t - (uint32_t)first[lo] * f_tiles;
   const uint32_t group = rest / (8 * f_tiles) * 8, size = min(8u, tiles - group);
   rest -= group * f_tiles;
   const uint32_t f = rest / size, r = group + rest - f * size;
-  RowTile m;
   m.expert = lo;
   m.row = off[lo] + (int)(r * kRows);
   m.rows = min(kRows, off[lo + 1] - m.row);
   m.f0 = (int)f * 256;
-  return m;
 }
 
 // 16 bytes of results: vectors of O.
@@ -362,8 +358,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
     bool ok = true;
     const uint32_t full0 = smem_u32(c.full), dst0 = smem_u32(smem);
     const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
+    RowTile m;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
-      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
+      row_tile<V::kTileRows>(m, t, f_tiles, off, first);
       const int part = columns(m) / V::kCtas;  // columns this CTA brings
       const int boxes = (part + 63) / 64;
       const uint32_t bytes = V::kCtas * (kABytes + boxes * kBox);
@@ -390,8 +387,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
     uint32_t use = 0;
     bool ok = true;
     const uint32_t a0 = desc_lo(smem_u32(smem), 16), b0 = desc_lo(smem_u32(smem) + kABytes, 16);
+    RowTile m;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
-      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
+      row_tile<V::kTileRows>(m, t, f_tiles, off, first);
       const uint32_t idesc = idesc_16(false, V::kTileRows, columns(m), 0, 0);  // e4m3 has the same code as fp16
       for (int kb = 0; kb < blocks; ++kb, ++use) {
         ok = wait_warp(&c.acc_empty[use & 1], (use >> 1 & 1u) ^ 1u, g.err, &c.abort) &&
@@ -427,8 +425,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&sc.full[u % kGroups]);
     };
     const int64_t n_blocks = (g.n - 1) / 128 + 1;
+    RowTile m;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
-      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
+      row_tile<V::kTileRows>(m, t, f_tiles, off, first);
       const float* xs = g.x_scale + m.row + kBM * (int64_t)rank;
       const int rows = m.rows - kBM * (int)rank;
       for (int kb = 0; kb < blocks; kb += kGroup, ++use) {
@@ -454,16 +453,17 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (ok && use > 0) ready(use - 1);
   } else if (warp >= 4) {
-    const int q = warp & 3, group = (warp - 4) >> 2;  // a quarter of the lanes, 64 columns
+    const int q = warp & 3, half = (warp - 4) >> 2;  // a quarter of the lanes, 128 columns
     uint4* stage = reinterpret_cast<uint4*>(smem + V::kStages * V::kStage + (warp - 4) * kRowStage);
     uint32_t use = 0, groups = 0;
     bool ok = true;
+    RowTile m;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
-      const RowTile m = row_tile<V::kTileRows>(t, f_tiles, g.n_experts, off, first);
-      const bool on = 64 * group < columns(m);
-      f32x2 sum[32];
+      row_tile<V::kTileRows>(m, t, f_tiles, off, first);
+      const bool on = 128 * half < columns(m);
+      f32x2 sum[64];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) sum[k] = 0;
+      for (int k = 0; k < 64; ++k) sum[k] = 0;
       for (int kb = 0; kb < blocks; ++kb, ++use) {
         const int i = kb % kGroup;
         const uint32_t s = groups % kGroups;
@@ -471,18 +471,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
         ok = ok && wait_acc(c, use, g.err);
         if (!ok) break;
         if (on) {
-          const float scale = sc.x[s][i][32 * q + lane] * sc.w[s][group / 2][i];
+          const float scale = sc.x[s][i][32 * q + lane] * sc.w[s][half][i];
           const f32x2 both = pair(scale, scale);
-          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 64u * group;
+          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 128u * half;
+          // The next 16 columns arrive while these are added.
+          uint32_t v[2][16];
+          tmem_ld_32x32b_x16(at, v[0]);
 #pragma unroll
-          for (int h = 0; h < 64; h += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(at + h, v);
+          for (int h = 0; h < 8; ++h) {
             tmem_ld_wait();
+            if (h < 7) tmem_ld_32x32b_x16(at + 16 * (h + 1), v[(h + 1) & 1]);
+            const uint32_t (&now)[16] = v[h & 1];
 #pragma unroll
             for (int k = 0; k < 16; k += 2)
-              sum[(h + k) / 2] =
-                  fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), both, sum[(h + k) / 2]);
+              sum[8 * h + k / 2] =
+                  fma2(pair(__uint_as_float(now[k]), __uint_as_float(now[k + 1])), both, sum[8 * h + k / 2]);
           }
         }
         release_acc<V::kPair>(c, use & 1, rank, lane);
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
       if (!on) continue;
       // 64 bytes of the warp's 32 rows at a time, so that a store covers whole sectors of 8 rows: 16-byte
       // chunk c of row r stands in slot c ^ (r / 2 % 4), free of bank conflicts.
-      constexpr int kValues = 16 / (int)sizeof(O), kPasses = 64 / (4 * kValues);
+      constexpr int kValues = 16 / (int)sizeof(O), kPasses = 128 / (4 * kValues);
       const int left = m.rows - kBM * (int)rank - 32 * q;
       O* y = static_cast<O*>(g.y) + ((int64_t)m.row + kBM * (int)rank + 32 * q) * g.ldy;
 #pragma unroll
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
         for (int r0 = 0; r0 < 32; r0 += 8) {
           const int r = r0 + lane / 4, ch = lane % 4;
           const uint4 v = stage[4 * r + (ch ^ (r >> 1 & 3))];
-          const int col = m.f0 + 64 * group + (pass * 4 + ch) * kValues, inside = g.n - col;
+          const int col = m.f0 + 128 * half + (pass * 4 + ch) * kValues, inside = g.n - col;
           if (r >= left || inside <= 0) continue;
           O* at = y + r * g.ldy + col;
           if (inside >= kValues && reinterpret_cast<uintptr_t>(at) % 16 == 0) {
