@@ -4,15 +4,15 @@
 //   y[r, c] = sum over the blocks b of 128 along k of
 //             x_scale[b][r] w_scale[e][c / 128][b] (sum over b's k of x[r, k] w_e[c, k])
 //
-// Tiles of y^T as in the grouped products of 16-bit operands (see grouped_mm.cu): 128 columns of y (the
-// weight, operand A) by up to kMaxN rows of one expert, on single CTAs or pairs.  A k-block is 128 bytes
-// of a row, that is one block of the scales: each is an accumulator of its own, and the epilogue warps add
-// it to the sums in registers, times the scale of its row of y (an accumulator column) and the weight's (the
-// same for the whole tile).  So every 128 terms are summed in the tensor core, the blocks in fp32 with
-// rounding to nearest.
+// A k-block is 128 bytes of a row, one block of the scales: each is an accumulator of its own (two in turn), and
+// the epilogue warps add it to the sums in registers, times its row's scale and the weight's.  So every 128 terms
+// are summed in the tensor core, the blocks in fp32 with rounding to nearest.
 //
-// Warp 3 brings the scales: a ring of slots in shared memory, each with a k-block's scales of the tile's
-// rows, loaded several k-blocks ahead (cp.async) and multiplied by the weight's when they are there.
+// Few rows per expert: tiles of y^T as in the grouped products of 16-bit operands (see grouped_mm.cu), 128
+// columns of y (the weight, operand A) by up to 64 rows of one expert, or a cluster of CTAs that share the
+// k-blocks of one.  Streaming the weight bounds them.  Many: tiles of y, below.
+//
+// Warp 3 brings the scales into a ring of slots in shared memory, several k-blocks ahead (cp.async).
 #include "grouped_kernel.cuh"
 
 namespace muon {
@@ -22,11 +22,11 @@ namespace {
 constexpr int kBK8 = 128;   // elements of a k-block: 128 bytes
 constexpr int kSlots = 8;   // of scales
 constexpr int kAhead = 6;   // k-blocks that scales are asked for ahead
-constexpr uint32_t kAccs = 2;
 constexpr int kStaging8 = 1024;          // bytes of each epilogue warp: 8 rows of its 32 columns
 
 struct Fp8Params {
-  CUtensorMap x, w;  // (k, rows): boxes of 128 x kBoxRows; (k, columns of y, expert): 128 x 128
+  CUtensorMap x, w;  // (k, rows) and (k, columns of y, expert): boxes of 128 x 16 and 128 x 128, or (tiles
+                     // of y) 128 x 128 and 128 x 64
   Fp8Mm g;
 };
 
@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const Fp8Mm& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = V::kPair ? cluster_ctarank() : 0u;
   const Part part_k = split_part<V>();
   if (threadIdx.x == 96) {
     prefetch_tmap(&p.w);
@@ -86,16 +85,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
       mbar_init(&sc.full[s], 1);
       mbar_init(&sc.empty[s], kEpiWarps);
     }
-  setup<V::kPair>(c, warp);
+  setup<false>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kMaxN, lane, first);
   __syncthreads();
-  sync_ctas<V::kPair>();
+  sync_ctas<false>();
   const uint32_t tmem = c.tmem;
   const uint32_t f_tiles = (uint32_t)(g.n - 1) / S::kM + 1, tiles = (uint32_t)first[g.n_experts] * f_tiles;
   const int blocks = (g.k - 1) / kBK8 + 1;
   int kb0 = 0, kb1 = blocks;  // this CTA's k-blocks
-  uint32_t unit = blockIdx.x / S::kCtas, units = gridDim.x / S::kCtas;
+  uint32_t unit = blockIdx.x, units = gridDim.x;
   if constexpr (V::kSplit) {
     const int shift = 31 - __clz(part_k.parts);  // parts is a power of two
     kb0 = (int)((int64_t)blocks * part_k.index >> shift);
@@ -109,33 +108,30 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     int64_t fills = 0;
     bool ok = true;
     const uint32_t full0 = smem_u32(c.full), dst0 = smem_u32(smem);
-    const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kBM>(t, f_tiles, g.n_experts, off, first);
-      const int part = m.n / S::kCtas;  // rows of x this CTA brings
-      const int boxes = (part + V::kBoxRows - 1) / V::kBoxRows;
-      const uint32_t bytes = S::kCtas * (kABytes + boxes * V::kBoxRows * 128);
-      const int f = m.f0 + kBM * (int)rank, row = (int)((uint32_t)m.row + part * rank);
+      const int boxes = (m.n + V::kBoxRows - 1) / V::kBoxRows;
+      const uint32_t bytes = kABytes + boxes * V::kBoxRows * 128;
       for (int kb = kb0; kb < kb1; ++kb, ++fills) {
         ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
         if (!ok) break;
-        const uint32_t sig = sig0 + 8 * ring.stage, a = dst0 + ring.stage * S::kStage;
+        const uint32_t sig = full0 + 8 * ring.stage, a = dst0 + ring.stage * S::kStage;
         if (elect_one()) {
-          if (rank == 0) expect(full0 + 8 * ring.stage, bytes);
-          load_3d<V::kPair>(a, &p.w, kb * kBK8, f, m.expert, sig);
+          expect(sig, bytes);
+          load_3d<false>(a, &p.w, kb * kBK8, m.f0, m.expert, sig);
 #pragma unroll
-          for (int b = 0; b < V::kMaxN / S::kCtas / V::kBoxRows; ++b)
+          for (int b = 0; b < V::kMaxN / V::kBoxRows; ++b)
             if (b < boxes)
-              load_2d<V::kPair>(a + kABytes + b * V::kBoxRows * 128, &p.x, kb * kBK8,
-                                (int)((uint32_t)row + b * V::kBoxRows), sig);
+              load_2d<false>(a + kABytes + b * V::kBoxRows * 128, &p.x, kb * kBK8,
+                             (int)((uint32_t)m.row + b * V::kBoxRows), sig);
         }
         __syncwarp();
         ring.next();
       }
     }
-    if (elect_one()) drain_ring<V>(c, fills, rank, g.err);
+    if (elect_one()) drain_ring<V>(c, fills, 0, g.err);
     __syncwarp();
-  } else if (warp == 1 && rank == 0) {
+  } else if (warp == 1) {
     Ring<V::kStages> ring;
     uint32_t use = 0;
     bool ok = true;
@@ -144,28 +140,27 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
       const MmTile m = mm_tile<V, kBM>(t, f_tiles, g.n_experts, off, first);
       const uint32_t idesc = idesc_16(false, S::kM, m.n, 0, 0);  // e4m3 has the same code as fp16
       for (int kb = kb0; kb < kb1; ++kb, ++use) {
-        ok = wait_warp(&c.acc_empty[use % kAccs], (use / kAccs & 1u) ^ 1u, g.err, &c.abort) &&
+        ok = wait_warp(&c.acc_empty[use & 1], (use >> 1 & 1u) ^ 1u, g.err, &c.abort) &&
              wait_warp(&c.full[ring.stage], ring.phase, g.err, &c.abort);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + use % kAccs * kAccCols;
+        const uint32_t d = tmem + (use & 1) * kAccCols;
         const uint32_t a = a0 + ring.stage * (S::kStage / 16), b = b0 + ring.stage * (S::kStage / 16);
         if (elect_one()) {
           // K = 32 each; columns past k are zeros in both operands.
-          mma<V::kPair, true>(d, a, b, idesc, 0);
-          mma<V::kPair, true>(d, a + 2, b + 2, idesc, 1);
-          mma<V::kPair, true>(d, a + 4, b + 4, idesc, 1);
-          mma<V::kPair, true>(d, a + 6, b + 6, idesc, 1);
-          commit<V::kPair>(&c.empty[ring.stage]);
-          commit<V::kPair>(&c.acc_full[use % kAccs]);
+          mma<false, true>(d, a, b, idesc, 0);
+          mma<false, true>(d, a + 2, b + 2, idesc, 1);
+          mma<false, true>(d, a + 4, b + 4, idesc, 1);
+          mma<false, true>(d, a + 6, b + 6, idesc, 1);
+          commit<false>(&c.empty[ring.stage]);
+          commit<false>(&c.acc_full[use & 1]);
         }
         __syncwarp();
         ring.next();
       }
     }
     if (elect_one()) {
-      if constexpr (V::kPair) tc_commit_pair(&c.mma_done, (uint16_t)0x1);
-      else tc_commit(&c.mma_done);
+      tc_commit(&c.mma_done);
       drain(&c.mma_done, 0, g.err);
     }
     __syncwarp();
@@ -183,10 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     };
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kBM>(t, f_tiles, g.n_experts, off, first);
-      const int f = m.f0 + kBM * (int)rank;
-      const int64_t n_blocks = (g.n - 1) / 128 + 1;
-      // (A pair's second CTA may have no columns: any scale will do.)
-      const float* ws = g.w_scale + ((int64_t)m.expert * n_blocks + (f < g.n ? f / 128 : 0)) * blocks;
+      const float* ws = g.w_scale + ((int64_t)m.expert * ((g.n - 1) / 128 + 1) + m.f0 / 128) * blocks;
       const float* xs = g.x_scale + m.row;
       for (int kb = kb0; kb < kb1; ++kb, ++use) {
         const int s = (int)(use % kSlots);
@@ -213,20 +205,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     bool ok = true;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kBM>(t, f_tiles, g.n_experts, off, first);
-      const int f = m.f0 + kBM * (int)rank + 32 * q;
+      const int f = m.f0 + 32 * q;
       f32x2 sum[16] = {};  // pairs
       for (int kb = kb0; kb < kb1; ++kb, ++use) {
         const uint32_t s = use % kSlots;
         ok = wait_warp(&sc.full[s], use / kSlots & 1u, g.err, &c.abort) &&
-             wait_acc<kAccs>(c, use, g.err);
+             wait_acc(c, use, g.err);
         if (!ok) break;
         if (32 * group < m.n) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + use % kAccs * kAccCols + 32u * group, v);
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 32u * group, v);
           tmem_ld_wait();
           add_block(sum, v, &sc.slot[s][32 * group]);
         }
-        release_acc<V::kPair>(c, use % kAccs, rank, lane);
+        release_acc<false>(c, use & 1, 0, lane);
         if (lane == 0) mbar_arrive(&sc.empty[s]);
       }
       if (!ok) break;
@@ -262,22 +254,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------- many rows
-// Tiles of y itself: 128 rows of one expert per CTA (x, operand A) by up to 256 columns (the weight, operand
-// B), on pairs of CTAs (256 rows, half of B each) or single ones.  An accumulator lane is then a row of y
-// and its scale one value of the thread's, where tiles of y^T need one for each column out of shared memory,
-// whose bandwidth the MMAs want for their operands (98304 rows, 1408 -> 2048: 501 us).
-constexpr int kRowWarps = 8;                        // of the epilogue: a block of 128 columns each
-constexpr int kRowThreads = 128 + 32 * kRowWarps;
-constexpr int kRowStage = 2048;                     // bytes of each epilogue warp: 64 bytes of its 32 rows
-constexpr int kGroup = 8;                           // k-blocks whose scales come together
+// Tiles of y itself: 128 rows of one expert (x, operand A) by up to 256 columns (the weight, operand B).  An
+// accumulator lane is then a row of y and its scale one value of the thread's, where tiles of y^T need one
+// for each column out of shared memory, whose bandwidth the MMAs want for their operands (98304 rows,
+// 1408 -> 2048: 501 us with those, 338 with these).  Adding up the accumulators bounds them: of 0.76 us for a
+// k-block 0.27 are its MMAs (bare, with the waits for them, 0.53).  On pairs of CTAs the same takes 364 us, as
+// a k-block waits for two epilogues.
+constexpr int kRowStage = 2048;  // bytes of each epilogue warp: 64 bytes of its 32 rows
+constexpr int kGroup = 8;        // k-blocks whose scales come together
 constexpr int kGroups = 3;
 
-template <bool kPair_>
 struct Rows8 {
-  static constexpr bool kPair = kPair_;
-  static constexpr int kCtas = kPair ? 2 : 1, kTileRows = kBM * kCtas, kTileCols = 256;
-  static constexpr int kStages = kPair ? 5 : 3;
-  static constexpr int kStage = kABytes + kTileCols / kCtas * 128;
+  static constexpr int kTileRows = kBM, kTileCols = 256, kStages = 3;
+  static constexpr int kStage = kABytes + kTileCols * 128;
 };
 
 struct RowScales {
@@ -321,8 +310,9 @@ __device__ __forceinline__ uint4 pack_16(const f32x2* v) {
   }
 }
 
-template <typename V, typename O>
-__global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_constant__ Fp8Params p) {
+template <typename O>
+__global__ void __launch_bounds__(kThreads, 1) fp8_rows_kernel(const __grid_constant__ Fp8Params p) {
+  using V = Rows8;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control c;
   __shared__ RowScales sc;
@@ -330,7 +320,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const Fp8Mm& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = V::kPair ? cluster_ctarank() : 0u;
   if (threadIdx.x == 96) {
     prefetch_tmap(&p.w);
     prefetch_tmap(&p.x);
@@ -338,17 +327,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
   if (threadIdx.x == 0)
     for (int s = 0; s < kGroups; ++s) {
       mbar_init(&sc.full[s], 1);
-      mbar_init(&sc.empty[s], kRowWarps);
+      mbar_init(&sc.empty[s], kEpiWarps);
     }
-  setup<V::kPair, kRowWarps>(c, warp);
+  setup<false>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kTileRows, lane, first);
   __syncthreads();
-  sync_ctas<V::kPair>();
+  sync_ctas<false>();
   const uint32_t tmem = c.tmem;
   const uint32_t f_tiles = (uint32_t)(g.n - 1) / 256 + 1, tiles = (uint32_t)first[g.n_experts] * f_tiles;
   const int blocks = (g.k - 1) / kBK8 + 1;
-  const uint32_t unit = blockIdx.x / V::kCtas, units = gridDim.x / V::kCtas;
   // The MMA's N: the tile's columns in steps of 32.
   const auto columns = [&](const RowTile& m) { return min(256, (g.n - m.f0 + 31) / 32 * 32); };
 
@@ -357,38 +345,34 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
     int64_t fills = 0;
     bool ok = true;
     const uint32_t full0 = smem_u32(c.full), dst0 = smem_u32(smem);
-    const uint32_t sig0 = V::kPair ? mapa_shared(full0, 0) : full0;
     RowTile m;
-    for (uint32_t t = unit; t < tiles && ok; t += units) {
+    for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       row_tile<V::kTileRows>(m, t, f_tiles, off, first);
-      const int part = columns(m) / V::kCtas;  // columns this CTA brings
-      const int boxes = (part + 63) / 64;
-      const uint32_t bytes = V::kCtas * (kABytes + boxes * kBox);
-      const int f = m.f0 + part * (int)rank, row = (int)((uint32_t)m.row + kBM * rank);
+      const int boxes = (columns(m) + 63) / 64;
       for (int kb = 0; kb < blocks; ++kb, ++fills) {
         ok = wait_warp(&c.empty[ring.stage], ring.phase ^ 1u, g.err, &c.abort);
         if (!ok) break;
-        const uint32_t sig = sig0 + 8 * ring.stage, a = dst0 + ring.stage * V::kStage;
+        const uint32_t sig = full0 + 8 * ring.stage, a = dst0 + ring.stage * V::kStage;
         if (elect_one()) {
-          if (rank == 0) expect(full0 + 8 * ring.stage, bytes);
-          load_2d<V::kPair>(a, &p.x, kb * kBK8, row, sig);
+          expect(sig, kABytes + boxes * kBox);
+          load_2d<false>(a, &p.x, kb * kBK8, m.row, sig);
 #pragma unroll
-          for (int b = 0; b < V::kTileCols / V::kCtas / 64; ++b)
-            if (b < boxes) load_3d<V::kPair>(a + kABytes + b * kBox, &p.w, kb * kBK8, f + 64 * b, m.expert, sig);
+          for (int b = 0; b < V::kTileCols / 64; ++b)
+            if (b < boxes) load_3d<false>(a + kABytes + b * kBox, &p.w, kb * kBK8, m.f0 + 64 * b, m.expert, sig);
         }
         __syncwarp();
         ring.next();
       }
     }
-    if (elect_one()) drain_ring<V>(c, fills, rank, g.err);
+    if (elect_one()) drain_ring<V>(c, fills, 0, g.err);
     __syncwarp();
-  } else if (warp == 1 && rank == 0) {
+  } else if (warp == 1) {
     Ring<V::kStages> ring;
     uint32_t use = 0;
     bool ok = true;
     const uint32_t a0 = desc_lo(smem_u32(smem), 16), b0 = desc_lo(smem_u32(smem) + kABytes, 16);
     RowTile m;
-    for (uint32_t t = unit; t < tiles && ok; t += units) {
+    for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       row_tile<V::kTileRows>(m, t, f_tiles, off, first);
       const uint32_t idesc = idesc_16(false, V::kTileRows, columns(m), 0, 0);  // e4m3 has the same code as fp16
       for (int kb = 0; kb < blocks; ++kb, ++use) {
@@ -399,20 +383,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
         const uint32_t d = tmem + (use & 1) * kAccCols;
         const uint32_t a = a0 + ring.stage * (V::kStage / 16), b = b0 + ring.stage * (V::kStage / 16);
         if (elect_one()) {
-          mma<V::kPair, true>(d, a, b, idesc, 0);
-          mma<V::kPair, true>(d, a + 2, b + 2, idesc, 1);
-          mma<V::kPair, true>(d, a + 4, b + 4, idesc, 1);
-          mma<V::kPair, true>(d, a + 6, b + 6, idesc, 1);
-          commit<V::kPair>(&c.acc_full[use & 1]);
-          commit<V::kPair>(&c.empty[ring.stage]);
+          mma<false, true>(d, a, b, idesc, 0);
+          mma<false, true>(d, a + 2, b + 2, idesc, 1);
+          mma<false, true>(d, a + 4, b + 4, idesc, 1);
+          mma<false, true>(d, a + 6, b + 6, idesc, 1);
+          commit<false>(&c.acc_full[use & 1]);
+          commit<false>(&c.empty[ring.stage]);
         }
         __syncwarp();
         ring.next();
       }
     }
     if (elect_one()) {
-      if constexpr (V::kPair) tc_commit_pair(&c.mma_done, (uint16_t)0x1);
-      else tc_commit(&c.mma_done);
+      tc_commit(&c.mma_done);
       drain(&c.mma_done, 0, g.err);
     }
     __syncwarp();
@@ -426,10 +409,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
     };
     const int64_t n_blocks = (g.n - 1) / 128 + 1;
     RowTile m;
-    for (uint32_t t = unit; t < tiles && ok; t += units) {
+    for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       row_tile<V::kTileRows>(m, t, f_tiles, off, first);
-      const float* xs = g.x_scale + m.row + kBM * (int64_t)rank;
-      const int rows = m.rows - kBM * (int)rank;
+      const float* xs = g.x_scale + m.row;
       for (int kb = 0; kb < blocks; kb += kGroup, ++use) {
         const uint32_t s = use % kGroups;
         ok = wait_warp(&sc.empty[s], (use / kGroups & 1u) ^ 1u, g.err, &c.abort);
@@ -439,7 +421,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
           if (kb + i < blocks)
 #pragma unroll
             for (int r = 0; r < kBM; r += 32)
-              if (r + lane < rows) copy_4(&sc.x[s][i][r + lane], xs + (int64_t)(kb + i) * g.ld_x_scale + r + lane);
+              if (r + lane < m.rows) copy_4(&sc.x[s][i][r + lane], xs + (int64_t)(kb + i) * g.ld_x_scale + r + lane);
         const int half = lane / kGroup, b = lane % kGroup;
         if (half < 2 && kb + b < blocks && m.f0 / 128 + half < n_blocks)
           copy_4(&sc.w[s][half][b], g.w_scale + ((int64_t)m.expert * n_blocks + m.f0 / 128 + half) * blocks + kb + b);
@@ -458,7 +440,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
     uint32_t use = 0, groups = 0;
     bool ok = true;
     RowTile m;
-    for (uint32_t t = unit; t < tiles && ok; t += units) {
+    for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       row_tile<V::kTileRows>(m, t, f_tiles, off, first);
       const bool on = 128 * half < columns(m);
       f32x2 sum[64];
@@ -474,21 +456,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
           const float scale = sc.x[s][i][32 * q + lane] * sc.w[s][half][i];
           const f32x2 both = pair(scale, scale);
           const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 128u * half;
-          // The next 16 columns arrive while these are added.
-          uint32_t v[2][16];
-          tmem_ld_32x32b_x16(at, v[0]);
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
+          for (int h = 0; h < 128; h += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(at + h, v);
             tmem_ld_wait();
-            if (h < 7) tmem_ld_32x32b_x16(at + 16 * (h + 1), v[(h + 1) & 1]);
-            const uint32_t (&now)[16] = v[h & 1];
 #pragma unroll
             for (int k = 0; k < 16; k += 2)
-              sum[8 * h + k / 2] =
-                  fma2(pair(__uint_as_float(now[k]), __uint_as_float(now[k + 1])), both, sum[8 * h + k / 2]);
+              sum[(h + k) / 2] =
+                  fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), both, sum[(h + k) / 2]);
           }
         }
-        release_acc<V::kPair>(c, use & 1, rank, lane);
+        release_acc<false>(c, use & 1, 0, lane);
         if (i == kGroup - 1 || kb == blocks - 1) {
           if (lane == 0) mbar_arrive(&sc.empty[s]);
           ++groups;
@@ -499,8 +478,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
       // 64 bytes of the warp's 32 rows at a time, so that a store covers whole sectors of 8 rows: 16-byte
       // chunk c of row r stands in slot c ^ (r / 2 % 4), free of bank conflicts.
       constexpr int kValues = 16 / (int)sizeof(O), kPasses = 128 / (4 * kValues);
-      const int left = m.rows - kBM * (int)rank - 32 * q;
-      O* y = static_cast<O*>(g.y) + ((int64_t)m.row + kBM * (int)rank + 32 * q) * g.ldy;
+      const int left = m.rows - 32 * q;
+      O* y = static_cast<O*>(g.y) + ((int64_t)m.row + 32 * q) * g.ldy;
 #pragma unroll
       for (int pass = 0; pass < kPasses; ++pass) {
         __syncwarp();
@@ -532,28 +511,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) fp8_rows_kernel(const __grid_c
     // Rows of no expert.
     const int64_t head = off[0], none = head + g.rows - off[g.n_experts];
     for (int64_t z = blockIdx.x; z < none; z += gridDim.x)
-      Store<O>::template zero_row<kRowWarps>(p, z < head ? z : off[g.n_experts] + z - head,
+      Store<O>::template zero_row<kEpiWarps>(p, z < head ? z : off[g.n_experts] + z - head,
                                              (int)threadIdx.x - 128);
   }
-  sync_ctas<V::kPair>();
-  if (warp == 2) {
-    if constexpr (V::kPair) tmem_dealloc_pair(tmem, kTmemCols);
-    else tmem_dealloc(tmem, kTmemCols);
-  }
+  sync_ctas<false>();
+  if (warp == 2) tmem_dealloc(tmem, kTmemCols);
 }
 
-// At least as many tiles as the offsets can make of the rows.
-template <typename V>
-int64_t row_tiles(const GroupedMm& g) {
-  return (g.rows / V::kTileRows + (g.rows < g.n_experts ? g.rows : g.n_experts)) *
-         (((int64_t)g.n - 1) / 256 + 1);
-}
-
-template <typename V, typename O>
+template <typename O>
 cudaError_t launch_rows(const Fp8Params& p, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  return launch(fp8_rows_kernel<V, O>, p, row_tiles<V>(p.g), V::kCtas, sms,
-                V::kStages * V::kStage + kRowWarps * kRowStage + 1024, &ready, st, kRowThreads);
+  // At least as many tiles as the offsets can make of the rows.
+  const int64_t tiles = (p.g.rows / Rows8::kTileRows + (p.g.rows < p.g.n_experts ? p.g.rows : p.g.n_experts)) *
+                        (((int64_t)p.g.n - 1) / Rows8::kTileCols + 1);
+  return launch(fp8_rows_kernel<O>, p, tiles, 1, sms,
+                Rows8::kStages * Rows8::kStage + kEpiWarps * kRowStage + 1024, &ready, st);
 }
 
 template <typename V, typename O>
@@ -563,16 +535,10 @@ cudaError_t launch_as(const Fp8Params& p, int parts, int sms, cudaStream_t st) {
                 V::kStages * Shape<V>::kStage + (V::kSplit ? 0 : kEpiWarps * kStaging8) + 1024, &ready, st);
 }
 
-struct Fp8Choice {
-  int parts;
-  bool narrow, pair;
-};
-
 template <typename O>
-cudaError_t launch_type(const Fp8Params& p, const Fp8Choice& c, int sms, cudaStream_t st) {
-  return c.parts > 1 ? launch_as<Split8, O>(p, c.parts, sms, st)
-         : c.narrow  ? launch_as<Narrow8, O>(p, 1, sms, st)
-         : c.pair    ? launch_rows<Rows8<true>, O>(p, sms, st) : launch_rows<Rows8<false>, O>(p, sms, st);
+cudaError_t launch_type(const Fp8Params& p, int parts, bool narrow, int sms, cudaStream_t st) {
+  return parts > 1 ? launch_as<Split8, O>(p, parts, sms, st)
+         : narrow  ? launch_as<Narrow8, O>(p, 1, sms, st) : launch_rows<O>(p, sms, st);
 }
 
 }  // namespace
@@ -584,18 +550,17 @@ cudaError_t launch_fp8_mm(const Fp8Mm& g, int sms, cudaStream_t st) {
   const int64_t line = ((int64_t)g.k + 15) / 16 * 16;
   const Operand x{g.x, g.rows, g.k, g.rows == 1 ? line : g.ldx, 1, 0};
   const Operand w{g.w, g.n, g.k, g.n == 1 ? line : g.ldw, g.n_experts, g.w_stride};
-  Fp8Choice c{1, false, false};
-  while (c.parts < kMostParts && mm_tiles<Split8>(g) * c.parts * 2 <= sms && g.k >= 4 * kBK8 * c.parts * 2)
-    c.parts *= 2;
-  c.narrow = g.rows <= Narrow8::kMaxN * (int64_t)g.n_experts || mm_tiles<Narrow8>(g) <= sms;
-  c.pair = !c.narrow && row_tiles<Rows8<true>>(g) * 2 >= sms;
-  const bool few = c.parts > 1 || c.narrow;
+  // The rules of the 16-bit products (see choose_tiles), and tiles of y itself where those take wide ones.
+  int parts = 1;
+  while (parts < kMostParts && mm_tiles<Split8>(g) * parts * 2 <= sms && g.k >= 4 * kBK8 * parts * 2) parts *= 2;
+  const bool narrow = g.rows <= Narrow8::kMaxN * (int64_t)g.n_experts || mm_tiles<Narrow8>(g) <= sms;
+  const bool few = parts > 1 || narrow;
   cudaError_t e = encode(&p.x, x, kE4m3, false, few ? Narrow8::kBoxRows : kBM);
   if (e == cudaSuccess) e = encode(&p.w, w, kE4m3, true, few ? kBM : 64);
   if (e != cudaSuccess) return e;
-  return g.out_dtype == kF32 ? launch_type<float>(p, c, sms, st)
-         : g.out_dtype == kBf16 ? launch_type<__nv_bfloat16>(p, c, sms, st)
-                                : launch_type<__half>(p, c, sms, st);
+  return g.out_dtype == kF32 ? launch_type<float>(p, parts, narrow, sms, st)
+         : g.out_dtype == kBf16 ? launch_type<__nv_bfloat16>(p, parts, narrow, sms, st)
+                                : launch_type<__half>(p, parts, narrow, sms, st);
 }
 
 }  // namespace muon
