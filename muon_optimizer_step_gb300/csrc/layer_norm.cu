@@ -52,24 +52,73 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& r) {
   }
 }
 
-// V weights from p on (`value` where there are none).
+// The arithmetic of V values: on pairs, two to an instruction, or (V = 1) on single ones.
 template <int V>
-__device__ __forceinline__ void load_weights(const float* p, bool wide, float value, float (&w)[V]) {
+using Wide = typename std::conditional<V == 1, float, f32x2>::type;
+template <int V>
+constexpr int kWide = V == 1 ? 1 : V / 2;
+
+template <typename W>
+__device__ __forceinline__ W both(float v) {
+  if constexpr (sizeof(W) == 4) return v;
+  else return pair(v, v);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Vec<T, V>& v, Wide<V> (&w)[kWide<V>]) {
+  if constexpr (V == 1) {
+    w[0] = cvt(v.v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) w[k / 2] = pair(v.v[k], v.v[k + 1]);
+  } else {
+    uint32_t q[V / 2];
+    memcpy(q, v.v, sizeof(q));
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      const float2 f = unpack_2<T>(q[k]);
+      w[k] = pair(f.x, f.y);
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_wide(T* p, const Wide<V> (&w)[kWide<V>]) {
+  Vec<T, V> v;
+  if constexpr (V == 1) {
+    put(&v.v[0], w[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      v.v[k] = parts(w[k / 2]).x;
+      v.v[k + 1] = parts(w[k / 2]).y;
+    }
+  } else {
+    uint32_t q[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) q[k] = pack_2<T>(parts(w[k]).x, parts(w[k]).y);
+    memcpy(v.v, q, sizeof(q));
+  }
+  store_vec<T, V>(p, v);
+}
+
+// V weights from p on (`value` where there are none); wide: they start on 16 bytes.
+template <int V>
+__device__ __forceinline__ void load_weights(const float* p, bool wide, float value, Wide<V> (&w)[kWide<V>]) {
   if (p == nullptr) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) w[k] = value;
-  } else if (V % 4 == 0 && wide) {
+    for (int k = 0; k < kWide<V>; ++k) w[k] = both<Wide<V>>(value);
+  } else if constexpr (V == 1) {
+    w[0] = __ldg(p);
+  } else if (wide) {
 #pragma unroll
     for (int k = 0; k < V; k += 4) {
       const float4 q = __ldg(reinterpret_cast<const float4*>(p + k));
-      w[k] = q.x;
-      w[(k + 1) % V] = q.y;
-      w[(k + 2) % V] = q.z;
-      w[(k + 3) % V] = q.w;
+      w[k / 2] = pair(q.x, q.y);
+      w[k / 2 + 1] = pair(q.z, q.w);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) w[k] = __ldg(p + k);
+    for (int k = 0; k < V; k += 2) w[k / 2] = pair(__ldg(p + k), __ldg(p + k + 1));
   }
 }
 
@@ -96,7 +145,7 @@ __device__ __forceinline__ float2 group_sum(float2 v, float2 (*red)[32], int tur
   return v;
 }
 
-struct Wide {
+struct Aligned {
   bool w, b;  // the weights (biases) start on 16 bytes
 };
 
@@ -106,39 +155,63 @@ constexpr int kBlockThreads = kTpr > 32 ? kTpr : 256;
 // (Threads without a row stay for the shuffles.)
 template <typename T, int V, int kTpr, int kN>
 __global__ void __launch_bounds__(kBlockThreads<kTpr>)
-norm_kernel(const NormArgs a, const Wide wide) {
+norm_kernel(const NormArgs a, const Aligned aligned) {
   constexpr int kRows = kBlockThreads<kTpr> / kTpr;
   __shared__ float2 red[2][32];
   const int t = threadIdx.x % kTpr, g = threadIdx.x / kTpr;
   const uint32_t cols = (uint32_t)a.cols;
   const float over = 1.f / (float)a.cols;
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
-    const int64_t r = r0 + g;
-    const bool on = r < a.rows;
-    const T* x = static_cast<const T*>(a.x) + (on ? r : 0) * a.ldx;
-    Vec<T, V> v[kN];
-    float2 s = make_float2(0.f, 0.f);
+  using W = Wide<V>;
+  // A thread with one vector of a row keeps its weights.
+  W hw[kWide<V>], hb[kWide<V>];
+  if (kN == 1 && (uint32_t)t * V < cols) {
+    load_weights<V>(a.w == nullptr ? nullptr : a.w + t * V, aligned.w, 1.f, hw);
+    load_weights<V>(a.b == nullptr ? nullptr : a.b + t * V, aligned.b, 0.f, hb);
+  }
+  Vec<T, V> next[kN];
+  // A row's values, asked for while the row before is at work.
+  const auto load = [&](int64_t r) {
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const uint32_t c = (uint32_t)(t + i * kTpr) * V;
-      if (on && c < cols) v[i] = load_vec<T, V>(x + c);
+      if (r < a.rows && c < cols) next[i] = load_vec<T, V>(x + c);
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  load((int64_t)blockIdx.x * kRows + g);
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += step) {
+    const int64_t r = r0 + g;
+    const bool on = r < a.rows;
+    float2 s = make_float2(0.f, 0.f);
+    W x[kN][kWide<V>], sum[kWide<V>];
+#pragma unroll
+    for (int k = 0; k < kWide<V>; ++k) sum[k] = both<W>(0.f);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (on && (uint32_t)(t + i * kTpr) * V < cols) {
+        widen<T, V>(next[i], x[i]);
+#pragma unroll
+        for (int k = 0; k < kWide<V>; ++k) sum[k] = add2(sum[k], x[i][k]);
+      }
+    load(r + step);
+#pragma unroll
+    for (int k = 0; k < kWide<V>; ++k) s.x += total(sum[k]);
+    const float mean = group_sum<kTpr>(s, red, turn++).x * over;
+#pragma unroll
+    for (int k = 0; k < kWide<V>; ++k) sum[k] = both<W>(0.f);
 #pragma unroll
     for (int i = 0; i < kN; ++i)
       if (on && (uint32_t)(t + i * kTpr) * V < cols)
 #pragma unroll
-        for (int k = 0; k < V; ++k) s.x += cvt(v[i].v[k]);
-    const float mean = group_sum<kTpr>(s, red, turn++).x * over;
+        for (int k = 0; k < kWide<V>; ++k) {
+          x[i][k] = add2(x[i][k], both<W>(-mean));
+          sum[k] = fma2(x[i][k], x[i][k], sum[k]);
+        }
     s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (on && (uint32_t)(t + i * kTpr) * V < cols)
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float d = cvt(v[i].v[k]) - mean;
-          s.x = fmaf(d, d, s.x);
-        }
+    for (int k = 0; k < kWide<V>; ++k) s.x += total(sum[k]);
     const float rstd = rsqrtf(group_sum<kTpr>(s, red, turn++).x * over + a.eps);
     if (on) {
       T* y = static_cast<T*>(a.out) + r * a.ldo;
@@ -146,13 +219,15 @@ norm_kernel(const NormArgs a, const Wide wide) {
       for (int i = 0; i < kN; ++i) {
         const uint32_t c = (uint32_t)(t + i * kTpr) * V;
         if (c >= cols) continue;
-        float w[V], b[V];
-        load_weights<V>(a.w == nullptr ? nullptr : a.w + c, wide.w, 1.f, w);
-        load_weights<V>(a.b == nullptr ? nullptr : a.b + c, wide.b, 0.f, b);
-        Vec<T, V> o;
+        W w[kWide<V>], b[kWide<V>];
+        if constexpr (kN > 1) {
+          load_weights<V>(a.w == nullptr ? nullptr : a.w + c, aligned.w, 1.f, w);
+          load_weights<V>(a.b == nullptr ? nullptr : a.b + c, aligned.b, 0.f, b);
+        }
 #pragma unroll
-        for (int k = 0; k < V; ++k) put(&o.v[k], fmaf((cvt(v[i].v[k]) - mean) * rstd, w[k], b[k]));
-        store_vec<T, V>(y + c, o);
+        for (int k = 0; k < kWide<V>; ++k)
+          b[k] = fma2(mul2(x[i][k], both<W>(rstd)), kN > 1 ? w[k] : hw[k], kN > 1 ? b[k] : hb[k]);
+        store_wide<T, V>(y + c, b);
       }
       if (t == 0) {
         if (a.mean != nullptr) a.mean[r] = mean;
@@ -197,73 +272,118 @@ __global__ void __launch_bounds__(kLong) norm_long_kernel(const NormArgs a) {
 // row behind.
 template <typename T, int V, int kTpr, int kN, bool kSums>
 __global__ void __launch_bounds__(kBlockThreads<kTpr>)
-norm_grad_kernel(const NormArgs a, const Wide wide) {
+norm_grad_kernel(const NormArgs a, const Aligned aligned) {
   constexpr int kThreads = kBlockThreads<kTpr>, kRows = kThreads / kTpr;
   __shared__ float2 red[2][32];
   const int t = threadIdx.x % kTpr, g = threadIdx.x / kTpr;
   const uint32_t cols = (uint32_t)a.cols;
   const float over = 1.f / (float)a.cols;
-  float dw[kN][V], db[kN][V];
+  using W = Wide<V>;
+  constexpr int H = kWide<V>;
+  W dw[kN][H], db[kN][H];
   if constexpr (kSums)
 #pragma unroll
     for (int i = 0; i < kN; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) dw[i][k] = db[i][k] = 0.f;
+      for (int k = 0; k < H; ++k) dw[i][k] = db[i][k] = both<W>(0.f);
+  W hw[H];  // as in the forward pass
+  if (kN == 1 && (uint32_t)t * V < cols)
+    load_weights<V>(a.w == nullptr ? nullptr : a.w + t * V, aligned.w, 1.f, hw);
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
-    const int64_t r = r0 + g;
-    const bool on = r < a.rows;
-    const T* x = static_cast<const T*>(a.x) + (on ? r : 0) * a.ldx;
-    const T* dy = static_cast<const T*>(a.dy) + (on ? r : 0) * a.lddy;
-    const float mean = on ? a.mean_in[r] : 0.f, rstd = on ? a.rstd_in[r] : 0.f;
-    Vec<T, V> xv[kN], dv[kN];
-    float2 s = make_float2(0.f, 0.f);
+  Vec<T, V> xv[kN], dv[kN], xn[kN], dn[kN];
+  float mean, rstd, mean_n = 0.f, rstd_n = 0.f;
+  const auto load = [&](int64_t r) {
+    if (r >= a.rows) return;
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
+    mean_n = a.mean_in[r];
+    rstd_n = a.rstd_in[r];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const uint32_t c = (uint32_t)(t + i * kTpr) * V;
-      if (on && c < cols) {
-        xv[i] = load_vec<T, V>(x + c);
-        dv[i] = load_vec<T, V>(dy + c);
+      if (c < cols) {
+        xn[i] = load_vec<T, V>(x + c);
+        dn[i] = load_vec<T, V>(dy + c);
       }
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  load((int64_t)blockIdx.x * kRows + g);
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += step) {
+    const int64_t r = r0 + g;
+    const bool on = r < a.rows;
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      xv[i] = xn[i];
+      dv[i] = dn[i];
+    }
+    mean = mean_n;
+    rstd = rstd_n;
+    load(r + step);
+    W s1[H], s2[H];
+#pragma unroll
+    for (int k = 0; k < H; ++k) s1[k] = s2[k] = both<W>(0.f);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const uint32_t c = (uint32_t)(t + i * kTpr) * V;
       if (!on || c >= cols) continue;
-      float w[V];
-      load_weights<V>(a.w == nullptr ? nullptr : a.w + c, wide.w, 1.f, w);
+      W w[H], x[H], d[H];
+      if constexpr (kN > 1) {
+        load_weights<V>(a.w == nullptr ? nullptr : a.w + c, aligned.w, 1.f, w);
+      } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float d = cvt(dv[i].v[k]), xh = (cvt(xv[i].v[k]) - mean) * rstd, u = d * w[k];
-        s.x += u;
-        s.y = fmaf(u, xh, s.y);
+        for (int k = 0; k < H; ++k) w[k] = hw[k];
+      }
+      widen<T, V>(xv[i], x);
+      widen<T, V>(dv[i], d);
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        const W xh = mul2(add2(x[k], both<W>(-mean)), both<W>(rstd)), u = mul2(d[k], w[k]);
+        s1[k] = add2(s1[k], u);
+        s2[k] = fma2(u, xh, s2[k]);
         if constexpr (kSums) {
-          dw[i][k] = fmaf(d, xh, dw[i][k]);
-          db[i][k] += d;
+          dw[i][k] = fma2(d[k], xh, dw[i][k]);
+          db[i][k] = add2(db[i][k], d[k]);
         }
       }
     }
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      s.x += total(s1[k]);
+      s.y += total(s2[k]);
+    }
     s = group_sum<kTpr>(s, red, turn++);
-    const float m1 = s.x * over, m2 = s.y * over;
     if (!on) continue;
+    // dx = dy (w rstd) - rstd m1 - (x - mean) rstd^2 m2
+    const W c1 = both<W>(-rstd * (s.x * over)), c2 = both<W>(-rstd * rstd * (s.y * over));
     T* dx = static_cast<T*>(a.out) + r * a.ldo;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const uint32_t c = (uint32_t)(t + i * kTpr) * V;
       if (c >= cols) continue;
-      float w[V];
-      load_weights<V>(a.w == nullptr ? nullptr : a.w + c, wide.w, 1.f, w);
-      Vec<T, V> o;
+      W w[H], x[H], d[H];
+      if constexpr (kN > 1) {
+        load_weights<V>(a.w == nullptr ? nullptr : a.w + c, aligned.w, 1.f, w);
+      } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float xh = (cvt(xv[i].v[k]) - mean) * rstd;
-        put(&o.v[k], rstd * (fmaf(cvt(dv[i].v[k]), w[k], -m1) - xh * m2));
+        for (int k = 0; k < H; ++k) w[k] = hw[k];
       }
-      store_vec<T, V>(dx + c, o);
+      widen<T, V>(xv[i], x);
+      widen<T, V>(dv[i], d);
+#pragma unroll
+      for (int k = 0; k < H; ++k)
+        d[k] = fma2(add2(x[k], both<W>(-mean)), c2, fma2(d[k], mul2(w[k], both<W>(rstd)), c1));
+      store_wide<T, V>(dx + c, d);
     }
   }
   if constexpr (kSums) {
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    const auto value = [](W v, int k) {
+      if constexpr (V == 1) return v;
+      else return k == 0 ? parts(v).x : parts(v).y;
+    };
+    constexpr int E = V / H;  // values of a W
     if constexpr (kRows == 1) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
@@ -271,8 +391,8 @@ norm_grad_kernel(const NormArgs a, const Wide wide) {
         if (c >= cols) continue;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-          part[c + k] = dw[i][k];
-          part[cols + c + k] = db[i][k];
+          part[c + k] = value(dw[i][k / E], k % E);
+          part[cols + c + k] = value(db[i][k / E], k % E);
         }
       }
     } else {
@@ -285,7 +405,7 @@ norm_grad_kernel(const NormArgs a, const Wide wide) {
         for (int i = 0; i < kN; ++i)
 #pragma unroll
           for (int k = 0; k < V; ++k)
-            sums[g * kCols + (t + i * kTpr) * V + k] = which == 0 ? dw[i][k] : db[i][k];
+            sums[g * kCols + (t + i * kTpr) * V + k] = value(which == 0 ? dw[i][k / E] : db[i][k / E], k % E);
         __syncthreads();
         for (uint32_t c = threadIdx.x; c < (uint32_t)kCols && c < cols; c += kThreads) {
           float s = 0.f;
@@ -320,6 +440,265 @@ __global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormArgs a)
     for (uint32_t c = threadIdx.x; c < cols; c += kLong) {
       const float u = cvt(dy[c]) * (a.w != nullptr ? a.w[c] : 1.f);
       put(&dx[c], rstd * (u - m1 - (cvt(x[c]) - mean) * rstd * m2));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- slabs
+// Longer rows: a block takes kSlab rows at a time.  First a warp per row sums it, twice for the forward pass
+// (the second time out of L1); then every thread has its columns of all the rows, with their weights, and in
+// the gradient the sums over the rows, in registers.  So weights are read once per block and the block
+// meets twice per kSlab rows, where a group of threads per row reads them, and meets, for every row.
+constexpr int kSlabThreads = 512, kSlab = kSlabThreads / 32;
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> keep_vec(const T* p) {  // as load_vec, to be read again soon
+  Vec<T, V> r;
+  if constexpr (V == 1) {
+    r.v[0] = *p;
+  } else {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    memcpy(r.v, &q, 16);
+  }
+  return r;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The columns of a thread in a slab's second part: vectors t, t + across, ... of rows g, g + groups, ...
+struct SlabShare {
+  uint32_t vectors, across;
+  int t, g, groups;
+};
+template <int V>
+__device__ __forceinline__ SlabShare slab_share(int32_t cols) {
+  SlabShare s;
+  s.vectors = (uint32_t)cols / V;
+  s.across = s.vectors < kSlabThreads ? (s.vectors + 31) / 32 * 32 : kSlabThreads;
+  s.groups = kSlabThreads / s.across;
+  s.g = threadIdx.x / s.across;
+  s.t = threadIdx.x % s.across;
+  return s;
+}
+
+template <typename T, int V, int kN>
+__global__ void __launch_bounds__(kSlabThreads, kN * V <= 16 ? 2 : 1)
+norm_slab_kernel(const NormArgs a, const Aligned aligned) {
+  using W = Wide<V>;
+  constexpr int H = kWide<V>;
+  __shared__ float2 stat[kSlab];
+  const SlabShare sh = slab_share<V>(a.cols);
+  const float over = 1.f / (float)a.cols;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  W w[kN][H], b[kN][H];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const uint32_t v = sh.t + i * sh.across;
+    if (v < sh.vectors) {
+      load_weights<V>(a.w == nullptr ? nullptr : a.w + v * V, aligned.w, 1.f, w[i]);
+      load_weights<V>(a.b == nullptr ? nullptr : a.b + v * V, aligned.b, 0.f, b[i]);
+    }
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * kSlab; r0 < a.rows; r0 += (int64_t)gridDim.x * kSlab) {
+    const int64_t mine = r0 + warp;
+    float mean = 0.f, rstd = 0.f;
+    if (mine < a.rows) {
+      const T* x = static_cast<const T*>(a.x) + mine * a.ldx;
+      W sum[H];
+#pragma unroll
+      for (int k = 0; k < H; ++k) sum[k] = both<W>(0.f);
+#pragma unroll 8
+      for (uint32_t v = lane; v < sh.vectors; v += 32) {
+        W e[H];
+        widen<T, V>(keep_vec<T, V>(x + v * V), e);
+#pragma unroll
+        for (int k = 0; k < H; ++k) sum[k] = add2(sum[k], e[k]);
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < H; ++k) s += total(sum[k]);
+      mean = warp_sum(s) * over;
+#pragma unroll
+      for (int k = 0; k < H; ++k) sum[k] = both<W>(0.f);
+#pragma unroll 8
+      for (uint32_t v = lane; v < sh.vectors; v += 32) {
+        W e[H];
+        widen<T, V>(keep_vec<T, V>(x + v * V), e);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+          e[k] = add2(e[k], both<W>(-mean));
+          sum[k] = fma2(e[k], e[k], sum[k]);
+        }
+      }
+      s = 0.f;
+#pragma unroll
+      for (int k = 0; k < H; ++k) s += total(sum[k]);
+      rstd = rsqrtf(warp_sum(s) * over + a.eps);
+      if (lane == 0) {
+        stat[warp] = make_float2(mean, rstd);
+        if (a.mean != nullptr) a.mean[mine] = mean;
+        if (a.rstd != nullptr) a.rstd[mine] = rstd;
+      }
+    }
+    __syncthreads();
+    const int rows = (int)(a.rows - r0 < kSlab ? a.rows - r0 : kSlab);
+    if (sh.g < sh.groups)
+#pragma unroll 4
+      for (int q = sh.g; q < rows; q += sh.groups) {
+        const T* x = static_cast<const T*>(a.x) + (r0 + q) * a.ldx;
+        T* y = static_cast<T*>(a.out) + (r0 + q) * a.ldo;
+        const float2 st = stat[q];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const uint32_t v = sh.t + i * sh.across;
+          if (v >= sh.vectors) continue;
+          W e[H];
+          widen<T, V>(load_vec<T, V>(x + v * V), e);
+#pragma unroll
+          for (int k = 0; k < H; ++k)
+            e[k] = fma2(mul2(add2(e[k], both<W>(-st.x)), both<W>(st.y)), w[i][k], b[i][k]);
+          store_wide<T, V>(y + v * V, e);
+        }
+      }
+    __syncthreads();
+  }
+}
+
+// Vector v of the weights in shared memory, which holds planes of 16 bytes of each vector (V = 1: as they are).
+template <int V>
+__device__ __forceinline__ void plane_weights(const float4* planes, uint32_t vectors, uint32_t v,
+                                              Wide<V> (&w)[kWide<V>]) {
+  if constexpr (V == 1) {
+    w[0] = reinterpret_cast<const float*>(planes)[v];
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const float4 q = planes[k / 4 * vectors + v];
+      w[k / 2] = pair(q.x, q.y);
+      w[k / 2 + 1] = pair(q.z, q.w);
+    }
+  }
+}
+
+// kBlocks: on an SM at a time.
+template <typename T, int V, int kN, bool kSums, int kBlocks>
+__global__ void __launch_bounds__(kSlabThreads, kBlocks)
+norm_grad_slab_kernel(const NormArgs a, const Aligned aligned) {
+  using W = Wide<V>;
+  constexpr int H = kWide<V>;
+  extern __shared__ float4 planes[];
+  __shared__ float4 stat[kSlab];  // mean, rstd, and what dx takes of the row's sums
+  const SlabShare sh = slab_share<V>(a.cols);
+  const float over = 1.f / (float)a.cols;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  W dw[kN][H], db[kN][H];
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int k = 0; k < H; ++k) dw[i][k] = db[i][k] = both<W>(0.f);
+  for (uint32_t v = threadIdx.x; v < sh.vectors; v += kSlabThreads) {
+    W w[H];
+    load_weights<V>(a.w == nullptr ? nullptr : a.w + v * V, aligned.w, 1.f, w);
+    if constexpr (V == 1) {
+      reinterpret_cast<float*>(planes)[v] = w[0];
+    } else {
+#pragma unroll
+      for (int k = 0; k < H; k += 2)
+        planes[k / 2 * sh.vectors + v] =
+            make_float4(parts(w[k]).x, parts(w[k]).y, parts(w[k + 1]).x, parts(w[k + 1]).y);
+    }
+  }
+  __syncthreads();
+  for (int64_t r0 = (int64_t)blockIdx.x * kSlab; r0 < a.rows; r0 += (int64_t)gridDim.x * kSlab) {
+    const int64_t mine = r0 + warp;
+    if (mine < a.rows) {
+      const T* x = static_cast<const T*>(a.x) + mine * a.ldx;
+      const T* dy = static_cast<const T*>(a.dy) + mine * a.lddy;
+      const float mean = a.mean_in[mine], rstd = a.rstd_in[mine];
+      W s1[H], s2[H];
+#pragma unroll
+      for (int k = 0; k < H; ++k) s1[k] = s2[k] = both<W>(0.f);
+#pragma unroll 4
+      for (uint32_t v = lane; v < sh.vectors; v += 32) {
+        W e[H], d[H], w[H];
+        widen<T, V>(keep_vec<T, V>(x + v * V), e);
+        widen<T, V>(keep_vec<T, V>(dy + v * V), d);
+        plane_weights<V>(planes, sh.vectors, v, w);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+          const W u = mul2(d[k], w[k]);
+          s1[k] = add2(s1[k], u);
+          s2[k] = fma2(u, mul2(add2(e[k], both<W>(-mean)), both<W>(rstd)), s2[k]);
+        }
+      }
+      float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        m1 += total(s1[k]);
+        m2 += total(s2[k]);
+      }
+      m1 = warp_sum(m1) * over;
+      m2 = warp_sum(m2) * over;
+      if (lane == 0) stat[warp] = make_float4(mean, rstd, -rstd * m1, -rstd * m2);
+    }
+    __syncthreads();
+    const int rows = (int)(a.rows - r0 < kSlab ? a.rows - r0 : kSlab);
+    if (sh.g < sh.groups)
+#pragma unroll 2
+      for (int q = sh.g; q < rows; q += sh.groups) {
+        const T* x = static_cast<const T*>(a.x) + (r0 + q) * a.ldx;
+        const T* dy = static_cast<const T*>(a.dy) + (r0 + q) * a.lddy;
+        T* dx = static_cast<T*>(a.out) + (r0 + q) * a.ldo;
+        const float4 st = stat[q];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const uint32_t v = sh.t + i * sh.across;
+          if (v >= sh.vectors) continue;
+          W e[H], d[H], w[H];
+          widen<T, V>(load_vec<T, V>(x + v * V), e);
+          widen<T, V>(load_vec<T, V>(dy + v * V), d);
+          plane_weights<V>(planes, sh.vectors, v, w);
+          // dx = dy (w rstd) - rstd m1 - xh rstd m2
+#pragma unroll
+          for (int k = 0; k < H; ++k) {
+            const W xh = mul2(add2(e[k], both<W>(-st.x)), both<W>(st.y));
+            if constexpr (kSums) {
+              dw[i][k] = fma2(d[k], xh, dw[i][k]);
+              db[i][k] = add2(db[i][k], d[k]);
+            }
+            e[k] = fma2(xh, both<W>(st.w), fma2(d[k], mul2(w[k], both<W>(st.y)), both<W>(st.z)));
+          }
+          store_wide<T, V>(dx + v * V, e);
+        }
+      }
+    __syncthreads();
+  }
+  if constexpr (kSums) {
+    // The groups add their sums to those of the groups before them, in the workspace.
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    const auto value = [](W v, int k) {
+      if constexpr (V == 1) return v;
+      else return k == 0 ? parts(v).x : parts(v).y;
+    };
+    constexpr int E = V / H;  // values of a W
+    for (int q = 0; q < sh.groups; ++q) {
+      if (q > 0) __syncthreads();
+      if (sh.g != q) continue;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t v = sh.t + i * sh.across, c = v * V;
+        if (v >= sh.vectors) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float x = value(dw[i][k / E], k % E), y = value(db[i][k / E], k % E);
+          part[c + k] = q > 0 ? part[c + k] + x : x;
+          part[a.cols + c + k] = q > 0 ? part[a.cols + c + k] + y : y;
+        }
+      }
     }
   }
 }
@@ -371,10 +750,12 @@ norm_parts_kernel(const float* __restrict__ part, int parts, int32_t cols, float
 // ---------------------------------------------------------------------------- launches
 // How a row is shared: its vectors, the threads that take them and how many each.
 struct RowPlan {
-  int v, tpr, n;  // tpr 0: too long for registers
+  int v, tpr, n;   // tpr 0: slabs; n 0: too long for registers
+  int blocks;      // of the gradient by slabs on an SM
 };
 
 constexpr int kMostInRegisters = 16384;  // columns
+constexpr int kFewRows = 304;            // two for each of 152 SMs
 constexpr int kLongRows = 64;            // rows of long ones whose columns a block sums, at least
 
 bool on_16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -384,41 +765,54 @@ RowPlan plan_row(const NormArgs& a, int dtype, bool grad) {
   const bool wide = a.cols % v == 0 && on_16(a.x) && on_16(a.out) && a.ldx % v == 0 && a.ldo % v == 0 &&
                     (!grad || (on_16(a.dy) && a.lddy % v == 0));
   const int64_t n = wide ? a.cols / v : a.cols;
-  RowPlan p{wide ? v : 1, 0, 0};
+  RowPlan p{wide ? v : 1, 0, 0, 1};
   if (n <= 8) p.tpr = 8, p.n = 1;
   else if (n <= 32) p.tpr = 32, p.n = 1;
-  else if (n <= 128) p.tpr = 32, p.n = 4;
-  else if (n <= 256) p.tpr = 256, p.n = 1;
-  else if (n <= 512) p.tpr = 512, p.n = 1;
-  else if (n <= 1024) p.tpr = 512, p.n = 2;
+  else if (n <= 512 && a.rows <= kFewRows) p.tpr = 512, p.n = 1;
+  else if (dtype != kF32) p.n = n <= 512 ? 1 : n <= 1024 ? 2 : n <= 2048 ? 4 : !wide && n <= 8192 ? 16 : 0;
+  else if (n <= 512) p.tpr = 128, p.n = 4;
+  else if (n <= 1024) p.tpr = 256, p.n = 4;
   else if (n <= 2048) p.tpr = 512, p.n = 4;
   else if (!wide && n <= 8192) p.tpr = 512, p.n = 16;
+  if (p.tpr == 0 && p.n == 1 && n <= 128) p.blocks = 2;
   return p;
 }
 
-int64_t rows_per_block(const RowPlan& p) { return p.tpr > 32 ? 1 : 256 / p.tpr; }
+int64_t rows_per_block(const RowPlan& p) {
+  return p.n == 0 ? kLongRows : p.tpr == 0 ? kSlab : p.tpr > 32 ? 1 : 256 / p.tpr;
+}
 
 // The gradient's blocks, each with sums of its own: two or four per SM of 152.
 int64_t grad_blocks(const RowPlan& p, int64_t rows) {
-  const int64_t per = p.tpr == 0 ? kLongRows : rows_per_block(p), most = p.tpr > 32 || p.tpr == 0 ? 304 : 608;
+  const int64_t per = rows_per_block(p),
+                most = p.n == 0 ? 304 : p.tpr == 0 ? 152 * p.blocks : p.tpr <= 128 ? 608 : 304;
   const int64_t blocks = (rows + per - 1) / per;
   return blocks < most ? blocks : most;
 }
 
-// f(type tag, V, kTpr, kN) for the plan.
+// f(V, kTpr, kN) for the plan, with kTpr 0 for slabs.
 template <typename T, int V, typename F>
 cudaError_t by_shape(const RowPlan& p, const F& f) {
-  using std::integral_constant;
-  if (p.tpr == 8) return f(integral_constant<int, V>(), integral_constant<int, 8>(), integral_constant<int, 1>());
-  if (p.tpr == 32 && p.n == 1)
-    return f(integral_constant<int, V>(), integral_constant<int, 32>(), integral_constant<int, 1>());
-  if (p.tpr == 32) return f(integral_constant<int, V>(), integral_constant<int, 32>(), integral_constant<int, 4>());
-  if (p.tpr == 256) return f(integral_constant<int, V>(), integral_constant<int, 256>(), integral_constant<int, 1>());
-  if (p.n == 1) return f(integral_constant<int, V>(), integral_constant<int, 512>(), integral_constant<int, 1>());
-  if (p.n == 2) return f(integral_constant<int, V>(), integral_constant<int, 512>(), integral_constant<int, 2>());
-  if (p.n == 4) return f(integral_constant<int, V>(), integral_constant<int, 512>(), integral_constant<int, 4>());
-  if constexpr (V == 1)
-    return f(integral_constant<int, V>(), integral_constant<int, 512>(), integral_constant<int, 16>());
+  const auto v = std::integral_constant<int, V>();
+  const auto go = [&](auto tpr, auto n) { return f(v, tpr, n); };
+  const std::integral_constant<int, 0> slab;
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 4> four;
+  const std::integral_constant<int, 16> many;
+  if (p.tpr == 8) return go(std::integral_constant<int, 8>(), one);
+  if (p.tpr == 32) return go(std::integral_constant<int, 32>(), one);
+  if (p.tpr == 512 && p.n == 1) return go(std::integral_constant<int, 512>(), one);
+  if constexpr (sizeof(T) == 4) {
+    if (p.tpr == 128) return go(std::integral_constant<int, 128>(), four);
+    if (p.tpr == 256) return go(std::integral_constant<int, 256>(), four);
+    if (p.n == 4) return go(std::integral_constant<int, 512>(), four);
+    if constexpr (V == 1) return go(std::integral_constant<int, 512>(), many);
+  } else {
+    if (p.n == 1) return go(slab, one);
+    if (p.n == 2) return go(slab, std::integral_constant<int, 2>());
+    if (p.n == 4) return go(slab, four);
+    if constexpr (V == 1) return go(slab, many);
+  }
   return cudaErrorInvalidValue;
 }
 
@@ -426,15 +820,16 @@ template <typename T>
 cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t st) {
   constexpr int dtype = sizeof(T) == 4 ? kF32 : kBf16, v = 16 / sizeof(T);
   const RowPlan p = plan_row(a, dtype, false);
-  const Wide wide{on_16(a.w), on_16(a.b)};
-  if (p.tpr == 0) {
+  const Aligned aligned{on_16(a.w), on_16(a.b)};
+  if (p.n == 0) {
     norm_long_kernel<T><<<(unsigned)(a.rows < 2 * sms ? a.rows : 2 * sms), kLong, 0, st>>>(a);
     return cudaGetLastError();
   }
   const int64_t per = rows_per_block(p), blocks = (a.rows + per - 1) / per, cap = (int64_t)sms * 8;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const auto go = [&](auto V, auto tpr, auto n) {
-    norm_kernel<T, V(), tpr(), n()><<<grid, kBlockThreads<tpr()>, 0, st>>>(a, wide);
+    if constexpr (tpr() == 0) norm_slab_kernel<T, V(), n()><<<grid, kSlabThreads, 0, st>>>(a, aligned);
+    else norm_kernel<T, V(), tpr(), n()><<<grid, kBlockThreads<tpr()>, 0, st>>>(a, aligned);
     return cudaGetLastError();
   };
   return p.v == 1 ? by_shape<T, 1>(p, go) : by_shape<T, v>(p, go);
@@ -444,11 +839,11 @@ template <typename T>
 cudaError_t launch_norm_grad(const NormArgs& a, int sms, cudaStream_t st) {
   constexpr int dtype = sizeof(T) == 4 ? kF32 : kBf16, v = 16 / sizeof(T);
   const RowPlan p = plan_row(a, dtype, true);
-  const Wide wide{on_16(a.w), false};
+  const Aligned aligned{on_16(a.w), false};
   const int64_t parts = grad_blocks(p, a.rows);
   const bool sums = a.dw != nullptr || a.db != nullptr;
   cudaError_t e = cudaSuccess;
-  if (a.rows > 0 && p.tpr == 0) {
+  if (a.rows > 0 && p.n == 0) {
     norm_grad_long_kernel<T><<<(unsigned)(a.rows < 2 * sms ? a.rows : 2 * sms), kLong, 0, st>>>(a);
     if (sums)
       norm_columns_kernel<T><<<dim3((unsigned)((a.cols - 1) / kColumns + 1), (unsigned)parts), kColumns, 0,
@@ -456,8 +851,21 @@ cudaError_t launch_norm_grad(const NormArgs& a, int sms, cudaStream_t st) {
     e = cudaGetLastError();
   } else if (a.rows > 0) {
     const auto go = [&](auto V, auto tpr, auto n) {
-      (sums ? norm_grad_kernel<T, V(), tpr(), n(), true> : norm_grad_kernel<T, V(), tpr(), n(), false>)
-          <<<(unsigned)parts, kBlockThreads<tpr()>, 0, st>>>(a, wide);
+      if constexpr (tpr() == 0) {
+        auto kernel = sums ? norm_grad_slab_kernel<T, V(), n(), true, 1> : norm_grad_slab_kernel<T, V(), n(), false, 1>;
+        if constexpr (n() == 1)
+          if (p.blocks == 2)
+            kernel = sums ? norm_grad_slab_kernel<T, V(), n(), true, 2> : norm_grad_slab_kernel<T, V(), n(), false, 2>;
+        const size_t smem = ((size_t)a.cols * 4 + 15) / 16 * 16;
+        if (smem > 48 * 1024) {
+          const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+          if (s != cudaSuccess) return s;
+        }
+        kernel<<<(unsigned)parts, kSlabThreads, smem, st>>>(a, aligned);
+      } else {
+        (sums ? norm_grad_kernel<T, V(), tpr(), n(), true> : norm_grad_kernel<T, V(), tpr(), n(), false>)
+            <<<(unsigned)parts, kBlockThreads<tpr()>, 0, st>>>(a, aligned);
+      }
       return cudaGetLastError();
     };
     e = p.v == 1 ? by_shape<T, 1>(p, go) : by_shape<T, v>(p, go);
