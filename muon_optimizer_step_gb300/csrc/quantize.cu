@@ -294,7 +294,7 @@ template <typename T>
 cudaError_t rows_as(const QuantizeRows& a, int sms, cudaStream_t st) {
   constexpr int v = 16 / sizeof(T);
   const int64_t blocks = a.rows * (((int64_t)a.cols + 127) / 128), per = kThreads / 16,
-                need = (blocks + 4 * per - 1) / (4 * per), cap = (int64_t)sms * 32;
+                need = (blocks + 4 * per - 1) / (4 * per), cap = (int64_t)sms * 8;
   const unsigned grid = (unsigned)(need < cap ? need : cap);
   const bool wide = a.cols % 8 == 0 && on(a.x, 16) && a.ldx % v == 0 && on(a.q, 8) && a.ldq % 8 == 0;
   (wide ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>)<<<grid, kThreads, 0, st>>>(a);
