@@ -236,10 +236,8 @@ muon_status muon_gated_mm_grad_workspace_bytes(const void* dy, int64_t lddy, con
   if (bytes == nullptr) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
   GatedGrad g{};
   set_product(&g, dy, lddy, w, ldw, w_stride, rows, n_experts, k, n, trans_w, kBf16);
-  static float wanted;
-  g.dp = row_weight_grad ? &wanted : nullptr;
   EXPERT_TRY(check_gated_grad(g));
-  *bytes = gated_grad_workspace(g);
+  *bytes = gated_grad_workspace(g, row_weight_grad != 0);
   return done(cudaSuccess, "");
 }
 
@@ -274,7 +272,7 @@ muon_status muon_gated_mm_grad(const void* dy, int64_t lddy, const void* w, int6
   EXPERT_TRY(check_matrix(out, ld_out, rows, n, dtype, true, "out"));
   EXPERT_TRY(check_floats(row_weight, "row_weight"));
   EXPERT_TRY(check_floats(d_row_weight, "d_row_weight"));
-  EXPERT_TRY(check_workspace(workspace, workspace_bytes, gated_grad_workspace(g)));
+  EXPERT_TRY(check_workspace(workspace, workspace_bytes, gated_grad_workspace(g, d_row_weight != nullptr)));
   Device d;
   EXPERT_TRY(current_device(&d));
   if (rows == 0) return done(cudaSuccess, "");

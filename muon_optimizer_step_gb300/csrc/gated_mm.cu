@@ -10,12 +10,19 @@
 // gated: a tile's 128 accumulator lanes are 64 columns of g and the same 64 columns of u, so a k-block
 // brings as many bytes into an SM as a plain product's of the same work.  The epilogue warp that holds 32
 // columns of g and the one that holds them of u put 16 rows at a time into shared memory; each then takes
-// g and u of 8 of them.  g and u go to memory only where the caller keeps them.
+// g and u of 8 of them.  g and u go to memory only where the caller keeps them.  Bound by the tensor cores:
+//   4096 rows, 4096 -> 14336, both kept   520 us  1.85 PFLOP/s
+//   192 rows, 2048 -> 1408, 64 experts    105 us  6.7 TB/s (the weights, HBM)
 //
-// grad: dh stays in the accumulators.  The epilogue reads g and u of its tile and writes three results.  dp_r is summed over 32 columns in a warp; a second kernel adds
-// those sums in order, so equal inputs give equal bits.
+// grad: dh stays in the accumulators.  The epilogue reads g and u of its tile and writes three results.  dp_r is
+// summed over 32 columns in a warp; a second kernel adds those sums in order, so equal inputs give equal bits.
+// The epilogue bounds it: its loads, exponentials and stores of a 256 x 256 tile take 18000 cycles, in which
+// the MMAs, 16400, get one accumulator ahead (98304 rows, 2048 -> 1408: 633 us, 0.90 PFLOP/s and 2.9 TB/s; without
+// dp 552, a plain product 349).  Tiles of half as many rows with four accumulators took 677 us (an MMA warp
+// needs 450 cycles to issue a k-block), single CTAs 639, eight warps of the epilogue 755.
 //
-// sum: the k-blocks of the second product follow those of the first.
+// sum: the k-blocks of the second product follow those of the first (24570 rows, 1408 -> 2048: 206 us, 1.38
+// PFLOP/s).
 #include "activation.cuh"
 #include "grouped_kernel.cuh"
 
@@ -47,9 +54,6 @@ struct Gated {
     return second ? &p.w2 : &p.w;
   }
   static __device__ __forceinline__ bool fine(const Params&) { return false; }
-  template <typename V>
-  static __device__ __forceinline__ void ahead(const Params&, const MmTile&, int, int, int, int) {}
-
   // Both warps of a pair give up, or neither: one that finished alone would wait for ever.
   static __device__ __forceinline__ bool agree(int q, int group, bool ok) {
     uint32_t all;
@@ -76,7 +80,7 @@ struct Gated {
   static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int group,
                                                 int lane, uint32_t tmem, const float (&kept)[32],
                                                 const F& release, uint8_t* staging) {
-    constexpr int kInTmem = kBlocks == 1 || !kKeep ? kBlocks * 2 : (kBlocks - 1) * 2;  // chunks
+    constexpr int kInTmem = kBlocks == 1 ? 2 : (kBlocks - 1) * 2;  // chunks
     const GatedMm& o = p.g;
     const int pair = gate_pair(q, group), mine = q >> 1;  // 0: has g; 1: has u
     float* slots = reinterpret_cast<float*>(staging) + pair * 2 * kSlot;
@@ -152,9 +156,6 @@ struct Grad {
   static __device__ __forceinline__ bool fine(const Params& p) { return p.g.dp != nullptr; }
   static __device__ __forceinline__ bool agree(int, int, bool ok) { return ok; }
 
-  template <typename V>
-  static __device__ __forceinline__ void ahead(const Params&, const MmTile&, int, int, int, int) {}
-
   // From dh, g, u and the row's weight (twice), two at a time: dgate, dup and the activation; adds dp's terms.
   // silu'(g) = s + silu(g) (1 - s).
   static __device__ __forceinline__ void values(f32x2 dh, f32x2 g, f32x2 u, f32x2 w, float* dgate, float* dup,
@@ -192,9 +193,8 @@ struct Grad {
   // then has eight columns of a row, the width of its loads and stores.
   template <typename V, int kBlocks, typename F>
   static __device__ __forceinline__ void finish(const Params& p, const MmTile& m, int f, int q, int group,
-                                                int lane, uint32_t tmem, const float (&kept)[32],
-                                                const F& release, uint8_t* staging) {
-    constexpr int kInTmem = kBlocks == 1 || !kKeep ? kBlocks * 4 : (kBlocks - 1) * 4;  // chunks
+                                                int lane, uint32_t tmem, const float (&)[32], const F&,
+                                                uint8_t* staging) {
     const GatedGrad& o = p.g;
     if (f + 32 * q >= o.n) return;
     float* stage = reinterpret_cast<float*>(staging) + (q + 4 * group) * kSlot;
@@ -223,9 +223,7 @@ struct Grad {
       const float weight = w;
       if (c + 1 < kBlocks * 4) load(c + 1);
       __syncwarp();
-      if (c < kInTmem) put_tmem_8(stage, lane, tmem + r0);
-      else put_chunk<1, 8>(stage, lane, c - kInTmem, [&](int, int k) { return kept[k]; });
-      if (c == kInTmem - 1) release();
+      put_tmem_8(stage, lane, tmem + r0);
       __syncwarp();
       float dh[8], dg[8], du[8], out[8];
       f32x2 terms = 0;
@@ -360,9 +358,9 @@ size_t gated_mm_workspace(const GatedMm& g) {
                                copy_bytes(w_of(g, g.w2, g.ldw2, g.w2_stride));
 }
 
-size_t gated_grad_workspace(const GatedGrad& g) {
+size_t gated_grad_workspace(const GatedGrad& g, bool row_weight_grad) {
   return g.rows == 0 ? 0 : copy_bytes(x_of(g, g.x, g.ldx)) + copy_bytes(w_of(g, g.w, g.ldw, g.w_stride)) +
-                               (g.dp != nullptr ? (size_t)(row_parts(g) * g.rows * 4) : 0);
+                               (row_weight_grad ? (size_t)(row_parts(g) * g.rows * 4) : 0);
 }
 
 size_t mm_sum_workspace(const MmSum& g) {

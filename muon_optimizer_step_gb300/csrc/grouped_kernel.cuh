@@ -1,15 +1,15 @@
 // The kernel of the products grouped by expert (see grouped_mm.cu), over what it does with a tile:
 // an Op says which tensor maps the loads take (Params, x_map, w_map; kPasses: products whose sums are
 // added; kGated: two weights, 64 columns of each in a tile's 128 lanes), how many columns of the result a
-// CTA's tile is wide (kCols), whether sums are kept in short segments (fine), and what becomes of the
-// accumulators (kWarps of the epilogue; ahead: before a tile's first, agree: whether warps that finish a tile
-// together all have it, finish, join for tiles that a cluster shares, zero_row).
+// CTA's tile is wide (kCols), whether sums are kept in short segments (fine), how many warps the epilogue has
+// (kWarps) and what becomes of the accumulators (agree: whether warps that finish a tile together all have
+// it; finish; join for tiles that a cluster shares; zero_row).
 //
-// kFromTmem: all but the last of a warp's blocks of sums go back into TMEM, over the tile's last segment, and
-// finish takes them from there a few columns at a time; once it has, it hands the accumulator back and takes
-// the last block from registers.  With all sums in registers an epilogue that reads and computes a lot beside
-// them spilled, and what spills has no L1 to go to beside the stages (backward of 98304 x 2048 -> 1408:
-// 1706 us); with all of them in TMEM the MMAs waited for the accumulator (636 us).
+// kFromTmem: a tile's sums go back into TMEM, over its last segment, and finish takes them from there a few
+// columns at a time.  With all sums in registers an epilogue that computes a lot beside them spills, and what
+// spills has no L1 to go to beside the stages (98304 x 2048 -> 1408 backward: 1706 us with, 633 without).
+// kKeep: the last block of a warp's columns stays in registers, so that the accumulator is handed back
+// earlier, where the epilogue has them to spare (4096 x 4096 -> 14336 forward: 531 -> 526 us).
 #pragma once
 
 #include "grouped_tiles.cuh"
@@ -188,7 +188,6 @@ grouped_mm_kernel(const __grid_constant__ typename Op::Params p) {
     bool ok = true;
     for (uint32_t t = unit; t < tiles && ok; t += units) {
       const MmTile m = mm_tile<V, kCols>(t, f_tiles, g.n_experts, off, first);
-      Op::template ahead<V>(p, m, m.f0 + kCols * (int)rank, q, group, lane);
       float sum[kBlocks][32];
       if constexpr (Op::kFromTmem) {  // (or the last tile's would be kept through its epilogue)
 #pragma unroll
@@ -392,8 +391,6 @@ struct Store {
   static __device__ __forceinline__ bool agree(int, int, bool ok) { return ok; }
   template <typename P>
   static __device__ __forceinline__ bool fine(const P&) { return sizeof(O) == 4; }
-  template <typename V, typename P>
-  static __device__ __forceinline__ void ahead(const P&, const MmTile&, int, int, int, int) {}
 
   template <typename V, typename P>
   static __device__ __forceinline__ void finish(const P& p, const MmTile& m, int f, int q, int half,

@@ -151,7 +151,7 @@ struct MmSum : GroupedMm {
 bool gated_mm_fits(const GroupedMm& g);
 size_t gated_mm_workspace(const GatedMm& g);
 cudaError_t launch_gated_mm(const GatedMm& g, void* workspace, int sms, cudaStream_t st);
-size_t gated_grad_workspace(const GatedGrad& g);
+size_t gated_grad_workspace(const GatedGrad& g, bool row_weight_grad);
 cudaError_t launch_gated_grad(const GatedGrad& g, void* workspace, int sms, cudaStream_t st);
 size_t mm_sum_workspace(const MmSum& g);
 cudaError_t launch_mm_sum(const MmSum& g, void* workspace, int sms, cudaStream_t st);

@@ -6,7 +6,8 @@
 // elements; the others become NaN.
 //
 // Rows (activations): blocks of 128 columns of a row, 16 threads each.  Weights: blocks of 128 x 128, a
-// CTA each, transposed on request through shared memory.  Both read each value once and are bound by HBM.
+// CTA each, transposed on request through shared memory.  Both read each value once: 24570 x 2048 bf16 36 us
+// (4.2 TB/s), 64 x 2048 x 1408 transposed 124 us (4.5 TB/s).
 #include <type_traits>
 
 #include "element.cuh"
