@@ -54,9 +54,10 @@
 //   24570 rows, 2048 -> 1408, 64 experts  112 us  1.26 PFLOP/s and 4.8 TB/s
 //   192 rows, 1408 -> 2048, 64 experts     54 us  6.5 TB/s (HBM)
 //   6 rows, 2048 -> 1408, 64 experts      9.2 us  (4.5 us are launch, offsets and first load)
-//   weight gradient of the first          452 us  1.25 PFLOP/s and 3.1 TB/s, 55 % (403 us with
-//                                                 segments of 12: loads alone took 343, stores
-//                                                 alone 288, MMAs alone 279)
+//   weight gradient of the first          411 us  1.38 PFLOP/s and 3.4 TB/s (loads alone took 343,
+//                                                 stores alone 288, MMAs alone 279; 452 while a
+//                                                 pair's second CTA handed its accumulators back with
+//                                                 a release, see release_acc)
 #include "grouped_kernel.cuh"
 
 namespace muon {

@@ -36,7 +36,8 @@ constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 // which multiply fastest, pay for short segments (24570 rows, 2048 -> 1408, 16-bit: 111 us with
 // 11, 118 with 8; weight gradient of 98304 rows, 64 x 2048 x 1408: 403 us with 12, 422 with 8, 452
 // with 6, 523 with 4), the others little (weight gradient of 24576 rows: 188 us with 12, 192 with
-// 4).  With kSegment32 the error is a plain fp32 product's or at most a rounding (2^-24) more.
+// 4; all of these while accumulators were handed back with a release, 411 with 6 since).  With kSegment32 the
+// error is a plain fp32 product's or at most a rounding (2^-24) more.
 struct Pair {
   static constexpr bool kPair = true, kSplit = false;
   static constexpr int kMaxN = 256, kBoxRows = 64, kStages = 6, kSub = 1;
