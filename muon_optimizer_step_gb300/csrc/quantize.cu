@@ -107,13 +107,17 @@ struct Raw {
 
   // As e4m3, times `inverse`; odd: there may be infinities, which become NaN.
   __device__ __forceinline__ uint2 convert(float inverse, bool odd) const {
+    return odd ? convert_as<true>(inverse) : convert_as<false>(inverse);
+  }
+  template <bool kOdd>
+  __device__ __forceinline__ uint2 convert_as(float inverse) const {
     uint32_t q[4];
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
       float2 v;
       if constexpr (sizeof(T) == 4) v = make_float2(__uint_as_float(w[k]), __uint_as_float(w[k + 1]));
       else v = unpack_2<T>(w[k / 2]);
-      if (odd) {
+      if constexpr (kOdd) {
         v.x = isinf(v.x) ? __int_as_float(0x7fc00000) : v.x;
         v.y = isinf(v.y) ? __int_as_float(0x7fc00000) : v.y;
       }
