@@ -386,13 +386,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
-// The same without the release, which waits for all of the thread's stores to be visible to the cluster:
-// where the arrival hands over no memory.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
 // TMA load into this CTA's shared memory that signals an mbarrier in either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t smem_dst, const void* tmap, int x, int y,
                                                  uint32_t bar_cluster_addr) {

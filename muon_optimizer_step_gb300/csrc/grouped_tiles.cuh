@@ -21,7 +21,6 @@ constexpr int kABytes = kBM * 128;  // 16 KB
 constexpr int kBox = 64 * 128;      // an MN-major box: 64 k-rows of 128 bytes
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 256;       // TMEM columns of one accumulator, of two
-constexpr int kMostAccs = 4;
 constexpr int kMaxStages = 6;
 constexpr long long kWaitBudget = 4000000000LL;  // ~2 s of SM clock per wait
 
@@ -86,7 +85,7 @@ struct Control {
   // wgrad on pairs, last stage of a tile: the second CTA's own operands have landed, and it
   // has zeroed the rows that are not its expert's.
   uint64_t tail[kMaxStages], fixed[kMaxStages];
-  uint64_t acc_full[kMostAccs], acc_empty[kMostAccs];
+  uint64_t acc_full[2], acc_empty[2];
   uint64_t mma_done;
   uint32_t tmem;
   int abort;
@@ -251,7 +250,7 @@ __device__ __forceinline__ void setup(Control& c, int warp) {
       mbar_init(&c.tail[s], 1);
       mbar_init(&c.fixed[s], 1);
     }
-    for (int b = 0; b < kMostAccs; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&c.acc_full[b], 1);
       mbar_init(&c.acc_empty[b], (kPair ? 2 : 1) * kWarps);
     }
@@ -288,6 +287,13 @@ __device__ __forceinline__ void teardown(Control& c, int warp) {
   }
 }
 
+// mbar_arrive_cluster without the release, which waits for all of the thread's stores to be visible to the
+// cluster: where the arrival hands over no memory.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 // An epilogue warp is done reading accumulator `ab`: its loads have completed (tmem_ld_wait), and no memory
 // is handed over, so the arrival in the other CTA needs no release.  (With one, it waited for the warp's
 // stores of the tile before: 1290 instead of 150 cycles.)
@@ -301,10 +307,9 @@ __device__ __forceinline__ void release_acc(Control& c, int ab, uint32_t rank, i
   }
 }
 
-// Waits for accumulator use number `use`, one of kAccs in turn (epilogue warp).
-template <uint32_t kAccs = 2>
+// Waits for accumulator use number `use` (epilogue warp).
 __device__ __forceinline__ bool wait_acc(Control& c, uint32_t use, int* err) {
-  if (!wait_warp(&c.acc_full[use % kAccs], use / kAccs & 1u, err, &c.abort)) return false;
+  if (!wait_warp(&c.acc_full[use & 1], use >> 1 & 1u, err, &c.abort)) return false;
   tc_fence_after();
   return true;
 }
