@@ -17,7 +17,7 @@
 // columns summed by blocks of columns in a pass of their own.
 //
 // Bound by HBM where the arithmetic, two values to an instruction, and the sums' latency leave room:
-//   16384 x 4096 bf16  62 us forward (4.3 TB/s), 107 us backward (3.8 TB/s)
+//   16384 x 4096 bf16  58 us forward (4.6 TB/s), 107 us backward (3.8 TB/s)
 //   16384 x 4096 fp32  89 us (6.0 TB/s), 155 us (5.2 TB/s)
 //   65536 x 768 bf16   56 us (3.6 TB/s), 88 us (3.4 TB/s)
 //   32 x 4096 bf16     7.9 us, 13 us (launches and the latency of one row)
@@ -497,24 +497,27 @@ struct SlabShare {
   uint32_t vectors, across;
   int t, g, groups;
 };
-template <int V>
+template <int V, int kThreads = kSlabThreads>
 __device__ __forceinline__ SlabShare slab_share(int32_t cols) {
   SlabShare s;
   s.vectors = (uint32_t)cols / V;
-  s.across = s.vectors < kSlabThreads ? (s.vectors + 31) / 32 * 32 : kSlabThreads;
-  s.groups = kSlabThreads / s.across;
+  s.across = s.vectors < kThreads ? (s.vectors + 31) / 32 * 32 : kThreads;
+  s.groups = kThreads / s.across;
   s.g = threadIdx.x / s.across;
   s.t = threadIdx.x % s.across;
   return s;
 }
 
-template <typename T, int V, int kN>
-__global__ void __launch_bounds__(kSlabThreads, kN * V <= 16 ? 2 : 1)
+// kThreads: half as many, and rows, where a row is long, but not the longest (16384 x 4096 bf16: 58 us against 62,
+// 8192 x 8192: 79 against 93; 65536 x 768: 73 against 56, 4096 x 16384: 113 against 91).
+template <typename T, int V, int kN, int kThreads>
+__global__ void __launch_bounds__(kThreads, kN * V <= 16 ? 2 : 1)
 norm_slab_kernel(const NormArgs a, const Aligned aligned) {
+  constexpr int kRows = kThreads / 32;
   using W = Wide<V>;
   constexpr int H = kWide<V>;
-  __shared__ float2 stat[kSlab];
-  const SlabShare sh = slab_share<V>(a.cols);
+  __shared__ float2 stat[kRows];
+  const SlabShare sh = slab_share<V, kThreads>(a.cols);
   const float over = 1.f / (float)a.cols;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   W w[kN][H], b[kN][H];
@@ -526,7 +529,7 @@ norm_slab_kernel(const NormArgs a, const Aligned aligned) {
       load_weights<V>(a.b == nullptr ? nullptr : a.b + v * V, aligned.b, 0.f, b[i]);
     }
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * kSlab; r0 < a.rows; r0 += (int64_t)gridDim.x * kSlab) {
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
     const int64_t mine = r0 + warp;
     float mean = 0.f, rstd = 0.f;
     if (mine < a.rows) {
@@ -568,11 +571,11 @@ norm_slab_kernel(const NormArgs a, const Aligned aligned) {
       }
     }
     if (slab_ahead<T>(a.cols)) {
-      const int64_t next = mine + (int64_t)gridDim.x * kSlab;
+      const int64_t next = mine + (int64_t)gridDim.x * kRows;
       prefetch_row(static_cast<const T*>(a.x) + next * a.ldx, next < a.rows ? a.cols : 0, lane);
     }
     __syncthreads();
-    const int rows = (int)(a.rows - r0 < kSlab ? a.rows - r0 : kSlab);
+    const int rows = (int)(a.rows - r0 < kRows ? a.rows - r0 : kRows);
     if (sh.g < sh.groups)
 #pragma unroll 4
       for (int q = sh.g; q < rows; q += sh.groups) {
@@ -784,6 +787,7 @@ norm_parts_kernel(const float* __restrict__ part, int parts, int32_t cols, float
 struct RowPlan {
   int v, tpr, n;   // tpr 0: slabs; n 0: too long for registers
   int blocks;      // of the gradient by slabs on an SM
+  bool half;       // slabs of half as many rows and threads (forward pass)
 };
 
 constexpr int kMostInRegisters = 16384;  // columns
@@ -797,7 +801,7 @@ RowPlan plan_row(const NormArgs& a, int dtype, bool grad) {
   const bool wide = a.cols % v == 0 && on_16(a.x) && on_16(a.out) && a.ldx % v == 0 && a.ldo % v == 0 &&
                     (!grad || (on_16(a.dy) && a.lddy % v == 0));
   const int64_t n = wide ? a.cols / v : a.cols;
-  RowPlan p{wide ? v : 1, 0, 0, 1};
+  RowPlan p{wide ? v : 1, 0, 0, 1, false};
   if (n <= 8) p.tpr = 8, p.n = 1;
   else if (n <= 32) p.tpr = 32, p.n = 1;
   else if (n <= 512 && a.rows <= kFewRows) p.tpr = 512, p.n = 1;
@@ -809,11 +813,12 @@ RowPlan plan_row(const NormArgs& a, int dtype, bool grad) {
   else if (n <= 2048) p.tpr = 512, p.n = 4;
   else if (!wide && n <= 8192) p.tpr = 512, p.n = 16;
   if (p.tpr == 0 && p.n == 1 && n <= 128) p.blocks = 2;
+  p.half = p.tpr == 0 && p.n > 0 && wide && !grad && n >= 256 && n <= 1024;
   return p;
 }
 
 int64_t rows_per_block(const RowPlan& p) {
-  return p.n == 0 ? kLongRows : p.tpr == 0 ? kSlab : p.tpr > 32 ? 1 : 256 / p.tpr;
+  return p.n == 0 ? kLongRows : p.tpr == 0 ? (p.half ? kSlab / 2 : kSlab) : p.tpr > 32 ? 1 : 256 / p.tpr;
 }
 
 // The gradient's blocks, each with sums of its own: two or four per SM of 152.
@@ -861,10 +866,15 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t st) {
   }
   // (Blocks that stay ask for their next slab ahead; the others make way for the next block's.)
   const int64_t per = rows_per_block(p), blocks = (a.rows + per - 1) / per,
-                cap = (int64_t)sms * (p.tpr == 0 && slab_ahead<T>(a.cols) ? 2 : 8);
+                cap = (int64_t)sms * (p.tpr == 0 && slab_ahead<T>(a.cols) ? (p.half ? 4 : 2) : p.half ? 16 : 8);
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const auto go = [&](auto V, auto tpr, auto n) {
-    if constexpr (tpr() == 0) norm_slab_kernel<T, V(), n()><<<grid, kSlabThreads, 0, st>>>(a, aligned);
+    if constexpr (tpr() == 0 && V() > 1)
+      if (p.half) {
+        norm_slab_kernel<T, V(), 2 * n(), kSlabThreads / 2><<<grid, kSlabThreads / 2, 0, st>>>(a, aligned);
+        return cudaGetLastError();
+      }
+    if constexpr (tpr() == 0) norm_slab_kernel<T, V(), n(), kSlabThreads><<<grid, kSlabThreads, 0, st>>>(a, aligned);
     else norm_kernel<T, V(), tpr(), n()><<<grid, kBlockThreads<tpr()>, 0, st>>>(a, aligned);
     return cudaGetLastError();
   };
