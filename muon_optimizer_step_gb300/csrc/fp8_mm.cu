@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 // Tiles of y itself: 128 rows of one expert (x, operand A) by up to 256 columns (the weight, operand B).  An
 // accumulator lane is then a row of y and its scale one value of the thread's, where tiles of y^T need one
 // for each column out of shared memory, whose bandwidth the MMAs want for their operands (98304 rows,
-// 1408 -> 2048: 501 us with those, 338 with these).  Adding up the accumulators bounds them: of 0.76 us for a
-// k-block 0.27 are its MMAs (bare, with the waits for them, 0.53).  On pairs of CTAs the same takes 364 us, as
-// a k-block waits for two epilogues.
+// 1408 -> 2048: 501 us with those, 338 with these).  The operands bound them, 48 KB a k-block out of L2 (273 us
+// with nothing read from the accumulators, 12.6 TB/s), and on top of that adding up the accumulators (loads of
+// them alone 313, multiply-adds alone 319); the MMAs themselves would take 150.  On pairs of CTAs, which load a
+// third less, the same takes 364 us, as a k-block waits for two epilogues.
 constexpr int kRowStage = 2048;  // bytes of each epilogue warp: 64 bytes of its 32 rows
 constexpr int kGroup = 8;        // k-blocks whose scales come together
 constexpr int kGroups = 3;
