@@ -614,15 +614,19 @@ __device__ __forceinline__ void plane_weights(const float4* planes, uint32_t vec
   }
 }
 
-// kBlocks: on an SM at a time.
-template <typename T, int V, int kN, bool kSums, int kBlocks>
-__global__ void __launch_bounds__(kSlabThreads, kBlocks)
+// kBlocks: on an SM at a time.  kThreads: half as many, and rows, two blocks of them, where a row has up to as many
+// vectors (24570 x 2048 bf16: 70 us against 75, 1024 x 2048: 13 against 17).  Of longer rows few or very many would
+// gain by it (32768 x 4096 bf16: 184 us against 191), those between lose by the second block's sums (4096 x 4096:
+// 44 against 41).
+template <typename T, int V, int kN, bool kSums, int kBlocks, int kThreads = kSlabThreads>
+__global__ void __launch_bounds__(kThreads, kBlocks)
 norm_grad_slab_kernel(const NormArgs a, const Aligned aligned) {
+  constexpr int kRows = kThreads / 32;
   using W = Wide<V>;
   constexpr int H = kWide<V>;
   extern __shared__ float4 planes[];
-  __shared__ float4 stat[kSlab];  // mean, rstd, and what dx takes of the row's sums
-  const SlabShare sh = slab_share<V>(a.cols);
+  __shared__ float4 stat[kRows];  // mean, rstd, and what dx takes of the row's sums
+  const SlabShare sh = slab_share<V, kThreads>(a.cols);
   const float over = 1.f / (float)a.cols;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   W dw[kN][H], db[kN][H];
@@ -630,7 +634,7 @@ norm_grad_slab_kernel(const NormArgs a, const Aligned aligned) {
   for (int i = 0; i < kN; ++i)
 #pragma unroll
     for (int k = 0; k < H; ++k) dw[i][k] = db[i][k] = both<W>(0.f);
-  for (uint32_t v = threadIdx.x; v < sh.vectors; v += kSlabThreads) {
+  for (uint32_t v = threadIdx.x; v < sh.vectors; v += kThreads) {
     W w[H];
     load_weights<V>(a.w == nullptr ? nullptr : a.w + v * V, aligned.w, 1.f, w);
     if constexpr (V == 1) {
@@ -643,7 +647,7 @@ norm_grad_slab_kernel(const NormArgs a, const Aligned aligned) {
     }
   }
   __syncthreads();
-  for (int64_t r0 = (int64_t)blockIdx.x * kSlab; r0 < a.rows; r0 += (int64_t)gridDim.x * kSlab) {
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
     const int64_t mine = r0 + warp;
     if (mine < a.rows) {
       const T* x = static_cast<const T*>(a.x) + mine * a.ldx;
@@ -676,12 +680,12 @@ norm_grad_slab_kernel(const NormArgs a, const Aligned aligned) {
       if (lane == 0) stat[warp] = make_float4(mean, rstd, -rstd * m1, -rstd * m2);
     }
     if (slab_ahead<T>(a.cols)) {
-      const int64_t next = mine + (int64_t)gridDim.x * kSlab;
+      const int64_t next = mine + (int64_t)gridDim.x * kRows;
       prefetch_row(static_cast<const T*>(a.x) + next * a.ldx, next < a.rows ? a.cols : 0, lane);
       prefetch_row(static_cast<const T*>(a.dy) + next * a.lddy, next < a.rows ? a.cols : 0, lane);
     }
     __syncthreads();
-    const int rows = (int)(a.rows - r0 < kSlab ? a.rows - r0 : kSlab);
+    const int rows = (int)(a.rows - r0 < kRows ? a.rows - r0 : kRows);
     if (sh.g < sh.groups)
 #pragma unroll 2
       for (int q = sh.g; q < rows; q += sh.groups) {
@@ -787,7 +791,7 @@ norm_parts_kernel(const float* __restrict__ part, int parts, int32_t cols, float
 struct RowPlan {
   int v, tpr, n;   // tpr 0: slabs; n 0: too long for registers
   int blocks;      // of the gradient by slabs on an SM
-  bool half;       // slabs of half as many rows and threads (forward pass)
+  bool half;       // slabs of half as many rows and threads
 };
 
 constexpr int kMostInRegisters = 16384;  // columns
@@ -813,7 +817,7 @@ RowPlan plan_row(const NormArgs& a, int dtype, bool grad) {
   else if (n <= 2048) p.tpr = 512, p.n = 4;
   else if (!wide && n <= 8192) p.tpr = 512, p.n = 16;
   if (p.tpr == 0 && p.n == 1 && n <= 128) p.blocks = 2;
-  p.half = p.tpr == 0 && p.n > 0 && wide && !grad && n >= 256 && n <= 1024;
+  p.half = p.tpr == 0 && p.n > 0 && wide && (grad ? n > 128 && n <= kSlabThreads / 2 : n >= 256 && n <= 1024);
   return p;
 }
 
@@ -824,7 +828,7 @@ int64_t rows_per_block(const RowPlan& p) {
 // The gradient's blocks, each with sums of its own: two or four per SM of 152.
 int64_t grad_blocks(const RowPlan& p, int64_t rows) {
   const int64_t per = rows_per_block(p),
-                most = p.n == 0 ? 304 : p.tpr == 0 ? 152 * p.blocks : p.tpr <= 128 ? 608 : 304;
+                most = p.n == 0 ? 304 : p.tpr == 0 ? 152 * (p.half ? 2 : p.blocks) : p.tpr <= 128 ? 608 : 304;
   const int64_t blocks = (rows + per - 1) / per;
   return blocks < most ? blocks : most;
 }
@@ -869,7 +873,7 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t st) {
                 cap = (int64_t)sms * (p.tpr == 0 && slab_ahead<T>(a.cols) ? (p.half ? 4 : 2) : p.half ? 16 : 8);
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const auto go = [&](auto V, auto tpr, auto n) {
-    if constexpr (tpr() == 0 && V() > 1)
+    if constexpr (tpr() == 0 && V() > 1 && n() <= 2)
       if (p.half) {
         norm_slab_kernel<T, V(), 2 * n(), kSlabThreads / 2><<<grid, kSlabThreads / 2, 0, st>>>(a, aligned);
         return cudaGetLastError();
@@ -902,12 +906,16 @@ cudaError_t launch_norm_grad(const NormArgs& a, int sms, cudaStream_t st) {
         if constexpr (n() == 1)
           if (p.blocks == 2)
             kernel = sums ? norm_grad_slab_kernel<T, V(), n(), true, 2> : norm_grad_slab_kernel<T, V(), n(), false, 2>;
+        if constexpr (V() > 1 && n() == 1)
+          if (p.half)
+            kernel = sums ? norm_grad_slab_kernel<T, V(), 1, true, 2, kSlabThreads / 2>
+                          : norm_grad_slab_kernel<T, V(), 1, false, 2, kSlabThreads / 2>;
         const size_t smem = ((size_t)a.cols * 4 + 15) / 16 * 16;
         if (smem > 48 * 1024) {
           const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
           if (s != cudaSuccess) return s;
         }
-        kernel<<<(unsigned)parts, kSlabThreads, smem, st>>>(a, aligned);
+        kernel<<<(unsigned)parts, p.half ? kSlabThreads / 2 : kSlabThreads, smem, st>>>(a, aligned);
       } else {
         (sums ? norm_grad_kernel<T, V(), tpr(), n(), true> : norm_grad_kernel<T, V(), tpr(), n(), false>)
             <<<(unsigned)parts, kBlockThreads<tpr()>, 0, st>>>(a, aligned);

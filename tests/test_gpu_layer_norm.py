@@ -214,6 +214,15 @@ def test_grad_many_rows(capi, rows, cols, dtype):
     _check_grad(capi, rows, cols, dtype, accumulate=True)
 
 
+@pytest.mark.parametrize("cols", [1024, 1032, 1536, 2040, 2048, 2056, 4096, 4104, 8192, 8200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_where_slabs_change(capi, cols, dtype):
+    """The lengths of a row on both sides of each change in the rows and threads of a block."""
+    for rows in (305, 1003):
+        _check_forward(capi, *_inputs(_gen(cols), rows, cols, dtype))
+        _check_grad(capi, rows, cols, dtype, accumulate=rows == 305)
+
+
 @pytest.mark.parametrize("place", [(8, 0, 16, 8), (3, 1, 0, 0), (0, 0, 1, 5), (8, 8, 8, 1)])
 def test_grad_strides(capi, place):
     for cols in (40, 768, 4096):
