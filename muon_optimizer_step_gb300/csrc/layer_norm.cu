@@ -911,7 +911,8 @@ cudaError_t launch_norm_grad(const NormArgs& a, int sms, cudaStream_t st) {
             kernel = sums ? norm_grad_slab_kernel<T, V(), 1, true, 2, kSlabThreads / 2>
                           : norm_grad_slab_kernel<T, V(), 1, false, 2, kSlabThreads / 2>;
         const size_t smem = ((size_t)a.cols * 4 + 15) / 16 * 16;
-        if (smem > 48 * 1024) {
+        // (The rows' statistics, which a kernel has besides, count towards the 48 KB of a launch that asks for nothing.)
+        if (smem + kSlab * sizeof(float4) > 48 * 1024) {
           const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
           if (s != cudaSuccess) return s;
         }
