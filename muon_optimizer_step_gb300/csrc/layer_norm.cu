@@ -21,6 +21,7 @@
 //   16384 x 4096 fp32  89 us (6.0 TB/s), 155 us (5.2 TB/s)
 //   65536 x 768 bf16   56 us (3.6 TB/s), 88 us (3.4 TB/s)
 //   32 x 4096 bf16     7.9 us, 13 us (launches and the latency of one row)
+#include <atomic>
 #include <type_traits>
 
 #include "element.cuh"
@@ -833,6 +834,17 @@ int64_t grad_blocks(const RowPlan& p, int64_t rows) {
   return blocks < most ? blocks : most;
 }
 
+// Allows a kernel's launches so many bytes of dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>* ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || ready->load(std::memory_order_acquire) >> dev & 1) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready->fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
+
 // f(V, kTpr, kN) for the plan, with kTpr 0 for slabs.
 template <typename T, int V, typename F>
 cudaError_t by_shape(const RowPlan& p, const F& f) {
@@ -911,9 +923,13 @@ cudaError_t launch_norm_grad(const NormArgs& a, int sms, cudaStream_t st) {
             kernel = sums ? norm_grad_slab_kernel<T, V(), 1, true, 2, kSlabThreads / 2>
                           : norm_grad_slab_kernel<T, V(), 1, false, 2, kSlabThreads / 2>;
         const size_t smem = ((size_t)a.cols * 4 + 15) / 16 * 16;
-        // (The rows' statistics, which a kernel has besides, count towards the 48 KB of a launch that asks for nothing.)
-        if (smem + kSlab * sizeof(float4) > 48 * 1024) {
-          const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // Only the longest rows' weights, with the rows' statistics, come near the 48 KB that a launch has by
+        // default.  Their kernels are allowed once what any of them may need: a limit that followed each call's
+        // rows would refuse another thread's longer ones between its call and its launch.
+        constexpr int kMostSmem = kMostInRegisters * 4;
+        if constexpr (V() > 1 && n() == 4) {
+          static std::atomic<uint64_t> ready[2];
+          const cudaError_t s = allow_smem(kernel, kMostSmem, &ready[sums]);
           if (s != cudaSuccess) return s;
         }
         kernel<<<(unsigned)parts, p.half ? kSlabThreads / 2 : kSlabThreads, smem, st>>>(a, aligned);
