@@ -362,8 +362,8 @@ norm_grad_kernel(const NormArgs a, const Aligned aligned) {
     }
     s = group_sum<kTpr>(s, red, turn++);
     if (!on) continue;
-    // dx = dy (w rstd) - rstd m1 - (x - mean) rstd^2 m2
-    const W c1 = both<W>(-rstd * (s.x * over)), c2 = both<W>(-rstd * rstd * (s.y * over));
+    // dx = dy (w rstd) - rstd m1 - xh (rstd m2): rstd^2 is beyond fp32 where rows have a tiny spread.
+    const W c1 = both<W>(-rstd * (s.x * over)), c2 = both<W>(-rstd * (s.y * over));
     T* dx = static_cast<T*>(a.out) + r * a.ldo;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -379,8 +379,10 @@ norm_grad_kernel(const NormArgs a, const Aligned aligned) {
       widen<T, V>(xv[i], x);
       widen<T, V>(dv[i], d);
 #pragma unroll
-      for (int k = 0; k < H; ++k)
-        d[k] = fma2(add2(x[k], both<W>(-mean)), c2, fma2(d[k], mul2(w[k], both<W>(rstd)), c1));
+      for (int k = 0; k < H; ++k) {
+        const W xh = mul2(add2(x[k], both<W>(-mean)), both<W>(rstd));
+        d[k] = fma2(xh, c2, fma2(d[k], mul2(w[k], both<W>(rstd)), c1));
+      }
       store_wide<T, V>(dx + c, d);
     }
   }
