@@ -13,6 +13,8 @@
 // k-blocks of one.  Streaming the weight bounds them.  Many: tiles of y, below.
 //
 // Warp 3 brings the scales into a ring of slots in shared memory, several k-blocks ahead (cp.async).
+#include <cstddef>
+
 #include "grouped_kernel.cuh"
 
 namespace muon {
@@ -42,10 +44,12 @@ struct Split8 {
 };
 
 struct Scales {
-  float slot[kSlots][64];
+  alignas(16) float slot[kSlots][64];  // read 16 bytes at a time
   float weight[kSlots][32];  // the weight's scale, a copy for each lane of warp 3
   uint64_t full[kSlots], empty[kSlots];
 };
+
+static_assert(alignof(Scales) >= 16 && offsetof(Scales, slot) % 16 == 0, "add_block reads the slots in 16-byte units");
 
 __device__ __forceinline__ void copy_4(void* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
