@@ -485,10 +485,11 @@ muon_status muon_quantize_weights(const void* w, int64_t ldw, int64_t w_stride, 
                                   int32_t transpose, int32_t dtype, cudaStream_t stream);
 /* muon_grouped_mm_fp8: y[r, :] = x[r, :] W_e^T for the rows r of every expert e (row_offsets NULL:
  * n_experts is 1 and owns every row), x (rows x k) and w (n x k for each expert) in e4m3 with the scales
- * of the two calls above (any finite values will do).  Each block's sum over 128 of k comes from the
- * tensor cores in fp32 and is added, times both scales, in fp32; one rounding to out_dtype (any
- * muon_dtype) at the store.  Rows of no expert get zeros.  x, w and all their rows must start on 16
- * bytes (MUON_ERR_ALIGNMENT otherwise): pitches and w_stride are multiples of 16, whatever k is. */
+ * of the two calls above (any finite values will do, also where the product of two is beyond fp32).  Each
+ * block's sum over 128 of k comes from the tensor cores in fp32 and is added, times both scales, in
+ * fp32; one rounding to out_dtype (any muon_dtype) at the store.  Rows of no expert get zeros.  x, w and
+ * all their rows must start on 16 bytes (MUON_ERR_ALIGNMENT otherwise): pitches and w_stride are
+ * multiples of 16, whatever k is. */
 muon_status muon_grouped_mm_fp8(const void* x, int64_t ldx, const float* x_scale, int64_t ld_x_scale,
                                 const void* w, int64_t ldw, int64_t w_stride, const float* w_scale,
                                 const int64_t* row_offsets, void* y, int64_t ldy, int64_t rows,

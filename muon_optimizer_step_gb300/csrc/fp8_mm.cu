@@ -22,7 +22,8 @@ namespace muon {
 namespace {
 
 constexpr int kBK8 = 128;   // elements of a k-block: 128 bytes
-constexpr int kSlots = 8;   // of scales
+// Slots of scales.  (With 8 the next k-block's waited for the epilogue: 3600 rows, 2048 -> 1408, 50.3 us against 47.3.)
+constexpr int kSlots = 16;
 constexpr int kAhead = 6;   // k-blocks that scales are asked for ahead
 constexpr int kStaging8 = 1024;          // bytes of each epilogue warp: 8 rows of its 32 columns
 
@@ -45,11 +46,31 @@ struct Split8 {
 
 struct Scales {
   alignas(16) float slot[kSlots][64];  // read 16 bytes at a time
+  float first[kSlots][64], again[kSlots][64];  // where `far`, see Factors (the slot then holds zeros)
+  int far[kSlots];
   float weight[kSlots][32];  // the weight's scale, a copy for each lane of warp 3
   uint64_t full[kSlots], empty[kSlots];
 };
 
 static_assert(alignof(Scales) >= 16 && offsetof(Scales, slot) % 16 == 0, "add_block reads the slots in 16-byte units");
+
+// What a block's sum is multiplied by: the product of its two scales, or, where that leaves 2^-100 .. 2^100, the
+// product by 2^-128 (2^128) and twice 2^64 (2^-64).  A sum is 0 or of 2^-18 .. 2^25, so that nothing on the way
+// leaves fp32's normal range unless the result does: a product of 2^128 and more would make NaN of a sum of 0, one
+// below 2^-126 would lose bits.
+struct Factors {
+  float first, again;
+};
+constexpr float kNearOne = 0x1p100f;
+__device__ __forceinline__ bool near_one(float product) {
+  return fabsf(product) >= 1.f / kNearOne && fabsf(product) <= kNearOne;
+}
+__device__ __forceinline__ Factors factors(float x, float w) {
+  const float p = x * w;
+  if (near_one(p) || x == 0.f || w == 0.f) return {p, 1.f};
+  return fabsf(p) > 1.f ? Factors{x * 0x1p-64f * (w * 0x1p-64f), 0x1p64f}
+                        : Factors{x * 0x1p64f * (w * 0x1p64f), 0x1p-64f};
+}
 
 __device__ __forceinline__ void copy_4(void* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -58,15 +79,52 @@ __device__ __forceinline__ void copy_4(void* dst, const float* src) {
 __device__ __forceinline__ float low(f32x2 v) { return parts(v).x; }
 __device__ __forceinline__ float high(f32x2 v) { return parts(v).y; }
 
+__device__ __forceinline__ f32x2 pair_of(const uint32_t* v) {
+  return pair(__uint_as_float(v[0]), __uint_as_float(v[1]));
+}
+
 // sum += 32 accumulator columns in v, times their scales from s on (16-byte aligned).
 __device__ __forceinline__ void add_block(f32x2 (&sum)[16], const uint32_t (&v)[32], const float* s) {
 #pragma unroll
   for (int k = 0; k < 32; k += 4) {
     f32x2 x, y;
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(smem_u32(s + k)));
-    sum[k / 2] = fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), x, sum[k / 2]);
-    sum[k / 2 + 1] = fma2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), y, sum[k / 2 + 1]);
+    sum[k / 2] = fma2(pair_of(v + k), x, sum[k / 2]);
+    sum[k / 2 + 1] = fma2(pair_of(v + k + 2), y, sum[k / 2 + 1]);
   }
+}
+// sum += a lane's 32 accumulator columns from `at` on, times both factors of their scales.  Out of line, the sums in
+// memory: few calls have any.
+static __device__ __noinline__ void add_far_block(f32x2* sum, uint32_t at, const float* first, const float* again) {
+#pragma unroll 1
+  for (int h = 0; h < 32; h += 16) {
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(at + h, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const f32x2 f = pair(first[h + k], first[h + k + 1]), t = pair(again[h + k], again[h + k + 1]);
+      sum[(h + k) / 2] = fma2(mul2(mul2(pair_of(v + k), f), t), t, sum[(h + k) / 2]);
+    }
+  }
+}
+// The factors of two rows of a slot; whether any of the warp's goes beyond the product (then they are stored).
+static __device__ __noinline__ bool far_slot(float* first, float* again, float x0, float x1, float w) {
+  const Factors f0 = factors(x0, w), f1 = factors(x1, w);
+  if (!__any_sync(0xffffffffu, f0.again != 1.f || f1.again != 1.f)) return false;
+  first[0] = f0.first, again[0] = f0.again;
+  first[32] = f1.first, again[32] = f1.again;
+  return true;
+}
+// f(the sums in memory): where sums in registers meet a function that is out of line.
+template <int kN, typename F>
+__device__ __forceinline__ void in_memory(f32x2 (&sum)[kN], const F& f) {
+  f32x2 there[kN];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) there[k] = sum[k];
+  f(there);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) sum[k] = there[k];
 }
 
 template <typename V, typename O>
@@ -84,11 +142,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     prefetch_tmap(&p.w);
     prefetch_tmap(&p.x);
   }
-  if (threadIdx.x == 0)
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&sc.full[s], 1);
-      mbar_init(&sc.empty[s], kEpiWarps);
-    }
+  if (warp == 3 && lane < kSlots) {
+    mbar_init(&sc.full[lane], 1);
+    mbar_init(&sc.empty[lane], kEpiWarps);
+    fence_mbar_init();
+  }
   setup<false>(c, warp);
   load_offsets(g.offsets, g.n_experts, g.rows, off, g.err);
   if (warp == 3) count_tiles(off, g.n_experts, V::kMaxN, lane, first);
@@ -174,9 +232,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     bool ok = true;
     const auto ready = [&](int64_t u) {  // multiplies what this lane has brought, and hands the slot over
       const int s = (int)(u % kSlots);
-      const float w = sc.weight[s][lane];
-#pragma unroll
-      for (int k = 0; k < 64; k += 32) sc.slot[s][k + lane] *= w;
+      const float w = sc.weight[s][lane], x0 = sc.slot[s][lane], x1 = sc.slot[s][32 + lane];
+      float p0 = x0 * w, p1 = x1 * w;
+      bool far = false;
+      if (__any_sync(0xffffffffu, !near_one(p0) || !near_one(p1))) {
+        far = far_slot(sc.first[s] + lane, sc.again[s] + lane, x0, x1, w);
+        p0 = far ? 0.f : p0;
+        p1 = far ? 0.f : p1;
+      }
+      sc.slot[s][lane] = p0;
+      sc.slot[s][32 + lane] = p1;
+      if (lane == 0) sc.far[s] = far;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc.full[s]);
     };
@@ -191,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < 64; k += 32)
           if (k + lane < m.rows) copy_4(&sc.slot[s][k + lane], xs + (int64_t)kb * g.ld_x_scale + k + lane);
+          else sc.slot[s][k + lane] = 1.f;  // (no row: nothing that counts as far)
         copy_4(&sc.weight[s][lane], ws + kb);
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (use >= kAhead) {
@@ -217,10 +284,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
              wait_acc(c, use, g.err);
         if (!ok) break;
         if (32 * group < m.n) {
+          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 32u * group;
+          const int far = sc.far[s];
           uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 32u * group, v);
+          tmem_ld_32x32b_x32(at, v);
           tmem_ld_wait();
           add_block(sum, v, &sc.slot[s][32 * group]);
+          if (__any_sync(0xffffffffu, far))
+            in_memory(sum, [&](f32x2* to) { add_far_block(to, at, &sc.first[s][32 * group], &sc.again[s][32 * group]); });
         }
         release_acc<false>(c, use & 1, 0, lane);
         if (lane == 0) mbar_arrive(&sc.empty[s]);
@@ -277,6 +348,7 @@ struct Rows8 {
 struct RowScales {
   float x[kGroups][kGroup][kBM];
   float w[kGroups][2][kGroup];  // of the tile's two blocks of 128 columns
+  int far[kGroups];  // whether a product of theirs may be far from 1
   uint64_t full[kGroups], empty[kGroups];
 };
 
@@ -313,6 +385,30 @@ __device__ __forceinline__ uint4 pack_16(const f32x2* v) {
     const float2 c = parts(v[2]), d = parts(v[3]);
     return make_uint4(pack_2<O>(a.x, a.y), pack_2<O>(b.x, b.y), pack_2<O>(c.x, c.y), pack_2<O>(d.x, d.y));
   }
+}
+
+// sum += the lane's row of `count` accumulators from use number `use` on, 128 columns from `at` on (in the first of the
+// two), times both factors of their scales.  Out of line, the sums in memory: the ordinary case has no registers for
+// it.  False where a wait gave up.
+static __device__ __noinline__ bool add_far_group(f32x2* sum, Control& c, uint32_t use, int count, uint32_t at, bool on,
+                                                  const float* x, const float* w, int lane, int* err) {
+#pragma unroll 1
+  for (int i = 0; i < count; ++i, ++use) {
+    if (!wait_acc(c, use, err)) return false;
+    const Factors f = factors(x[i * kBM], w[i]);
+    const f32x2 first = pair(f.first, f.first), again = pair(f.again, f.again);
+#pragma unroll 1
+    for (int h = 0; on && h < 128; h += 16) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(at + (use & 1) * kAccCols + h, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; k += 2)
+        sum[(h + k) / 2] = fma2(mul2(mul2(pair_of(v + k), first), again), again, sum[(h + k) / 2]);
+    }
+    release_acc<false>(c, use & 1, 0, lane);
+  }
+  return true;
 }
 
 template <typename O>
@@ -409,8 +505,25 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_rows_kernel(const __grid_cons
     uint32_t use = 0;
     bool ok = true;
     const auto ready = [&](uint32_t u) {
+      // The largest and the smallest magnitudes (but 0) of what this lane has brought, and of all.
+      const uint32_t s = u % kGroups, inf = 0x7f800000u;
+      uint32_t x_most = 0, x_least = inf, w_most = 0, w_least = inf;
+      const auto look = [&](float v, uint32_t& most, uint32_t& least) {
+        const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+        most = max(most, b);
+        least = b == 0 ? least : min(least, b);
+      };
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+        for (int r = 0; r < kBM; r += 32) look(sc.x[s][i][r + lane], x_most, x_least);
+      if (lane < 2 * kGroup) look(sc.w[s][lane / kGroup][lane % kGroup], w_most, w_least);
+      const auto most = [](uint32_t v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, v)); };
+      const auto least = [](uint32_t v) { return __uint_as_float(__reduce_min_sync(0xffffffffu, v)); };
+      const float high = most(x_most) * most(w_most), low = least(x_least) * least(w_least);
+      if (lane == 0) sc.far[s] = !(high <= kNearOne && low >= 1.f / kNearOne);
       __syncwarp();  // every lane's copies have landed
-      if (lane == 0) mbar_arrive(&sc.full[u % kGroups]);
+      if (lane == 0) mbar_arrive(&sc.full[s]);
     };
     const int64_t n_blocks = (g.n - 1) / 128 + 1;
     RowTile m;
@@ -423,13 +536,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_rows_kernel(const __grid_cons
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < kGroup; ++i)
-          if (kb + i < blocks)
 #pragma unroll
-            for (int r = 0; r < kBM; r += 32)
-              if (r + lane < m.rows) copy_4(&sc.x[s][i][r + lane], xs + (int64_t)(kb + i) * g.ld_x_scale + r + lane);
+          for (int r = 0; r < kBM; r += 32) {
+            float* to = &sc.x[s][i][r + lane];
+            if (kb + i < blocks && r + lane < m.rows) copy_4(to, xs + (int64_t)(kb + i) * g.ld_x_scale + r + lane);
+            else *to = 0.f;
+          }
         const int half = lane / kGroup, b = lane % kGroup;
-        if (half < 2 && kb + b < blocks && m.f0 / 128 + half < n_blocks)
-          copy_4(&sc.w[s][half][b], g.w_scale + ((int64_t)m.expert * n_blocks + m.f0 / 128 + half) * blocks + kb + b);
+        if (half < 2) {
+          float* to = &sc.w[s][half][b];
+          if (kb + b < blocks && m.f0 / 128 + half < n_blocks)
+            copy_4(to, g.w_scale + ((int64_t)m.expert * n_blocks + m.f0 / 128 + half) * blocks + kb + b);
+          else *to = 0.f;
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (use > 0) {
           asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -451,32 +570,39 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_rows_kernel(const __grid_cons
       f32x2 sum[64];
 #pragma unroll
       for (int k = 0; k < 64; ++k) sum[k] = 0;
-      for (int kb = 0; kb < blocks; ++kb, ++use) {
-        const int i = kb % kGroup;
+      const uint32_t at0 = tmem + ((uint32_t)(32 * q) << 16) + 128u * half;
+      for (int kb = 0; kb < blocks; kb += kGroup, ++groups) {
         const uint32_t s = groups % kGroups;
-        if (i == 0) ok = wait_warp(&sc.full[s], groups / kGroups & 1u, g.err, &c.abort);
-        ok = ok && wait_acc(c, use, g.err);
+        ok = wait_warp(&sc.full[s], groups / kGroups & 1u, g.err, &c.abort);
         if (!ok) break;
-        if (on) {
-          const float scale = sc.x[s][i][32 * q + lane] * sc.w[s][half][i];
-          const f32x2 both = pair(scale, scale);
-          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (use & 1) * kAccCols + 128u * half;
+        const int count = min(kGroup, blocks - kb);
+        if (__any_sync(0xffffffffu, sc.far[s])) {
+          in_memory(sum, [&](f32x2* to) {
+            ok = add_far_group(to, c, use, count, at0, on, &sc.x[s][0][32 * q + lane], sc.w[s][half], lane, g.err);
+          });
+          use += count;
+        } else {
+          for (int i = 0; i < count; ++i, ++use) {
+            ok = wait_acc(c, use, g.err);
+            if (!ok) break;
+            if (on) {
+              const float scale = sc.x[s][i][32 * q + lane] * sc.w[s][half][i];
+              const f32x2 both = pair(scale, scale);
+              const uint32_t at = at0 + (use & 1) * kAccCols;
 #pragma unroll
-          for (int h = 0; h < 128; h += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(at + h, v);
-            tmem_ld_wait();
+              for (int h = 0; h < 128; h += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(at + h, v);
+                tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; k += 2)
-              sum[(h + k) / 2] =
-                  fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), both, sum[(h + k) / 2]);
+                for (int k = 0; k < 16; k += 2) sum[(h + k) / 2] = fma2(pair_of(v + k), both, sum[(h + k) / 2]);
+              }
+            }
+            release_acc<false>(c, use & 1, 0, lane);
           }
         }
-        release_acc<false>(c, use & 1, 0, lane);
-        if (i == kGroup - 1 || kb == blocks - 1) {
-          if (lane == 0) mbar_arrive(&sc.empty[s]);
-          ++groups;
-        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&sc.empty[s]);
       }
       if (!ok) break;
       if (!on) continue;
