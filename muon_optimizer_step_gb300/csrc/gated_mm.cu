@@ -71,7 +71,7 @@ struct Gated {
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
       const f32x2 x = pair(g[k], g[k + 1]);
-      const float2 a = parts(mul2(mul2(mul2(x, sigmoid2(x)), pair(u[k], u[k + 1])), pair(w, w)));
+      const float2 a = parts(mul2(mul2(mul2(x, sigmoid2<false>(x)), pair(u[k], u[k + 1])), pair(w, w)));
       v[k] = a.x, v[k + 1] = a.y;
     }
   }
@@ -160,7 +160,7 @@ struct Grad {
   // silu'(g) = s + silu(g) (1 - s).
   static __device__ __forceinline__ void values(f32x2 dh, f32x2 g, f32x2 u, f32x2 w, float* dgate, float* dup,
                                                 float* out, f32x2& dp) {
-    const f32x2 s = sigmoid2(g), silu = mul2(g, s);
+    const f32x2 s = sigmoid2<true>(g), silu = mul2(g, s);
     const f32x2 slope = fma2(silu, fma2(s, pair(-1.f, -1.f), pair(1.f, 1.f)), s);
     const f32x2 d = mul2(dh, w), t = mul2(silu, u);
     const float2 a = parts(mul2(d, mul2(u, slope))), b = parts(mul2(d, silu)), c = parts(mul2(t, w));
