@@ -848,7 +848,7 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>* ready) {
 }
 
 // f(V, kTpr, kN) for the plan, with kTpr 0 for slabs.
-template <typename T, int V, typename F>
+template <typename T, int V, bool kGrad, typename F>
 cudaError_t by_shape(const RowPlan& p, const F& f) {
   const auto v = std::integral_constant<int, V>();
   const auto go = [&](auto tpr, auto n) { return f(v, tpr, n); };
@@ -868,7 +868,8 @@ cudaError_t by_shape(const RowPlan& p, const F& f) {
     if (p.n == 1) return go(slab, one);
     if (p.n == 2) return go(slab, std::integral_constant<int, 2>());
     if (p.n == 4) return go(slab, four);
-    if constexpr (V == 1) return p.tpr == 512 ? go(std::integral_constant<int, 512>(), many) : go(slab, many);
+    if constexpr (V == 1 && kGrad) return go(std::integral_constant<int, 512>(), many);
+    if constexpr (V == 1 && !kGrad) return go(slab, many);
   }
   return cudaErrorInvalidValue;
 }
@@ -892,11 +893,12 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t st) {
         norm_slab_kernel<T, V(), 2 * n(), kSlabThreads / 2><<<grid, kSlabThreads / 2, 0, st>>>(a, aligned);
         return cudaGetLastError();
       }
-    if constexpr (tpr() == 0) norm_slab_kernel<T, V(), n(), kSlabThreads><<<grid, kSlabThreads, 0, st>>>(a, aligned);
+    if constexpr (tpr() == 0 && V() > 1 && n() == 2) return cudaErrorInvalidValue;  // (these are all half)
+    else if constexpr (tpr() == 0) norm_slab_kernel<T, V(), n(), kSlabThreads><<<grid, kSlabThreads, 0, st>>>(a, aligned);
     else norm_kernel<T, V(), tpr(), n()><<<grid, kBlockThreads<tpr()>, 0, st>>>(a, aligned);
     return cudaGetLastError();
   };
-  return p.v == 1 ? by_shape<T, 1>(p, go) : by_shape<T, v>(p, go);
+  return p.v == 1 ? by_shape<T, 1, false>(p, go) : by_shape<T, v, false>(p, go);
 }
 
 template <typename T>
@@ -941,7 +943,7 @@ cudaError_t launch_norm_grad(const NormArgs& a, int sms, cudaStream_t st) {
       }
       return cudaGetLastError();
     };
-    e = p.v == 1 ? by_shape<T, 1>(p, go) : by_shape<T, v>(p, go);
+    e = p.v == 1 ? by_shape<T, 1, true>(p, go) : by_shape<T, v, true>(p, go);
   }
   if (e != cudaSuccess || !sums) return e;
   const int64_t tiles = (2 * (int64_t)a.cols + 31) / 32, cap = (int64_t)sms * 16;
