@@ -12,7 +12,8 @@
 // columns of y (the weight, operand A) by up to 64 rows of one expert, or a cluster of CTAs that share the
 // k-blocks of one.  Streaming the weight bounds them.  Many: tiles of y, below.
 //
-// Warp 3 brings the scales into a ring of slots in shared memory, several k-blocks ahead (cp.async).
+// Warp 3 brings the scales into a ring of slots in shared memory, several k-blocks ahead (cp.async).  It also looks
+// for scales whose product is so far from 1 that it takes more than one factor (see Factors).
 #include <cstddef>
 
 #include "grouped_kernel.cuh"
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 // Tiles of y itself: 128 rows of one expert (x, operand A) by up to 256 columns (the weight, operand B).  An
 // accumulator lane is then a row of y and its scale one value of the thread's, where tiles of y^T need one
 // for each column out of shared memory, whose bandwidth the MMAs want for their operands (98304 rows,
-// 1408 -> 2048: 501 us with those, 338 with these).  The operands bound them, 48 KB a k-block out of L2 (273 us
+// 1408 -> 2048: 501 us with those, 335 with these).  The operands bound them, 48 KB a k-block out of L2 (273 us
 // with nothing read from the accumulators, 12.6 TB/s), and on top of that adding up the accumulators (loads of
 // them alone 313, multiply-adds alone 319); the MMAs themselves would take 150.  On pairs of CTAs, which load a
 // third less, the same takes 364 us, as a k-block waits for two epilogues.

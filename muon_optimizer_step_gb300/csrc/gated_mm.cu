@@ -11,17 +11,19 @@
 // brings as many bytes into an SM as a plain product's of the same work.  The epilogue warp that holds 32
 // columns of g and the one that holds them of u put 16 rows at a time into shared memory; each then takes
 // g and u of 8 of them.  g and u go to memory only where the caller keeps them.  Bound by the tensor cores:
-//   4096 rows, 4096 -> 14336, both kept   520 us  1.85 PFLOP/s
+//   4096 rows, 4096 -> 14336, both kept   541-575 us  1.67-1.78 PFLOP/s (power)
 //   192 rows, 2048 -> 1408, 64 experts    105 us  6.7 TB/s (the weights, HBM)
+// (Passes in a graph, here and below.)
 //
 // grad: dh stays in the accumulators.  The epilogue reads g and u of its tile and writes three results.  dp_r is
 // summed over 32 columns in a warp; a second kernel adds those sums in order, so equal inputs give equal bits.
 // The epilogue bounds it: its loads, exponentials and stores of a 256 x 256 tile take 18000 cycles, in which
-// the MMAs, 16400, get one accumulator ahead (98304 rows, 2048 -> 1408: 633 us, 0.90 PFLOP/s and 2.9 TB/s; without
-// dp 552, a plain product 349).  Tiles of half as many rows with four accumulators took 677 us (an MMA warp
-// needs 450 cycles to issue a k-block), single CTAs 639, eight warps of the epilogue 755.
+// the MMAs, 16400, get one accumulator ahead (98304 rows, 2048 -> 1408: 638 us, 0.89 PFLOP/s and 2.8 TB/s, of which
+// the fine sigmoid is 9; without dp 555-585; the plain product, muon_swiglu_grad and the activation again 713).  With
+// the plain sigmoid it took 633, tiles of half as many rows with four accumulators 677 (an MMA warp needs 450 cycles
+// to issue a k-block), single CTAs 639, eight warps of the epilogue 755.
 //
-// sum: the k-blocks of the second product follow those of the first (24570 rows, 1408 -> 2048: 206 us, 1.38
+// sum: the k-blocks of the second product follow those of the first (24570 rows, 1408 -> 2048: 208 us, 1.36
 // PFLOP/s).
 #include "activation.cuh"
 #include "grouped_kernel.cuh"

@@ -16,11 +16,12 @@
 // of 16-bit values go by slabs (below).  Rows too long for registers are read again for each sum, and their
 // columns summed by blocks of columns in a pass of their own.
 //
-// Bound by HBM where the arithmetic, two values to an instruction, and the sums' latency leave room:
-//   16384 x 4096 bf16  58 us forward (4.6 TB/s), 107 us backward (3.8 TB/s)
-//   16384 x 4096 fp32  89 us (6.0 TB/s), 155 us (5.2 TB/s)
-//   65536 x 768 bf16   56 us (3.6 TB/s), 88 us (3.4 TB/s)
-//   32 x 4096 bf16     7.9 us, 13 us (launches and the latency of one row)
+// Bound by HBM as far as the arithmetic, two values to an instruction, and the sums' latency leave room:
+//   16384 x 4096 bf16  57 us forward (4.7 TB/s), 102 us backward (3.9 TB/s)
+//   16384 x 4096 fp32  88 us (6.1 TB/s), 151 us (5.3 TB/s)
+//   65536 x 768 bf16   54 us (3.7 TB/s), 88 us (3.4 TB/s)
+//   32 x 4096 bf16     2.9 us, 9 us (launches and the latency of one row)
+// (Passes in a graph; a slab's two parts wait for each other, which is what keeps the 16-bit rows from HBM's rate.)
 #include <atomic>
 #include <type_traits>
 
